@@ -24,6 +24,11 @@ __all__ = [
     "mxfp4_repack",
     "mxfp4_dequant",
     "mxfp4_tile",
+    "mxfp4_quantize",
+    "mxfp4_unpack",
+    "mxfp4_matmul",
+    "mxfp4_linear",
+    "mxfp4_linear_workspace_size",
     "moe_mxfp4_ffn_workspace_size",
     "moe_mxfp4_ffn",
     "moe_mxfp4_ffn_noalloc",
@@ -48,7 +53,7 @@ __all__ = [
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libk3moe.so")
 ACT_SILU_MUL = 0
-DTYPE_F32, DTYPE_BF16 = 0, 1
+DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 MAX_TOPK = 64
 MAX_EXPERTS_FFN = 8192
 
@@ -109,6 +114,16 @@ lib.moe_latent_block.restype = ctypes.c_int
 lib.moe_latent_block.argtypes = _block_args
 lib.moe_latent_block_profiled.restype = ctypes.c_int
 lib.moe_latent_block_profiled.argtypes = _block_args + [ctypes.POINTER(ctypes.c_void_p)]
+lib.mxfp4_quantize.restype = ctypes.c_int
+lib.mxfp4_quantize.argtypes = [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp]
+lib.mxfp4_unpack.restype = ctypes.c_int
+lib.mxfp4_unpack.argtypes = [_vp, _vp, _i64, _i64, _i32, _vp, _vp]
+lib.mxfp4_matmul.restype = ctypes.c_int
+lib.mxfp4_matmul.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]
+lib.mxfp4_linear_workspace_size.restype = _sz
+lib.mxfp4_linear_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.mxfp4_linear.restype = ctypes.c_int
+lib.mxfp4_linear.argtypes = [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _sz, _vp]
 BLOCK_STAGE_EVENTS = 7
 # launches between consecutive events of moe_latent_block_profiled
 BLOCK_STAGES = ("dense1", "mid", "route", "ffn", "dense2", "sum")
@@ -137,10 +152,9 @@ def _ptr(t: torch.Tensor | None) -> int | None:
 
 
 def _dev(t: torch.Tensor, name: str, dtype: torch.dtype | tuple) -> None:
-    dts = dtype if isinstance(dtype, tuple) else (dtype,)
-    if t.dtype not in dts:
-        raise TypeError(f"{name}: expected dtype {dts}, got {t.dtype}")
-    if t.device.type != "cuda":
+    if t.dtype is not dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise TypeError(f"{name}: expected dtype {dtype}, got {t.dtype}")
+    if not t.is_cuda:
         raise ValueError(f"{name}: must be a device tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
@@ -148,6 +162,23 @@ def _dev(t: torch.Tensor, name: str, dtype: torch.dtype | tuple) -> None:
 
 def _stream(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _launch(fn: str, device: torch.device, *args) -> None:
+    """Calls entry point `fn` with `args` and the current stream of `device`,
+    which is made the current device for the call where it is not."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        status = getattr(lib, fn)(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            status = getattr(lib, fn)(*args, _raw_stream(index))
+    if status != 0:
+        raise K3MoeError(fn, status)
+
+
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
 
 
 def moe_route_topk(logits: torch.Tensor, bias: torch.Tensor | None, k: int, normalize: bool = True,
@@ -234,6 +265,133 @@ def mxfp4_dequant(blocks: torch.Tensor, out_dtype: torch.dtype = torch.float32,
     if out.numel() != R * K:
         raise ValueError("out has the wrong size")
     _check("mxfp4_dequant", lib.mxfp4_dequant(_ptr(blocks), R, K, code, _ptr(out), _stream(blocks.device)))
+    return out
+
+
+_FLOAT_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+
+
+def _out_code(out_dtype: torch.dtype) -> int:
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    return _FLOAT_CODES[out_dtype]
+
+
+def _mx_pair(packed: torch.Tensor, scale: torch.Tensor, name: str, dims: int | None = None) -> int:
+    """Checks a microscaled pair; returns K."""
+    _dev(packed, name, torch.uint8)
+    _dev(scale, name, torch.uint8)
+    ps, ss = packed.shape, scale.shape
+    if not ps or (dims is not None and len(ps) != dims):
+        raise ValueError(f"{name}: packed must have {dims or 'at least 1'} dimensions")
+    K = ps[-1] * 2
+    if ss[:-1] != ps[:-1] or ss[-1] * 32 != K:
+        raise ValueError(f"{name}: scale must be [..., R, K/32] for packed [..., R, K/2]")
+    if scale.get_device() != packed.get_device():
+        raise ValueError(f"{name}: packed and scale are on different devices")
+    return K
+
+
+def _same_device(ref: torch.Tensor, **others) -> None:
+    index = ref.get_device()
+    for n, t in others.items():
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{n}: must be on {ref.device}")
+
+
+def mxfp4_quantize(x: torch.Tensor, saturate: bool = True, packed: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None):
+    """Float rows [..., R, K] (f32, bf16 or f16; K a multiple of 32) to
+    microscaled 4 bits: (packed u8 [..., R, K/2], scale u8 [..., R, K/32]), the
+    layout mxfp4_repack, mxfp4_matmul and mxfp4_linear read. saturate=False
+    takes the next larger scale where a block's largest element would be
+    clamped."""
+    _dev(x, "x", tuple(_FLOAT_CODES))
+    if x.dim() < 1:
+        raise ValueError("x must be [..., K]")
+    K = x.shape[-1]
+    if K % 32:
+        raise ValueError("K must be a multiple of 32")
+    lead = x.shape[:-1]
+    if packed is None:
+        packed = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
+    if _mx_pair(packed, scale, "output") != K or packed.shape[:-1] != lead:
+        raise ValueError("packed must be [..., R, K/2] for x [..., R, K]")
+    _same_device(x, packed=packed)
+    R = x.numel() // K if K else 0
+    _launch("mxfp4_quantize", x.device, x.data_ptr(), _FLOAT_CODES[x.dtype], R, K, int(bool(saturate)), packed.data_ptr(),
+            scale.data_ptr())
+    return packed, scale
+
+
+def mxfp4_unpack(packed: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype = torch.float32,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """Values [..., R, K] (f32 or bf16) of a microscaled pair (packed u8
+    [..., R, K/2], scale u8 [..., R, K/32]); NaN where the scale byte is 255."""
+    K = _mx_pair(packed, scale, "input")
+    code = _out_code(out_dtype)
+    if out is None:
+        out = torch.empty((*packed.shape[:-1], K), dtype=out_dtype, device=packed.device)
+    _dev(out, "out", out_dtype)
+    if out.numel() != packed.numel() * 2:
+        raise ValueError("out has the wrong size")
+    _same_device(packed, out=out)
+    R = packed.numel() * 2 // K if K else 0
+    _launch("mxfp4_unpack", packed.device, packed.data_ptr(), scale.data_ptr(), R, K, code, out.data_ptr())
+    return out
+
+
+def mxfp4_matmul(a_packed: torch.Tensor, a_scale: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
+                 out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Product of two microscaled matrices, A [M, K] times W [N, K] transposed:
+    out [M, N] f32 or bf16, summed in fp32."""
+    K = _mx_pair(a_packed, a_scale, "A", 2)
+    if _mx_pair(w_packed, w_scale, "W", 2) != K:
+        raise ValueError("A and W have different K")
+    M, N = a_packed.shape[0], w_packed.shape[0]
+    code = _out_code(out_dtype)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a_packed.device)
+    _dev(out, "out", out_dtype)
+    if out.shape != (M, N):
+        raise ValueError("out must be [M, N]")
+    _same_device(a_packed, W=w_packed, out=out)
+    _launch("mxfp4_matmul", a_packed.device, a_packed.data_ptr(), a_scale.data_ptr(), w_packed.data_ptr(), w_scale.data_ptr(),
+            M, N, K, code, out.data_ptr())
+    return out
+
+
+def mxfp4_linear_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib.mxfp4_linear_workspace_size(M, N, K))
+
+
+def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor, saturate: bool = True,
+                 out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows x [M, K] (f32, bf16 or f16), quantised as mxfp4_quantize does, times
+    a microscaled weight matrix W [N, K]: out [M, N] f32 or bf16. The same bits
+    as mxfp4_quantize and mxfp4_matmul in turn."""
+    _dev(x, "x", tuple(_FLOAT_CODES))
+    K = _mx_pair(w_packed, w_scale, "W", 2)
+    if x.dim() != 2 or x.shape[1] != K:
+        raise ValueError("x must be [M, K]")
+    M, N = x.shape[0], w_packed.shape[0]
+    code = _out_code(out_dtype)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
+    _dev(out, "out", out_dtype)
+    if out.shape != (M, N):
+        raise ValueError("out must be [M, N]")
+    need = mxfp4_linear_workspace_size(M, N, K)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    if workspace is not None:
+        _dev(workspace, "workspace", torch.uint8)
+    _same_device(x, W=w_packed, out=out, workspace=workspace)
+    _launch("mxfp4_linear", x.device, x.data_ptr(), _FLOAT_CODES[x.dtype], w_packed.data_ptr(), w_scale.data_ptr(), M, N, K,
+            int(bool(saturate)), code, out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
     return out
 
 

@@ -2,6 +2,7 @@
 // Every check runs before anything is enqueued; nothing here aborts.
 #include "k3moe.h"
 #include "k3moe_internal.h"
+#include "k3moe_ops.h"
 
 #include <math.h>
 #include <sys/syscall.h>
@@ -181,6 +182,16 @@ int ffn_shape_status(int64_t T, int32_t D, int32_t I, int32_t E, int32_t k) {
   // grouped rows are int32 inside the kernels
   if (T * (int64_t)k > 0x7FFFFFFF || T > 0x7FFFFFFF) return K3MOE_ERR_SHAPE;
   return K3MOE_OK;
+}
+
+// Rows of microscaled values: R rows of K elements.
+bool mx_rows_ok(int64_t R, int64_t K) {
+  return R >= 0 && K > 0 && K <= K3MOE_MAX_K_MX && (K % 32) == 0 && R < ((int64_t)1 << 46) / K;
+}
+bool mx_float_type(int32_t t) { return t == K3MOE_DTYPE_F32 || t == K3MOE_DTYPE_BF16 || t == K3MOE_DTYPE_F16; }
+bool mx_product_ok(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || M > 0x7FFFFFFF || N > 0x7FFFFFFF || K <= 0 || K > K3MOE_MAX_K_MX || (K % 32) != 0) return false;
+  return ((M + 63) / 64) * ((N + 63) / 64) <= 0x7FFFFFFF;
 }
 
 // Events recorded at the launch boundaries (moe_mxfp4_ffn_profiled).
@@ -544,6 +555,70 @@ int mxfp4_dequant(const uint8_t* blocks, int64_t R, int64_t K, int32_t out_dtype
   if (misaligned(blocks) || misaligned(out)) return K3MOE_ERR_ALIGN;
   return device_status(launch_dequant(blocks, nblocks, out_dtype == K3MOE_DTYPE_BF16, out,
                                       static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_quantize(const void* x, int32_t x_dtype, int64_t R, int64_t K, int32_t saturate, uint8_t* packed,
+                   uint8_t* scale, void* stream) {
+  if (!mx_rows_ok(R, K)) return K3MOE_ERR_SHAPE;
+  if (!mx_float_type(x_dtype)) return K3MOE_ERR_UNSUPPORTED;
+  if (R == 0) return K3MOE_OK;
+  if (!x || !packed || !scale) return K3MOE_ERR_NULL;
+  if (misaligned(x) || misaligned(packed) || misaligned(scale)) return K3MOE_ERR_ALIGN;
+  return device_status(launch_quantize(x, x_dtype, R * K, saturate, packed, scale, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_unpack(const uint8_t* packed, const uint8_t* scale, int64_t R, int64_t K, int32_t out_dtype, void* out,
+                 void* stream) {
+  if (!mx_rows_ok(R, K)) return K3MOE_ERR_SHAPE;
+  if (out_dtype != K3MOE_DTYPE_F32 && out_dtype != K3MOE_DTYPE_BF16) return K3MOE_ERR_UNSUPPORTED;
+  if (R == 0) return K3MOE_OK;
+  if (!packed || !scale || !out) return K3MOE_ERR_NULL;
+  if (misaligned(packed) || misaligned(scale) || misaligned(out)) return K3MOE_ERR_ALIGN;
+  return device_status(launch_unpack(packed, scale, R * K, out_dtype == K3MOE_DTYPE_BF16, out,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+int mxfp4_matmul(const uint8_t* a_packed, const uint8_t* a_scale, const uint8_t* w_packed, const uint8_t* w_scale,
+                 int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* out, void* stream) {
+  if (!mx_product_ok(M, N, K)) return K3MOE_ERR_SHAPE;
+  if (out_dtype != K3MOE_DTYPE_F32 && out_dtype != K3MOE_DTYPE_BF16) return K3MOE_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return K3MOE_OK;
+  if (!a_packed || !a_scale || !w_packed || !w_scale || !out) return K3MOE_ERR_NULL;
+  if (misaligned(a_packed) || misaligned(a_scale) || misaligned(w_packed) || misaligned(w_scale) || misaligned(out))
+    return K3MOE_ERR_ALIGN;
+  const bool bf16 = out_dtype == K3MOE_DTYPE_BF16;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (mx_few_supported(M, (int)(K / 32)))
+    return device_status(launch_mx_few(a_packed, -1, a_scale, w_packed, w_scale, M, (int)N, (int)K, 0, bf16, out, s));
+  return device_status(launch_mx_tiles(a_packed, a_scale, w_packed, w_scale, M, (int)N, (int)K, bf16, out, s));
+}
+
+size_t mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
+  if (!mx_product_ok(M, N, K) || M == 0 || N == 0 || mx_few_supported(M, (int)(K / 32))) return 0;
+  return align_up((size_t)M * (K / 2), 256) + align_up((size_t)M * (K / 32), 256);
+}
+
+int mxfp4_linear(const void* x, int32_t x_dtype, const uint8_t* w_packed, const uint8_t* w_scale, int64_t M, int64_t N,
+                 int64_t K, int32_t saturate, int32_t out_dtype, void* out, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+  if (!mx_product_ok(M, N, K)) return K3MOE_ERR_SHAPE;
+  if (!mx_float_type(x_dtype) || (out_dtype != K3MOE_DTYPE_F32 && out_dtype != K3MOE_DTYPE_BF16))
+    return K3MOE_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return K3MOE_OK;
+  const size_t need = mxfp4_linear_workspace_size(M, N, K);
+  if (!x || !w_packed || !w_scale || !out || (need && !workspace)) return K3MOE_ERR_NULL;
+  if (misaligned(x) || misaligned(w_packed) || misaligned(w_scale) || misaligned(out) || (need && misaligned(workspace)))
+    return K3MOE_ERR_ALIGN;
+  if (workspace_bytes < need) return K3MOE_ERR_WORKSPACE;
+  const bool bf16 = out_dtype == K3MOE_DTYPE_BF16;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!need)
+    return device_status(launch_mx_few(x, x_dtype, nullptr, w_packed, w_scale, M, (int)N, (int)K, saturate, bf16, out, s));
+  uint8_t* const ap = static_cast<uint8_t*>(workspace);
+  uint8_t* const as = ap + align_up((size_t)M * (K / 2), 256);
+  const hipError_t e = launch_quantize(x, x_dtype, M * K, saturate, ap, as, s);
+  if (e != hipSuccess) return K3MOE_ERR_DEVICE;
+  return device_status(launch_mx_tiles(ap, as, w_packed, w_scale, M, (int)N, (int)K, bf16, out, s));
 }
 
 size_t moe_mxfp4_ffn_workspace_size(int64_t T, int32_t D, int32_t I, int32_t E, int32_t k) {

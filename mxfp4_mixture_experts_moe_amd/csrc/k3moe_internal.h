@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include "k3moe.h"
+#include "k3moe_ops.h"
 #include <stddef.h>
 #include <stdint.h>
 
@@ -63,6 +64,20 @@ hipError_t launch_repack(const uint8_t* packed, const uint8_t* scale, int64_t nb
                          hipStream_t s);
 hipError_t launch_dequant(const uint8_t* blocks, int64_t nblocks, int out_bf16, void* out, hipStream_t s);
 hipError_t launch_tile(const uint8_t* src, int64_t nmat, int N, int nb, uint8_t* dst, hipStream_t s);
+
+// Microscaled 4-bit quantisation and decode of n elements (n a multiple of 32),
+// compressed-tensors layout.
+hipError_t launch_quantize(const void* x, int x_dtype, int64_t n, int saturate, uint8_t* packed, uint8_t* scale,
+                           hipStream_t s);
+hipError_t launch_unpack(const uint8_t* packed, const uint8_t* scale, int64_t n, int out_bf16, void* out,
+                         hipStream_t s);
+// Products of microscaled 4-bit matrices: the few-row kernel (A packed when xs
+// is set, else float rows it quantises itself) and the tile kernels.
+bool mx_few_supported(int64_t M, int nb);
+hipError_t launch_mx_few(const void* x, int x_dtype, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int64_t M,
+                         int N, int K, int saturate, bool out_bf16, void* out, hipStream_t s);
+hipError_t launch_mx_tiles(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t M, int N,
+                           int K, bool out_bf16, void* out, hipStream_t s);
 
 // Stage-tiled order of an MXFP4 matrix of N rows x nb 17-byte blocks (the
 // order mxfp4_tile writes and the FFN kernels read): rows in groups of 16 and
