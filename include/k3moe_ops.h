@@ -89,6 +89,41 @@ int mxfp4_linear(const void* x, int32_t x_dtype, const uint8_t* w_packed, const 
                  int64_t K, int32_t saturate, int32_t out_dtype, void* out, void* workspace, size_t workspace_bytes,
                  void* stream);
 
+/* Most tokens of moe_mxfp4_layer. */
+#define K3MOE_MAX_LAYER_TOKENS 16
+
+/*
+ * moe_mxfp4_layer — the routed layer of a few tokens in two launches: routing
+ * as moe_route_topk, then the experts and their weighted sum as moe_mxfp4_ffn.
+ * Sources: as those two (llama.cpp pull request "model: add Kimi-K3 text
+ * model": expert count, used experts, sigmoid gating, exp_probs_b;
+ * build_moe_ffn: route -> per-expert products -> weighted sum).
+ *
+ *   x_bf16   bf16 [T, D]         latent activations
+ *   logits   f32 [T, E], bias f32 [E] or NULL, normalize, route_scale: routing
+ *   w1, w3   u8 [E, I, D/32, 17], w2 u8 [E, D, I/32, 17]: expert matrices in
+ *            the stage-tiled order of mxfp4_tile, as moe_mxfp4_ffn reads them
+ *   out      f32 [T, D]
+ *   topk_ids i32 [T, k], topk_w f32 [T, k]: optional outputs of the routing
+ *            (NULL: kept in the workspace), the bits of moe_route_topk
+ *   workspace  moe_mxfp4_layer_workspace_size() bytes; contents on entry do
+ *            not matter and are clobbered
+ *
+ * Precision: bf16 x, exact weights, fp32 accumulation; h = SiLU(g) * u in fp32
+ * enters the down product as three bf16 parts (24 significant bits); the k
+ * expert outputs are summed in fp32 in slot order (deterministic, no atomics
+ * on values). moe_mxfp4_ffn rounds h to about 16 bits, so the two agree to
+ * that. More than 1024 experts take a third launch (the router's own).
+ * Sizes: 0 <= T <= K3MOE_MAX_LAYER_TOKENS (T == 0 is a no-op), D, I, E and k
+ * as for moe_mxfp4_ffn. Calls that overlap (two streams, two graphs) need
+ * workspaces of their own.
+ */
+size_t moe_mxfp4_layer_workspace_size(int64_t T, int32_t D, int32_t I, int32_t E, int32_t k);
+int moe_mxfp4_layer(const void* x_bf16, const float* logits, const float* bias, const uint8_t* w1, const uint8_t* w3,
+                    const uint8_t* w2, int64_t T, int32_t D, int32_t I, int32_t E, int32_t k, int32_t normalize,
+                    float route_scale, int32_t act, float* out, int32_t* topk_ids, float* topk_w, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

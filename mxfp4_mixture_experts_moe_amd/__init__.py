@@ -29,6 +29,8 @@ __all__ = [
     "mxfp4_matmul",
     "mxfp4_linear",
     "mxfp4_linear_workspace_size",
+    "moe_mxfp4_layer",
+    "moe_mxfp4_layer_workspace_size",
     "moe_mxfp4_ffn_workspace_size",
     "moe_mxfp4_ffn",
     "moe_mxfp4_ffn_noalloc",
@@ -55,6 +57,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libk3moe.so
 ACT_SILU_MUL = 0
 DTYPE_F32, DTYPE_BF16, DTYPE_F16 = 0, 1, 2
 MAX_TOPK = 64
+MAX_LAYER_TOKENS = 16
 MAX_EXPERTS_FFN = 8192
 
 if not os.path.exists(LIB_PATH):
@@ -122,6 +125,10 @@ lib.mxfp4_matmul.restype = ctypes.c_int
 lib.mxfp4_matmul.argtypes = [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]
 lib.mxfp4_linear_workspace_size.restype = _sz
 lib.mxfp4_linear_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.moe_mxfp4_layer_workspace_size.restype = _sz
+lib.moe_mxfp4_layer_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _i32]
+lib.moe_mxfp4_layer.restype = ctypes.c_int
+lib.moe_mxfp4_layer.argtypes = [_vp] * 6 + [_i64] + [_i32] * 5 + [_f32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
 lib.mxfp4_linear.restype = ctypes.c_int
 lib.mxfp4_linear.argtypes = [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _sz, _vp]
 BLOCK_STAGE_EVENTS = 7
@@ -393,6 +400,57 @@ def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
     _launch("mxfp4_linear", x.device, x.data_ptr(), _FLOAT_CODES[x.dtype], w_packed.data_ptr(), w_scale.data_ptr(), M, N, K,
             int(bool(saturate)), code, out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
     return out
+
+
+def moe_mxfp4_layer_workspace_size(T: int, D: int, I: int, E: int, k: int) -> int:
+    return int(lib.moe_mxfp4_layer_workspace_size(T, D, I, E, k))
+
+
+def moe_mxfp4_layer(x: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor | None, w1: torch.Tensor, w3: torch.Tensor,
+                    w2: torch.Tensor, k: int, normalize: bool = True, route_scale: float = 1.0, act: int = ACT_SILU_MUL,
+                    out: torch.Tensor | None = None, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None):
+    """The routed layer for up to MAX_LAYER_TOKENS tokens in two launches:
+    moe_route_topk(logits, bias, k, normalize, route_scale), then the experts'
+    outputs summed with the gate weights. x bf16 [T, D]; logits f32 [T, E];
+    bias f32 [E] or None; w1/w3 u8 [E, I, D/32, 17] and w2 u8 [E, D, I/32, 17],
+    stage-tiled (mxfp4_tile). Returns (out f32 [T, D], ids int32 [T, k], weights
+    f32 [T, k])."""
+    _dev(x, "x", torch.bfloat16)
+    _dev(logits, "logits", torch.float32)
+    if bias is not None:
+        _dev(bias, "bias", torch.float32)
+    _dev(w1, "w1", torch.uint8)
+    _dev(w3, "w3", torch.uint8)
+    _dev(w2, "w2", torch.uint8)
+    if x.dim() != 2 or logits.dim() != 2 or w1.dim() != 4:
+        raise ValueError("x must be [T, D], logits [T, E], w1 [E, I, D/32, 17]")
+    T, D = x.shape
+    E, I = w1.shape[0], w1.shape[1]
+    if logits.shape != (T, E) or (bias is not None and bias.shape != (E,)):
+        raise ValueError("logits must be [T, E] and bias [E]")
+    if w1.shape != (E, I, D // 32, 17) or w3.shape != w1.shape or w2.shape != (E, D, I // 32, 17):
+        raise ValueError("expert weights have inconsistent shapes")
+    dev = x.device
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.float32, device=dev)
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+    _dev(out, "out", torch.float32)
+    _dev(ids, "ids", torch.int32)
+    _dev(weights, "weights", torch.float32)
+    if out.shape != (T, D) or ids.shape != (T, k) or weights.shape != (T, k):
+        raise ValueError("out must be [T, D], ids and weights [T, k]")
+    if workspace is None:
+        workspace = torch.empty(max(moe_mxfp4_layer_workspace_size(T, D, I, E, k), 1), dtype=torch.uint8, device=dev)
+    _dev(workspace, "workspace", torch.uint8)
+    _same_device(x, logits=logits, bias=bias, w1=w1, w3=w3, w2=w2, out=out, ids=ids, weights=weights, workspace=workspace)
+    _launch("moe_mxfp4_layer", dev, x.data_ptr(), logits.data_ptr(), _ptr(bias), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(), T, D,
+            I, E, k, int(bool(normalize)), float(route_scale), act, out.data_ptr(), ids.data_ptr(), weights.data_ptr(),
+            workspace.data_ptr(), workspace.numel())
+    return out, ids, weights
 
 
 def moe_mxfp4_ffn_workspace_size(T: int, D: int, I: int, E: int, k: int) -> int:

@@ -621,6 +621,46 @@ int mxfp4_linear(const void* x, int32_t x_dtype, const uint8_t* w_packed, const 
   return device_status(launch_mx_tiles(ap, as, w_packed, w_scale, M, (int)N, (int)K, bf16, out, s));
 }
 
+size_t moe_mxfp4_layer_workspace_size(int64_t T, int32_t D, int32_t I, int32_t E, int32_t k) {
+  if (T <= 0 || T > K3MOE_MAX_LAYER_TOKENS || ffn_shape_status(T, D, I, E, k) != K3MOE_OK) return 0;
+  return layer_workspace_bytes(T, D, I, k);
+}
+
+int moe_mxfp4_layer(const void* x_bf16, const float* logits, const float* bias, const uint8_t* w1, const uint8_t* w3,
+                    const uint8_t* w2, int64_t T, int32_t D, int32_t I, int32_t E, int32_t k, int32_t normalize,
+                    float route_scale, int32_t act, float* out, int32_t* topk_ids, float* topk_w, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  const int st = ffn_shape_status(T, D, I, E, k);
+  if (st != K3MOE_OK) return st;
+  if (T > K3MOE_MAX_LAYER_TOKENS) return K3MOE_ERR_SHAPE;
+  if (act != K3MOE_ACT_SILU_MUL) return K3MOE_ERR_UNSUPPORTED;
+  if (T == 0) return K3MOE_OK;
+  if (!x_bf16 || !logits || !w1 || !w3 || !w2 || !out || !workspace) return K3MOE_ERR_NULL;
+  if (misaligned(x_bf16) || misaligned(logits) || misaligned(bias) || misaligned(w1) || misaligned(w3) ||
+      misaligned(w2) || misaligned(out) || misaligned(topk_ids) || misaligned(topk_w) || misaligned(workspace))
+    return K3MOE_ERR_ALIGN;
+  if (workspace_bytes < layer_workspace_bytes(T, D, I, k)) return K3MOE_ERR_WORKSPACE;
+  LayerCall c{};
+  c.x = static_cast<const uint16_t*>(x_bf16);
+  c.logits = logits;
+  c.bias = bias;
+  c.w1 = w1;
+  c.w3 = w3;
+  c.w2 = w2;
+  c.T = (int)T;
+  c.D = D;
+  c.I = I;
+  c.E = E;
+  c.k = k;
+  c.normalize = normalize;
+  c.route_scale = route_scale;
+  c.out = out;
+  c.ids = topk_ids;
+  c.w = topk_w;
+  c.workspace = workspace;
+  return device_status(launch_layer(c, static_cast<hipStream_t>(stream)));
+}
+
 size_t moe_mxfp4_ffn_workspace_size(int64_t T, int32_t D, int32_t I, int32_t E, int32_t k) {
   if (ffn_shape_status(T, D, I, E, k) != K3MOE_OK || T == 0) return 0;
   return ffn_workspace_layout(ffn_chunk_tokens(T, D, I, k), D, I, E, k).total;

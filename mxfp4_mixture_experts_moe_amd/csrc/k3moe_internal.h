@@ -186,6 +186,21 @@ hipError_t launch_combine(const float* y, const int8_t* y_scale, bool mixed, con
                           int64_t T, int D, int k,
                           float* out, hipStream_t s);
 
+// The whole routed layer for a few tokens (plan + one persistent kernel).
+struct LayerCall {
+  const uint16_t* x;
+  const float *logits, *bias;
+  const uint8_t *w1, *w3, *w2;
+  int T, D, I, E, k, normalize;
+  float route_scale;
+  float* out;
+  int32_t* ids;  // null: kept in the workspace
+  float* w;      // null: kept in the workspace
+  void* workspace;
+};
+size_t layer_workspace_bytes(int64_t T, int32_t D, int32_t I, int32_t k);
+hipError_t launch_layer(const LayerCall& c, hipStream_t s);
+
 // Verify batches: distinct[w] = distinct experts routed by the rows of
 // position <= w of S sequences of W rows (W <= kMaxVerifyWidth, E <= 8192).
 constexpr int kMaxVerifyWidth = 64;
