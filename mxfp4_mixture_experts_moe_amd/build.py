@@ -44,8 +44,9 @@ FLAGS = [
 
 
 # per-source additions: the Q4_K GEMM consumes every MFMA result in VALU
-# arithmetic, so its accumulators stay in VGPRs (no AGPR copies)
-EXTRA_FLAGS = {"ffn_q4k.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# arithmetic, so its accumulators stay in VGPRs (no AGPR copies); the few-token
+# layer's change places every stage
+EXTRA_FLAGS = {"ffn_q4k.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "layer.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str) -> str:

@@ -1,20 +1,31 @@
 // The whole routed layer for a few tokens (T <= 16) in two launches: a plan
-// (routing, grouping, x in operand order) and one persistent kernel that runs
+// (routing, grouping, x in operand form) and one persistent kernel that runs
 // gate/up, down and the weighted sum of all experts without a launch between
-// them.  Weights, routing and arithmetic are those of moe_route_topk and
-// moe_mxfp4_ffn (bf16 x, exact MXFP4 weights, fp32 MFMA accumulation, SiLU(g) *
-// u in fp32), except that h enters the down product as three bf16 parts
-// (h = hi + mid + lo, exact to 2^-24), so its rounding stays below that of the
-// fp32 sums.
+// them.  Weights, routing and formulas are those of moe_route_topk and
+// moe_mxfp4_ffn.
+//
+// Products.  The 4-bit weights go into the block-scaled matrix instructions as
+// they are stored (16 bytes of codes and one scale byte per block), so decoding
+// costs five register operations a block.  The other operand is fp8 there, so
+// activations enter as fixed-point digits: with q = v / 2^s, 2^s chosen per
+// 32-block so that the block's largest |q| lies in [8, 16),
+//   d0 = rint(q), d1 = rint(32 (q - d0)), d2 = rint(32 (32 (q - d0) - d1)), ...
+// every digit an integer of magnitude <= 16 (exact in e4m3), digit p with the
+// scale 2^(s - 5p) in a column of its own; the columns are added in fp32.  The
+// instruction adds the products of a block in a fixed-point window of about
+// 2^14 below the largest (measured; e4m3 operands of 8 binades already lose
+// bits) and everything else in fp32: digits times E2M1 codes span 0.5 .. 96 and
+// stay inside, so each column is as exact as an fp32 sum.  x takes four
+// digits (2^-19 of its block's largest; a bf16 value within 2^-11 of that is
+// exact), h five (2^-24).
 //
 // With a few tokens the layer is a stream over the chosen experts' bytes
 // (about 4 flop per byte and row): what costs time beside the stream are its
 // interruptions, the drain and refill of the memory pipeline at every launch.
 // The persistent kernel has none: a wave takes units of work from one list,
-//   1. gate/up units: 16 features of w1 and of w3 for a tile of up to 4 rows of
-//      one expert, over all of D;
-//   2. down units: 32 features of w2 for one grouped row (three columns: its
-//      hi, mid and lo parts), over all of I;
+//   1. gate/up units: 32 features of w1 and of w3 for a tile of up to two rows
+//      of one expert, over all of D;
+//   2. down units: 32 features of w2 for one grouped row, over all of I;
 //   3. sum units: 32 features of out for all tokens, slots in order;
 // in that order, expert by expert, and streams their weights through a private
 // ring of three LDS stages that runs on across units.
@@ -29,26 +40,75 @@
 // out would give NaN outputs.)  A wave never waits with an unfinished unit in
 // its ring: a down unit that is not ready is held back until the ring is empty.
 //
-// Visibility.  Results (h parts, y) are written with device-scope stores, which
-// go through the XCD's L2, and counted (device-scope add, no return) once the
-// store has completed, that is once a later wait of the in-order vector-memory
-// counter covers it: three stages later, at no cost, or at once where the ring
-// runs dry.  A release fence would write back the whole L2 instead.  The
-// reader checks the count, then takes an acquire fence, after which its plain
-// loads see what was counted.  A wave checks only until it has seen every
-// gate/up unit counted.
+// Visibility.  Results (digits of h, y) are written with device-scope stores,
+// which go through the XCD's L2, and counted (device-scope add, no return) once
+// the store has completed, that is once a later wait of the in-order
+// vector-memory counter covers it: three stages later, at no cost, or at once
+// where the ring runs dry.  A release fence would write back the whole L2
+// instead.  The reader checks the count and then reads with device-scope loads,
+// which a stale line of its own L2 cannot answer; an acquire fence per check
+// would invalidate that L2 (57 ns each, measured, for every wave of the XCD in
+// turn).  A wave checks only until it has seen every gate/up unit counted.
+#include "mx_common.h"
 #include "route_device.h"
 #include "stream_device.h"
+
+#include <type_traits>
 
 namespace k3moe {
 namespace {
 
+constexpr int kXDigits = 4, kHDigits = 5;
+constexpr int kPlane = 512;     // bytes of one digit of a row's stage
+constexpr int kXRow = kXDigits * kPlane;        // x: digits of a (row, stage); its scales are apart
+constexpr int kHRow = kHDigits * kPlane + 16;   // h: digits and scales of a (row, stage)
+
+// Operand order.  A lane's 16 code bytes of a block hold elements j and j + 16 in
+// byte j, so digit bytes go in the order 0, 16, 1, 17, ...: element e < 16 at
+// byte 2e of the block's 32, element 16 + e at byte 2e + 1.  Of a stage's plane,
+// the 16-byte chunk c (block c / 2) sits at chunk c with its low three bits
+// xor the digit number, so that the columns of a read fall into different
+// banks.  The 16 scale bytes of a stage are transposed, block 4 r + g at byte
+// 4 g + r: a lane of group g reads its four rounds as one dword.
+//
+// Eight values in that order (those of quarter i of the block: elements 4i + t
+// and 16 + 4i + t) as N digits: out[p] = eight bytes.
+template <int N>
+__device__ __forceinline__ void digits8(const float (&v)[8], uint32_t e, uint2 (&out)[N]) {
+  const float unit = __uint_as_float((257u - e) << 23);  // 2^(130 - e): |v| * unit < 16
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = v[i] * unit;
+#pragma unroll
+  for (int p = 0; p < N; ++p) {
+    float d[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      d[i] = rintf(q[i]);
+      q[i] = (q[i] - d[i]) * 32.0f;  // exact: both are multiples of the unit's last bit
+    }
+    int lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[0], d[1], 0, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(d[2], d[3], lo, true);
+    int hi = __builtin_amdgcn_cvt_pk_fp8_f32(d[4], d[5], 0, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(d[6], d[7], hi, true);
+    out[p] = make_uint2((uint32_t)lo, (uint32_t)hi);
+  }
+}
+// Exponent field of a block for digits8, from its largest magnitude's bits: at
+// least 23, so that the scale byte e - 3 of digit 0 leaves room for 5 * 4 less.
+__device__ __forceinline__ uint32_t digit_exp(uint32_t top) { return max(top >> 23, 23u); }
+// Byte offset in a stage's plane of quarter i of block bb, digit p.
+__device__ __forceinline__ int digit_at(int bb, int i, int p) {
+  const int c = 2 * bb + (i >> 1);
+  return 16 * ((c & ~7) | ((c ^ p) & 7)) + 8 * (i & 1);
+}
+
 // ---------------------------------------------------------------------------
 // Plan.  Workgroup 0 routes (a wave per token), groups the T * k entries by
-// expert and clears the counters of the main kernel; the others write x in the
-// operand order of the decoded blocks (P order).
+// expert and clears the counters of the main kernel; the others write x as
+// digits.
 constexpr int kPlanThreads = 1024;
-constexpr int kGuTileRows = 4;
+constexpr int kGuTileRows = 2;
 
 struct LayerPlan {
   const float* logits;
@@ -58,12 +118,12 @@ struct LayerPlan {
   float route_scale;
   int32_t* ids;    // [T, k]
   float* w;        // [T, k]
-  uint16_t* xp;    // [T, D]
-  int4* gt;        // gate/up tiles: expert, first row, rows
+  uint8_t* xd;     // [T][stages][kXRow] digits of x
+  uint8_t* xs;     // [T][stages][16] their scale bytes
+  int4* gt;        // gate/up tiles: expert, first row, rows, tokens of the rows (a byte each)
   int2* rows;      // grouped rows: expert, gate/up tile
-  int32_t* row_tok;
   int32_t* slot_row;
-  int32_t* head;   // [0] gate/up tiles, [1] next ticket, [2] gate/up units counted
+  int32_t* head;   // [0] gate/up tiles, [1] next ticket
   uint32_t* flags;
   int n_flags;
 };
@@ -72,18 +132,26 @@ template <int NPER>
 __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
   const int tid = threadIdx.x;
   if (blockIdx.x > 0) {
-    // position 8i + 2t (+1) of a 32-block holds element 4i + t (16 + 4i + t)
-    const int64_t n = (int64_t)p.T * p.D / 8;
-    const int64_t u = (int64_t)(blockIdx.x - 1) * kPlanThreads + tid;
-    if (u >= n) return;
-    const uint16_t* src = p.x + (u >> 2) * 32 + 4 * (u & 3);
+    // four lanes a block, eight elements each
+    const int nb = p.D >> 5, nst = (nb + 15) >> 4;
+    const int u = (int)(blockIdx.x - 1) * kPlanThreads + tid;
+    if (u >= p.T * nb * 4) return;
+    const int i = u & 3, t = (u >> 2) / nb, b = (u >> 2) - t * nb;
+    const uint16_t* src = p.x + (int64_t)t * p.D + 32 * b + 4 * i;
     const uint2 lo = *reinterpret_cast<const uint2*>(src), hi = *reinterpret_cast<const uint2*>(src + 16);
-    uint4 r;
-    r.x = __builtin_amdgcn_perm(hi.x, lo.x, 0x05040100u);
-    r.y = __builtin_amdgcn_perm(hi.x, lo.x, 0x07060302u);
-    r.z = __builtin_amdgcn_perm(hi.y, lo.y, 0x05040100u);
-    r.w = __builtin_amdgcn_perm(hi.y, lo.y, 0x07060302u);
-    reinterpret_cast<uint4*>(p.xp)[u] = r;
+    float v[8];
+    v[0] = __uint_as_float(lo.x << 16), v[2] = __uint_as_float(lo.x & 0xFFFF0000u);
+    v[4] = __uint_as_float(lo.y << 16), v[6] = __uint_as_float(lo.y & 0xFFFF0000u);
+    v[1] = __uint_as_float(hi.x << 16), v[3] = __uint_as_float(hi.x & 0xFFFF0000u);
+    v[5] = __uint_as_float(hi.y << 16), v[7] = __uint_as_float(hi.y & 0xFFFF0000u);
+    const uint32_t e = digit_exp(mx_block_top(v));
+    uint2 d[kXDigits];
+    digits8<kXDigits>(v, e, d);
+    const int64_t piece = (int64_t)t * nst + (b >> 4);
+#pragma unroll
+    for (int q = 0; q < kXDigits; ++q)
+      *reinterpret_cast<uint2*>(p.xd + piece * kXRow + q * kPlane + digit_at(b & 15, i, q)) = d[q];
+    if (i == 0) p.xs[piece * 16 + 4 * (b & 3) + ((b & 15) >> 2)] = (uint8_t)(e - 3u);
     return;
   }
   __shared__ uint32_t s_mask[K3MOE_MAX_EXPERTS_FFN];  // tokens of each expert
@@ -140,7 +208,15 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
     const int m = __popc(s_mask[e]);
     if (m == 0) continue;
     s_base[e] = (uint32_t)at[0] | (uint32_t)at[1] << 16;
-    for (int r = 0; r < m; r += kGuTileRows) p.gt[at[1]++] = make_int4(e, at[0] + r, min(kGuTileRows, m - r), 0);
+    uint32_t toks = s_mask[e];
+    for (int r = 0; r < m; r += kGuTileRows) {
+      int tk = 0;
+      for (int i = 0; i < min(kGuTileRows, m - r); ++i) {
+        tk |= __builtin_ctz(toks) << (8 * i);
+        toks &= toks - 1u;
+      }
+      p.gt[at[1]++] = make_int4(e, at[0] + r, min(kGuTileRows, m - r), tk);
+    }
     at[0] += m;
   }
   __syncthreads();
@@ -150,243 +226,333 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
     const uint32_t b = s_base[e];
     const int row = (int)(b & 0xFFFFu) + rank;
     p.slot_row[tid] = row;
-    p.row_tok[row] = t;
     p.rows[row] = make_int2(e, (int)(b >> 16) + rank / kGuTileRows);
   }
   if (tid == 0) {
     p.head[0] = tiles;
     p.head[1] = 0;
-    p.head[2] = 0;
   }
 }
 
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 4;            // waves per workgroup, one workgroup per CU
 constexpr int kRing = 3;             // LDS stages per wave
-constexpr int kStageK = 512;         // K per stage: 16 blocks of each row
-constexpr int kStageRowBytes = 272;  // bytes of a weight row per whole stage
-constexpr int kRowDw = 68;
-constexpr int kMatBytes = 16 * kStageRowBytes;  // a 16-row group of a stage
+constexpr int kMatBytes = 16 * 272;  // a 16-row group of a whole stage: 16 rows x 16 blocks of 17 bytes
+constexpr int kRowDw = 68;           // dwords of a row of it
 constexpr int kWBytes = 2 * kMatBytes;
-constexpr int kActRow = 1040;        // LDS bytes per activation row (1024 + 16)
-constexpr int kActRows = 4;
-constexpr int kStageBytes = kWBytes + kActRows * kActRow;
-constexpr int kMatLoads = 5;         // 16-byte-a-lane loads of a group's stage (4352 bytes)
-constexpr int kW = 2 * kMatLoads;    // weight loads per stage
+constexpr int kXRowLds = kXRow + 64; // second row of a gate/up tile: four 16-byte banks on
+constexpr int kActBytes = kXRowLds + kXRow;  // also holds the kHRow bytes of a down row
+constexpr int kStageBytes = kWBytes + kActBytes + 64;  // + scale bytes of x
+constexpr int kChunks = 2 * 16 * 17; // 16-byte chunks of a stage's two groups
+constexpr int kW = (kChunks + 63) / 64;  // weight loads per stage; the last is partial
 constexpr int kNt = 2;               // cache policy of the weight loads: nontemporal
+constexpr int kDevScope = 16;        // cache policy of a load that must see other XCDs' stores (sc1)
 constexpr int kSpinLimit = 1 << 21;
+constexpr int kChunk = 4;            // tickets a workgroup draws at once
+// Counters sit on lines of their own: device-scope adds to one line are served
+// one after another, 11.4 ns each (measured; to different lines they overlap).
+constexpr int kFlagStride = 32;
+static_assert(kHRow <= kActBytes, "a down row fits the activation part");
 static_assert(kWaves * kRing * kStageBytes <= 160 * 1024, "LDS");
 
 enum { kGateUp = 0, kDown = 1, kSum = 2, kNone = 3 };
 
 struct LayerArgs {
-  const uint16_t* xp;
+  const uint8_t *xd, *xs;
   const uint8_t *w1, *w3, *w2;
   int D, I, T, k;
   const int4* gt;
   const int2* rows;
-  const int32_t* row_tok;
   const int32_t* slot_row;
   const float* w;
   int32_t* head;
-  uint32_t* flags;  // [rows] gate/up units done per tile, then [D / 32] down units done per feature group
-  uint16_t* h;      // [3][rows][hstride] bf16 parts in P order
-  int64_t hplane;   // elements between the parts
-  int hstride;      // elements between rows
+  uint32_t* flags;  // gate/up units done per tile ([rows]), then down units done per feature group ([D / 32])
+  uint8_t* h;       // [rows][hstride] digits and scales of h, stage by stage
+  int hstride;
   float* y;         // [rows][D]
   float* out;       // [T, D]
 };
 
 struct Unit {
-  int kind, fg, expert, row0, nrows, tile;
+  int kind, fg, expert, row0, nrows, tile, toks;
 };
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-__device__ __forceinline__ void store_dev(uint16_t* p, uint32_t v) {
-  __hip_atomic_store(p, (uint16_t)v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ __forceinline__ void store_dev(uint8_t* p, uint2 v) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)v.y << 32 | v.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ __forceinline__ void store_dev(float* p, f32x4_t v) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  const f32x2 a = {v[0], v[1]}, b = {v[2], v[3]};
-  uint64_t* q = reinterpret_cast<uint64_t*>(p);
-  __hip_atomic_store(q, __builtin_bit_cast(uint64_t, a), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  __hip_atomic_store(q + 1, __builtin_bit_cast(uint64_t, b), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  uint8_t* q = reinterpret_cast<uint8_t*>(p);
+  store_dev(q, make_uint2(__float_as_uint(v[0]), __float_as_uint(v[1])));
+  store_dev(q + 8, make_uint2(__float_as_uint(v[2]), __float_as_uint(v[3])));
 }
 
-// Blocks of the last, shorter stage (width blocks per row): MFMA rounds one at
-// a time, block b of row rho at byte (rho * width + b) * 17 of the group.
-__device__ __forceinline__ void tail_round(const uint8_t* group, int rho, int b, int width, bf16x8_t op[4]) {
-  const int bb = min(b, width - 1);
-  const uint32_t at = (uint32_t)(rho * width + bb) * 17u, sh = at & 3u;
-  const uint32_t* d = reinterpret_cast<const uint32_t*>(group) + (at >> 2);
-  const uint32_t sel = 0x03020100u + 0x01010101u * (sh + 1u);  // bytes sh + 1 .. of two neighbouring dwords
-  uint32_t v[5];
+// Sums of one 16-row group: codes of four rounds (block 4 rnd + g of row rho) times the staged digits.
+struct BOperand {
+  u32x4_t q[4][2];  // per round: positions 16 g .. of the round's first and second 64
+  uint32_t scale;   // byte rnd: scale of block 4 rnd + g
+};
+template <int kRnd>
+__device__ __forceinline__ f32x4_t mfma_round(const uint32_t (&a)[4], uint32_t sa, const BOperand& b, f32x4_t c) {
+  const i32x8_t av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const u32x4_t lo = b.q[kRnd][0], hi = b.q[kRnd][1];
+  const i32x8_t bv = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 0, 0, (int)sa, kRnd, (int)b.scale);
+}
+
+// Both 16-row groups of a stage in LDS at `st`.  A block starts at byte sh of
+// its first dword: sh = g in a whole stage; (rho * width + block) * 17 % 4 in
+// the last, shorter one (kTail), whose blocks from `width` on count as zeros.
+template <bool kTail>
+__device__ __forceinline__ void stage_sums(const uint8_t* st, int rho, int g, int width, const BOperand& b, f32x4_t& c0,
+                                           f32x4_t& c1) {
+  uint32_t d[2][4][5];
+  uint32_t sh[4];
 #pragma unroll
-  for (int i = 0; i < 5; ++i) v[i] = d[i];
-  const float sf = e8m0_to_f32(__builtin_amdgcn_ubfe(v[0], 8 * sh, 8));
+  for (int rnd = 0; rnd < 4; ++rnd) {
+    int at;
+    if constexpr (kTail) {
+      at = (rho * width + min(4 * rnd + g, width - 1)) * 17;
+      sh[rnd] = (uint32_t)at & 3u;
+      at >>= 2;
+    } else {
+      at = rho * kRowDw + 17 * rnd + 4 * g;
+      sh[rnd] = (uint32_t)g;
+    }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t q = __builtin_amdgcn_perm(v[i + 1], v[i], sel);
-    op[i] = decode_dword(b < width ? q : 0u, sf);
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int j = 0; j < 5; ++j) d[mi][rnd][j] = reinterpret_cast<const uint32_t*>(st + mi * kMatBytes)[at + j];
   }
+  auto round = [&](auto rc) __attribute__((always_inline)) {
+    constexpr int rnd = decltype(rc)::value;
+    const uint32_t sel = 0x04030201u + 0x01010101u * sh[rnd];
+    uint32_t a[2][4], sa[2];
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[mi][i] = __builtin_amdgcn_perm(d[mi][rnd][i + 1], d[mi][rnd][i], sel);
+      sa[mi] = d[mi][rnd][0] >> (8 * sh[rnd]);  // byte 0 counts
+      if (kTail && 4 * rnd + g >= width) {
+        a[mi][0] = a[mi][1] = a[mi][2] = a[mi][3] = 0u;
+        sa[mi] = 127u;
+      }
+    }
+    c0 = mfma_round<rnd>(a[0], sa[0], b, c0);
+    c1 = mfma_round<rnd>(a[1], sa[1], b, c1);
+  };
+  round(std::integral_constant<int, 0>{});
+  round(std::integral_constant<int, 1>{});
+  round(std::integral_constant<int, 2>{});
+  round(std::integral_constant<int, 3>{});
 }
 
 __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves][kRing][kStageBytes];
-  __shared__ int fifo[kWaves][4][8];
-  __shared__ int s_first;
+  __shared__ unsigned long long s_pool;
 
   const int lane = threadIdx.x & 63;
   const int wave = uni(threadIdx.x >> 6);
   const int rho = lane & 15, g = lane >> 4;
   const int nrows = a.T * a.k;
-  const int nfg = a.I >> 4, nfu = a.D >> 5;
-  const int n_gu = *as_const(a.head) * nfg, n_dn = nrows * nfu;
-  const uint32_t row_b13 = (uint32_t)(a.D >> 5) * 17, row_b2 = (uint32_t)(a.I >> 5) * 17;
-  const int nst13 = (a.D + kStageK - 1) / kStageK, nst2 = (a.I + kStageK - 1) / kStageK;
+  const int nfg = a.I >> 5, nfu = a.D >> 5;
+  const int n_gt = *as_const(a.head);
+  const int n_gu = n_gt * nfg, n_dn = nrows * nfu;
+  const uint32_t grp13 = (uint32_t)nfu * 272, grp2 = (uint32_t)nfg * 272;  // bytes of a 16-row group
+  const int nst13 = (nfu + 15) >> 4, nst2 = (nfg + 15) >> 4;
+  const float rcp_fg = 1.0f / (float)nfg, rcp_fu = 1.0f / (float)nfu;
 
-  auto claim = [&]() -> int {
-    int v = 0;
-    if (lane == 0) v = __hip_atomic_fetch_add(a.head + 1, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    return uni(v);
+  // n / d for 0 <= n < 2^23 by its reciprocal r (one step off at most)
+  auto div = [](int n, int d, float r) {
+    int q = (int)((float)n * r);
+    q -= q * d > n ? 1 : 0;
+    q += (q + 1) * d <= n ? 1 : 0;
+    return q;
   };
-  auto unit_of = [&](int t) -> Unit {
+  auto unit_of = [&](int t) __attribute__((always_inline)) -> Unit {
     if (t < n_gu) {
-      const int i = t / nfg;
+      const int i = uni(div(t, nfg, rcp_fg));
       const auto q = as_const(reinterpret_cast<const int32_t*>(a.gt)) + 4 * i;
-      return Unit{kGateUp, t - i * nfg, q[0], q[1], q[2], i};
+      return Unit{kGateUp, t - i * nfg, q[0], q[1], q[2], i, q[3]};
     }
     t -= n_gu;
     if (t < n_dn) {
-      const int r = t / nfu;
+      const int r = uni(div(t, nfu, rcp_fu));
       const auto q = as_const(reinterpret_cast<const int32_t*>(a.rows)) + 2 * r;
-      return Unit{kDown, t - r * nfu, q[0], r, 1, q[1]};
+      return Unit{kDown, t - r * nfu, q[0], r, 1, q[1], 0};
     }
     t -= n_dn;
-    return Unit{t < nfu ? kSum : kNone, t, 0, 0, 0, 0};
+    return Unit{t < nfu ? kSum : kNone, t, 0, 0, 0, 0, 0};
   };
 
-  // the workgroup's first four tickets in one add
-  if (threadIdx.x == 0) s_first = __hip_atomic_fetch_add(a.head + 1, kWaves, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // Tickets: the workgroup draws kChunk consecutive ones at a time and its
+  // waves take them from LDS (low half: the next ticket, high half: how many
+  // are left, or kRefill while the wave that found none fetches more; that wave
+  // is running and waits only for its add to return).
+  constexpr uint32_t kRefill = 0xFFFFFFFFu;
+  if (threadIdx.x == 0) s_pool = 0ull;
   __syncthreads();
-  Unit iu = unit_of(uni(s_first) + wave);  // the unit to issue next (or being issued)
+  auto claim = [&]() __attribute__((always_inline)) -> int {
+    int v = 0;
+    if (lane == 0)
+      for (;;) {
+        unsigned long long s = __hip_atomic_load(&s_pool, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        const uint32_t left = (uint32_t)(s >> 32);
+        if (left == kRefill) {
+          __builtin_amdgcn_s_sleep(1);
+        } else if (left > 0) {
+          if (__hip_atomic_compare_exchange_strong(&s_pool, &s, s + 1ull - (1ull << 32), __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                                   __HIP_MEMORY_SCOPE_WORKGROUP)) {
+            v = (int)(uint32_t)s;
+            break;
+          }
+        } else if (__hip_atomic_compare_exchange_strong(&s_pool, &s, (unsigned long long)kRefill << 32, __ATOMIC_RELAXED,
+                                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) {
+          v = __hip_atomic_fetch_add(a.head + 1, kChunk, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          __hip_atomic_store(&s_pool, (unsigned long long)(kChunk - 1) << 32 | (uint32_t)(v + 1), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_WORKGROUP);
+          break;
+        }
+      }
+    return uni(v);
+  };
+  Unit iu = unit_of(claim());  // the unit being issued, or the next one
+  Unit nu{kNone, 0, 0, 0, 0, 0, 0};  // the one after it, drawn while iu's loads go out
+  bool drawn = true;
 
-  uint32_t woff[kMatLoads];
-#pragma unroll
-  for (int j = 0; j < kMatLoads; ++j) {
-    const int c = 64 * j + lane;
-    woff[j] = c < 16 * 17 ? 16u * (uint32_t)c : 0u;
-  }
-  const bool wtail = lane < 16 * 17 - 64 * (kMatLoads - 1);
+  // Chunk c = 64 j + lane of a stage: byte 16 c of the first group's run, then
+  // of the second group's, `grp` bytes on in the matrix.
+  uint32_t woff[kW];
+  const bool wlast = lane < kChunks - 64 * (kW - 1);
+  const __amdgpu_buffer_rsrc_t xr =
+      __builtin_amdgcn_make_buffer_rsrc((void*)a.xd, 0, a.T * nst13 * kXRow, 0x00020000);
+  const __amdgpu_buffer_rsrc_t xsr = __builtin_amdgcn_make_buffer_rsrc((void*)a.xs, 0, a.T * nst13 * 16, 0x00020000);
+  const __amdgpu_buffer_rsrc_t hr = __builtin_amdgcn_make_buffer_rsrc((void*)a.h, 0, nrows * a.hstride, 0x00020000);
 
-  // ---- issue side
-  const uint8_t* wbase[2];
-  uint32_t wrows = 0;  // bytes of a 16-row group
-  uint32_t xsrc[kActRows];
-  int is = 0, ist = 0;      // stage of iu, its number of stages
-  bool open = false;        // iu's loads have begun
+  // ---- issue side.  A stage is the same 512 columns of two neighbouring 16-row
+  // groups of one matrix: of w2 (down), or of w1 and then of w3 (gate/up), where
+  // the digits of x travel with w1.
+  const uint8_t *wb0 = nullptr, *wb1 = nullptr;  // first group of w1 and w3, or of w2
+  uint32_t grp = 0;         // bytes of a 16-row group of iu's matrix
+  uint32_t wso = 0;         // byte of the stage in it
+  int act0 = 0, act1 = 0;   // byte offsets of the stage's activations: rows of x, or (act0) the row of h
+  uint32_t sco = 0;         // per lane: scale bytes of tile row `lane`
+  int left = 0;             // stages of iu not yet issued (0: iu's loads have not begun)
   bool bad = false;         // a bounded wait ran out
   bool all_done = false;    // every gate/up unit has been seen counted
-  int pushed = 0, popped = 0;
+  bool waited = false;      // iu's tile has been waited for
 
-  auto prep = [&]() {
-    if (iu.kind == kGateUp) {
-      const size_t off = (size_t)iu.expert * a.I * row_b13 + (size_t)(16 * iu.fg) * row_b13;
-      wbase[0] = a.w1 + off;
-      wbase[1] = a.w3 + off;
-      wrows = 16 * row_b13;
-      ist = nst13;
+  auto prep = [&]() __attribute__((always_inline)) {
+    // (plain values first, assigned once: the compiler would merge assignments
+    // at the ends of two branches into one through memory)
+    const bool gu = iu.kind == kGateUp;
+    const uint32_t gb = gu ? grp13 : grp2;
+    const size_t off = ((size_t)iu.expert * (size_t)(2 * (gu ? nfg : nfu)) + (size_t)(2 * iu.fg)) * gb;
+    const int t0 = iu.toks & 255, t1 = (iu.toks >> 8) & 255;
+    wb0 = (gu ? a.w1 : a.w2) + off;
+    wb1 = a.w3 + off;
+    grp = gb;
 #pragma unroll
-      for (int m = 0; m < kActRows; ++m)
-        xsrc[m] = (uint32_t)as_const(a.row_tok)[iu.row0 + (m < iu.nrows ? m : 0)] * (uint32_t)a.D * 2;
-    } else {
-      const size_t off = (size_t)iu.expert * a.D * row_b2 + (size_t)(32 * iu.fg) * row_b2;
-      wrows = 16 * row_b2;
-      wbase[0] = a.w2 + off;
-      wbase[1] = a.w2 + off + wrows;
-      ist = nst2;
+    for (int j = 0; j < kW; ++j) {
+      const int c = 64 * j + lane;
+      woff[j] = c < kChunks / 2 ? 16u * (uint32_t)c : gb + 16u * (uint32_t)(c - kChunks / 2);
     }
-    is = 0;
-    open = true;
-    int* f = fifo[wave][pushed & 3];
-    ++pushed;
-    if (lane == 0) {
-      f[0] = iu.kind, f[1] = iu.fg, f[2] = iu.row0, f[3] = iu.nrows, f[4] = iu.tile;
+    left = gu ? 2 * nst13 : nst2;
+    act0 = uni(gu ? t0 * nst13 * kXRow : iu.row0 * a.hstride);
+    act1 = uni(t1 * nst13 * kXRow);
+    sco = (uint32_t)((lane == 1 ? t1 : t0) * nst13) * 16;
+    wso = 0;
+    drawn = false;
+    waited = false;
+  };
+  // What a stage in flight is: bit 0 kind, 1 w3, 2 last stage of its
+  // unit, 3 shorter stage; bits 4.. its activation loads, 8.. its features;
+  // and row0 | rows << 10 | tile << 16.
+  int sd0[kRing] = {0, 0, 0}, sd1[kRing] = {0, 0, 0};
+  int inflight = 0;
+  auto load_x = [&](uint8_t* dst, int so) __attribute__((always_inline)) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (__attribute__((address_space(3))) void*)(uintptr_t)dst, 16, 16 * lane, so, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 1024), 16, 16 * lane,
+                                             so + 1024, 0, 0);
+  };
+  auto issue = [&](int buf) __attribute__((always_inline)) {
+    uint8_t* const dst = &lds[wave][buf][0];
+    uint8_t* const ad = dst + kWBytes;
+    const bool gu = iu.kind == kGateUp;
+    const bool half = gu && (left & 1) != 0;  // an even number of stages: w3 at the odd ones
+    const __amdgpu_buffer_rsrc_t wr =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(half ? wb1 : wb0), 0, (int)(2 * grp), 0x00020000);
+#pragma unroll
+    for (int j = 0; j < kW - 1; ++j) {
+      const uint32_t vo = woff[j];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 1024 * j), 16, vo, wso,
+                                               0, kNt);
+    }
+    if (wlast) {
+      const uint32_t vo = woff[kW - 1];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          wr, (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 1024 * (kW - 1)), 16, vo, wso, 0, kNt);
+    }
+    const bool tail = wso + kMatBytes > grp;
+    const int d0 = (gu ? 0 : 1) | (half ? 2 : 0) | (left == 1 ? 4 : 0) | (tail ? 8 : 0) |
+                   (half ? 0 : gu ? 2 * iu.nrows + 1 : 3) << 4 | iu.fg << 8;
+    const int d1 = iu.row0 | iu.nrows << 10 | iu.tile << 16;
+    if (!gu) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(hr, (__attribute__((address_space(3))) void*)(uintptr_t)ad, 16, 16 * lane, act0, 0,
+                                               kDevScope);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(hr, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + 1024), 16, 16 * lane,
+                                               act0 + 1024, 0, kDevScope);
+      if (lane < (kHRow - 2048) / 16)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(hr, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + 2048), 16, 16 * lane,
+                                                 act0 + 2048, 0, kDevScope);
+    } else if (!half) {
+      load_x(ad, act0);
+      if (iu.nrows > 1) load_x(ad + kXRowLds, act1);
+      if (lane < iu.nrows)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(xsr, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + kActBytes), 16, sco, 0,
+                                                 0, 0);
+    }
+    act0 += gu ? (half ? 0 : kXRow) : kHRow;
+    act1 += half ? 0 : kXRow;
+    sco += half ? 0u : 16u;
+    wso += gu && !half ? 0u : kMatBytes;
+    sd0[2] = inflight == 2 ? d0 : sd0[2], sd1[2] = inflight == 2 ? d1 : sd1[2];
+    sd0[1] = inflight == 1 ? d0 : sd0[1], sd1[1] = inflight == 1 ? d1 : sd1[1];
+    sd0[0] = inflight == 0 ? d0 : sd0[0], sd1[0] = inflight == 0 ? d1 : sd1[0];
+    ++inflight;
+    if (--left == 0) {
+      if (!drawn) nu = unit_of(claim());
+      drawn = true;
+      iu = nu;
     }
   };
-  // issues one stage of iu into ring buffer `buf`; returns its activation loads
-  auto issue = [&](int buf) -> int {
-    uint8_t* dst = &lds[wave][buf][0];
-    const uint32_t wso = (uint32_t)(kMatBytes * is);
-#pragma unroll
-    for (int mi = 0; mi < 2; ++mi) {
-      const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)wbase[mi], 0, (int)wrows, 0x00020000);
-#pragma unroll
-      for (int j = 0; j < kMatLoads - 1; ++j) {
-        const uint32_t vo = woff[j];
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (__attribute__((address_space(3))) void*)(uintptr_t)(dst + mi * kMatBytes + 1024 * j),
-                                                 16, vo, wso, 0, kNt);
-      }
-      if (wtail) {
-        const uint32_t vo = woff[kMatLoads - 1];
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            wr, (__attribute__((address_space(3))) void*)(uintptr_t)(dst + mi * kMatBytes + 1024 * (kMatLoads - 1)), 16, vo, wso, 0, kNt);
-      }
-    }
-    uint8_t* adst = dst + kWBytes;
-    const uint32_t aso = (uint32_t)(kStageK * 2 * is);
-    int n = 0;
-    if (iu.kind == kGateUp) {
-      const __amdgpu_buffer_rsrc_t xr =
-          __builtin_amdgcn_make_buffer_rsrc((void*)a.xp, 0, (int)((uint32_t)a.T * (uint32_t)a.D * 2), 0x00020000);
-#pragma unroll
-      for (int m = 0; m < kActRows; ++m)
-        if (m < iu.nrows) {
-          const uint32_t so = xsrc[m] + aso;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (__attribute__((address_space(3))) void*)(uintptr_t)(adst + kActRow * m), 16,
-                                                   16 * lane, so, 0, 0);
-        }
-      n = iu.nrows;
-    } else {
-#pragma unroll
-      for (int m = 0; m < 3; ++m) {
-        const uint16_t* hb = a.h + m * a.hplane + (int64_t)iu.row0 * a.hstride;
-        const __amdgpu_buffer_rsrc_t hr = __builtin_amdgcn_make_buffer_rsrc((void*)hb, 0, a.I * 2, 0x00020000);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(hr, (__attribute__((address_space(3))) void*)(uintptr_t)(adst + kActRow * m), 16,
-                                                 16 * lane, aso, 0, 0);
-      }
-      n = 3;
-    }
-    if (++is == ist) {
-      open = false;
-      iu = unit_of(claim());
-    }
-    return n;
-  };
-  auto seen = [&](const uint32_t* f) -> uint32_t {
+  auto seen = [&](const uint32_t* f) __attribute__((always_inline)) -> uint32_t {
     return (uint32_t)uni((int)__hip_atomic_load(f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
   };
   // whether iu can be issued now (no waiting)
-  auto ready = [&]() -> bool {
+  auto ready = [&]() __attribute__((always_inline)) -> bool {
     if (iu.kind == kGateUp) return true;
     if (iu.kind != kDown) return false;
-    if (all_done) return true;
-    if (seen(a.flags + iu.tile) < (uint32_t)nfg) return false;
-    all_done = seen(reinterpret_cast<const uint32_t*>(a.head) + 2) >= (uint32_t)n_gu;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+    if (all_done || waited) return true;
+    if (seen(a.flags + iu.tile * kFlagStride) < (uint32_t)nfg) return false;
+    bool all = true;  // look whether that was the last check this wave needs
+    for (int i = lane; i < n_gt; i += 64)
+      all = all && __hip_atomic_load(a.flags + i * kFlagStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= (uint32_t)nfg;
+    all_done = __all(all);
     return true;
   };
 
   // ---- publishing
   int pub[3] = {-1, -1, -1};  // flags of finished units, by age in stages
-  auto publish = [&](int f) {
-    if (f >= 0 && lane == 0) {
-      (void)__hip_atomic_fetch_add(a.flags + f, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (f < nrows) (void)__hip_atomic_fetch_add(a.head + 2, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
+  auto publish = [&](int f) __attribute__((always_inline)) {
+    if (f >= 0 && lane == 0)
+      (void)__hip_atomic_fetch_add(a.flags + f * kFlagStride, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
-  auto flush = [&]() {
+  auto flush = [&]() __attribute__((always_inline)) {
     wait_vm<0>();
 #pragma unroll
     for (int i = 2; i >= 0; --i) {
@@ -395,35 +561,31 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     }
   };
 
-  f32x4_t acc[2][2];
-#pragma unroll
-  for (int mi = 0; mi < 2; ++mi) acc[mi][0] = acc[mi][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const uint32_t qsel = 0x03020100u + 0x01010101u * (uint32_t)(g + 1);
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc[2][2] = {{zero, zero}, {zero, zero}};  // [w1 / w3 by turns][16-row group]
+  BOperand bop{};
+  // LDS offsets of this lane's digits.  gate/up: column 4 r + p is digit p of
+  // tile row r; columns from 8 on repeat.  down: columns 0 .. 4 are the digits.
+  const int xp = rho & 3, hp = rho < kHDigits ? rho : 0;
+  const int xoff0 = xp * kPlane + 16 * (g ^ xp), xoff1 = xp * kPlane + 16 * ((4 + g) ^ xp);
+  const int hoff0 = hp * kPlane + 16 * (g ^ hp), hoff1 = hp * kPlane + 16 * ((4 + g) ^ hp);
+  const uint32_t xsub = 0x05050505u * (uint32_t)xp, hsub = 0x05050505u * (uint32_t)hp;
 
-  int buf_i = 0, buf_c = 0, inflight = 0;
-  int na[kRing] = {0, 0, 0};  // activation loads of the stages in flight, oldest first
-  Unit cu{kNone, 0, 0, 0, 0, 0};
-  int cs = 0, cst = 0;  // stage of cu, its number of stages (0: no unit)
-  int boff = kWBytes;
-
+  int buf_i = 0, buf_c = 0;
   for (;;) {
     while (inflight < kRing) {
-      if (!open) {
+      if (left == 0) {
         if (!ready()) break;
         prep();
       }
-      const int n = issue(buf_i);
+      issue(buf_i);
       buf_i = buf_i == kRing - 1 ? 0 : buf_i + 1;
-      if (inflight == 0) na[0] = n;
-      else if (inflight == 1) na[1] = n;
-      else na[2] = n;
-      ++inflight;
     }
     if (inflight == 0) {
       // the ring is empty and iu cannot start: count what is finished, then wait
       flush();
       if (iu.kind == kNone) break;
-      const uint32_t* f = a.flags + (iu.kind == kDown ? iu.tile : nrows + iu.fg);
+      const uint32_t* f = a.flags + (iu.kind == kDown ? iu.tile : nrows + iu.fg) * kFlagStride;
       const uint32_t need = iu.kind == kDown ? (uint32_t)nfg : (uint32_t)nrows;
       int spins = 0;
       while (seen(f) < need) {
@@ -433,151 +595,164 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
           break;
         }
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
       if (iu.kind == kSum) {
-        // eight lanes a token (four features each), eight tokens at a time
-        const int f4 = 32 * iu.fg + 4 * (lane & 7);
+        // eight lanes a token (four features each), eight tokens and 16 slots at a time
+        const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc((void*)a.y, 0, nrows * a.D * 4, 0x00020000);
+        const uint32_t f4 = (uint32_t)(32 * iu.fg + 4 * (lane & 7));
         for (int t = lane >> 3; t < a.T; t += 8) {
-          f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
-          for (int j = 0; j < a.k; ++j) {
-            const float wt = a.w[t * a.k + j];
-            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(a.y + (int64_t)a.slot_row[t * a.k + j] * a.D + f4);
+          f32x4_t sum = zero;
+          for (int j0 = 0; j0 < a.k; j0 += 16) {
+            uint32_t at[16];
+            float wt[16];
+            u32x4_t v[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) sum[c] = fmaf(wt, v[c], sum[c]);
+            for (int j = 0; j < 16; ++j) {
+              const int q = t * a.k + min(j0 + j, a.k - 1);
+              at[j] = (uint32_t)a.slot_row[q] * (uint32_t)a.D * 4 + 4 * f4;
+              wt[j] = a.w[q];
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = __builtin_amdgcn_raw_buffer_load_b128(yr, at[j], 0, kDevScope);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (j0 + j < a.k)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const uint32_t bits = v[j][c];
+                  sum[c] = fmaf(wt[j], __uint_as_float(bits), sum[c]);
+                }
           }
           if (bad) sum[0] = sum[1] = sum[2] = sum[3] = __uint_as_float(0x7FC00000u);
           *reinterpret_cast<f32x4_t*>(a.out + (int64_t)t * a.D + f4) = sum;
         }
         iu = unit_of(claim());
       } else {
-        prep();
-        const int n = issue(buf_i);
-        buf_i = buf_i == kRing - 1 ? 0 : buf_i + 1;
-        na[0] = n;
-        inflight = 1;
+        waited = true;
       }
       continue;
     }
 
+    if (!drawn && inflight == kRing) {  // with the ring full
+      nu = unit_of(claim());
+      drawn = true;
+    }
     // the oldest stage has landed once only the loads of the newer ones are out
-    if (inflight == 3)
-      wait_vm_plus<2 * kW>(na[1] + na[2]);
-    else if (inflight == 2)
-      wait_vm_plus<kW>(na[1]);
-    else
+    // (activation loads of a stage: 0, 3 or 5, so these counts are exact but at
+    // a change of kind, where they wait for a little more)
+    if (inflight == 3) {
+      const int n = ((sd0[1] >> 4) & 15) + ((sd0[2] >> 4) & 15);
+      if (n >= 6) wait_vm<2 * kW + 6>();
+      else if (n >= 5) wait_vm<2 * kW + 5>();
+      else if (n >= 3) wait_vm<2 * kW + 3>();
+      else wait_vm<2 * kW>();
+    } else if (inflight == 2) {
+      wait_vm<kW>();
+    } else {
       wait_vm<0>();
+    }
     // a unit finished three stages ago: its stores are older than these loads
     publish(pub[2]);
     pub[2] = pub[1];
     pub[1] = pub[0];
     pub[0] = -1;
-    if (cst == 0) {
-      const int* f = fifo[wave][popped & 3];
-      ++popped;
-      cu.kind = uni(f[0]), cu.fg = uni(f[1]), cu.row0 = uni(f[2]), cu.nrows = uni(f[3]), cu.tile = uni(f[4]);
-      cs = 0;
-      cst = cu.kind == kGateUp ? nst13 : nst2;
-      // column rho reads activation row rho: tile row (gate/up), part of h
-      // (down); the other columns repeat row 0 and are dropped
-      boff = kWBytes + kActRow * (rho < (cu.kind == kGateUp ? cu.nrows : 3) ? rho : 0);
-    }
-    const uint8_t* st = &lds[wave][buf_c][0];
+    const int d0 = sd0[0], d1 = sd1[0];
+    sd0[0] = sd0[1], sd1[0] = sd1[1];
+    sd0[1] = sd0[2], sd1[1] = sd1[2];
+    const uint8_t* const st = &lds[wave][buf_c][0];
     buf_c = buf_c == kRing - 1 ? 0 : buf_c + 1;
     --inflight;
-    na[0] = na[1];
-    na[1] = na[2];
-    const int width = (cu.kind == kGateUp ? a.D : a.I) / 32 - 16 * cs;  // blocks left
-    const uint8_t* bl = st + boff;
-    if (width >= 16) {
-      const uint32_t* wl = reinterpret_cast<const uint32_t*>(st);
-      bf16x8_t bop[4][4];
-#pragma unroll
-      for (int rnd = 0; rnd < 4; ++rnd)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) bop[rnd][i] = *reinterpret_cast<const bf16x8_t*>(bl + 64 * (4 * rnd + g) + 16 * i);
-      uint32_t wd[2][4][5];
-#pragma unroll
-      for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-        for (int rnd = 0; rnd < 4; ++rnd)
-#pragma unroll
-          for (int j = 0; j < 5; ++j) wd[mi][rnd][j] = wl[(16 * mi + rho) * kRowDw + 17 * rnd + 4 * g + j];
-#pragma unroll
-      for (int r0 = 0; r0 < 4; r0 += 2) {
-        bf16x8_t aop[2][2][4];
-#pragma unroll
-        for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-          for (int rr = 0; rr < 2; ++rr) decode_dwords(wd[mi][r0 + rr], g, qsel, aop[mi][rr]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int rr = 0; rr < 2; ++rr)
-#pragma unroll
-            for (int mi = 0; mi < 2; ++mi)
-              acc[mi][rr] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(aop[mi][rr][i], bop[r0 + rr][i], acc[mi][rr], 0, 0, 0);
+    const bool down = (d0 & 1) != 0, second = (d0 & 2) != 0;
+    const int rows = (d1 >> 10) & 3;
+    const int width = (d0 & 8) ? ((down ? nfg : nfu) & 15) : 16;
+
+    if (!second) {
+      const uint8_t* const ad = st + kWBytes;
+      const uint8_t *p0, *p1;
+      if (down) {
+        p0 = ad + hoff0, p1 = ad + hoff1;
+        bop.scale = *reinterpret_cast<const uint32_t*>(ad + kHDigits * kPlane + 4 * g) - hsub;
+      } else {
+        const int r = (rho & 4) && rows > 1 ? 1 : 0;
+        p0 = ad + r * kXRowLds + xoff0, p1 = ad + r * kXRowLds + xoff1;
+        bop.scale = *reinterpret_cast<const uint32_t*>(ad + kActBytes + 16 * r + 4 * g) - xsub;
       }
-    } else {
-      for (int rnd = 0; 4 * rnd < width; ++rnd) {
-        const int b = 4 * rnd + g;
-        bf16x8_t aop[2][4];
-        tail_round(st, rho, b, width, aop[0]);
-        tail_round(st + kMatBytes, rho, b, width, aop[1]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint4 q = *reinterpret_cast<const uint4*>(bl + 64 * b + 16 * i);
-          if (b >= width) q = make_uint4(0u, 0u, 0u, 0u);  // past K: whatever the buffer holds
-          const bf16x8_t bo = __builtin_bit_cast(bf16x8_t, q);
+      for (int rnd = 0; rnd < 4; ++rnd) {
+        bop.q[rnd][0] = *reinterpret_cast<const u32x4_t*>(p0 + 128 * rnd);
+        bop.q[rnd][1] = *reinterpret_cast<const u32x4_t*>(p1 + 128 * rnd);
+      }
+      if (width < 16) {  // blocks past K: whatever the buffer holds
 #pragma unroll
-          for (int mi = 0; mi < 2; ++mi)
-            acc[mi][0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(aop[mi][i], bo, acc[mi][0], 0, 0, 0);
+        for (int rnd = 0; rnd < 4; ++rnd) {
+          if (4 * rnd + (g >> 1) >= width) bop.q[rnd][0] = u32x4_t{0u, 0u, 0u, 0u};
+          if (4 * rnd + 2 + (g >> 1) >= width) bop.q[rnd][1] = u32x4_t{0u, 0u, 0u, 0u};
+          if (4 * rnd + g >= width) bop.scale = (bop.scale & ~(0xFFu << (8 * rnd))) | 127u << (8 * rnd);
         }
       }
     }
-
-    if (++cs == cst) {
-      // lane holds, in column rho, features 4g + v of both 16-row groups
-      f32x4_t sum[2];
+    // acc[0] takes this stage; in a gate/up unit w1's and w3's sums take turns
+    if (width == 16) stage_sums<false>(st, rho, g, width, bop, acc[0][0], acc[0][1]);
+    else stage_sums<true>(st, rho, g, width, bop, acc[0][0], acc[0][1]);
+    if (!down)
 #pragma unroll
       for (int mi = 0; mi < 2; ++mi) {
-        sum[mi] = acc[mi][0] + acc[mi][1];
-        acc[mi][0] = acc[mi][1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        const f32x4_t o = acc[0][mi];
+        acc[0][mi] = acc[1][mi];
+        acc[1][mi] = o;
       }
-      if (cu.kind == kGateUp) {
-        if (rho < cu.nrows) {
-          // feature 16 fg + 4g + v is element 16 (fg & 1) + 4g + v of I-block
-          // fg / 2, at its P-order position 8g + 2v + (fg & 1)
-          uint16_t* h = a.h + (int64_t)(cu.row0 + rho) * a.hstride + 32 * (cu.fg >> 1) + 8 * g + (cu.fg & 1);
+
+    if (d0 & 4) {
+      // lane holds, in column rho, features 4 g + v of each 16-row group
+      const int fg = d0 >> 8, row0 = d1 & 1023;
+      if (!down) {
+        float gt[8], up[8];  // feature 4 g + v of group i at 2 v + i: the digits' byte order
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const float gt = sum[0][v], up = sum[1][v];
-            const float hv = gt / (1.0f + expf(-gt)) * up;
-            const uint32_t hi = f32_to_bf16_bits(hv);
-            // no remainder of an infinity or a NaN
-            const float r1 = (hi & 0x7F80u) == 0x7F80u ? 0.0f : hv - __uint_as_float(hi << 16);
-            const uint32_t mid = f32_to_bf16_bits(r1);
-            const uint32_t lo = f32_to_bf16_bits(r1 - __uint_as_float(mid << 16));
-            store_dev(h + 2 * v, hi);
-            store_dev(h + a.hplane + 2 * v, mid);
-            store_dev(h + 2 * a.hplane + 2 * v, lo);
+            const float c = acc[0][i][v], u = acc[1][i][v];
+            gt[2 * v + i] = c + (__shfl_down(c, 1, 16) + (__shfl_down(c, 2, 16) + __shfl_down(c, 3, 16)));
+            up[2 * v + i] = u + (__shfl_down(u, 1, 16) + (__shfl_down(u, 2, 16) + __shfl_down(u, 3, 16)));
           }
+        float h[8];
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          h[i] = gt[i] / (1.0f + expf(-gt[i])) * up[i];
+          top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
         }
-        pub[0] = cu.tile;
+        top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+        top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+        if ((rho & 3) == 0 && (rho >> 2) < rows) {
+          const uint32_t e = digit_exp(top);
+          uint2 dg[kHDigits];
+          digits8<kHDigits>(h, e, dg);
+          uint8_t* const hb = a.h + (int64_t)(row0 + (rho >> 2)) * a.hstride + (fg >> 4) * kHRow;
+#pragma unroll
+          for (int p = 0; p < kHDigits; ++p) store_dev(hb + p * kPlane + digit_at(fg & 15, g, p), dg[p]);
+          if (g == 0)
+            __hip_atomic_store(hb + kHDigits * kPlane + 4 * (fg & 3) + ((fg & 15) >> 2), (uint8_t)(e - 3u), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+        }
+        pub[0] = d1 >> 16;
       } else {
+        f32x4_t sum[2];
 #pragma unroll
         for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            sum[mi][v] += __shfl_down(sum[mi][v], 1, 16) + __shfl_down(sum[mi][v], 2, 16);
+          for (int v = 0; v < 4; ++v) {
+            const float c = acc[0][mi][v];
+            sum[mi][v] = c + (__shfl_down(c, 1, 16) + (__shfl_down(c, 2, 16) + (__shfl_down(c, 3, 16) + __shfl_down(c, 4, 16))));
+          }
         if (rho == 0) {
-          float* y = a.y + (int64_t)cu.row0 * a.D + 32 * cu.fg + 4 * g;
+          float* y = a.y + (int64_t)row0 * a.D + 32 * fg + 4 * g;
           if (bad) sum[0][0] = sum[1][0] = __uint_as_float(0x7FC00000u);
 #pragma unroll
           for (int mi = 0; mi < 2; ++mi) store_dev(y + 16 * mi, sum[mi]);
         }
-        pub[0] = nrows + cu.fg;
+        pub[0] = nrows + fg;
       }
-      cst = 0;
+      acc[0][0] = acc[0][1] = acc[1][0] = acc[1][1] = zero;
     }
   }
 }
@@ -585,31 +760,32 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct LayerWorkspace {
-  size_t ids, w, xp, gt, rows, row_tok, slot_row, head, flags, h, y, total;
+  size_t ids, w, xd, xs, gt, rows, slot_row, head, flags, h, y, total;
   int64_t n, n_flags;
   int hstride;
 };
 LayerWorkspace layer_layout(int64_t T, int32_t D, int32_t I, int32_t k) {
   LayerWorkspace l{};
   size_t off = 0;
-  auto take = [&](size_t bytes) {
+  auto take = [&](size_t bytes) __attribute__((always_inline)) {
     const size_t at = off;
     off += align256(bytes);
     return at;
   };
+  const int nst13 = (D / 32 + 15) / 16, nst2 = (I / 32 + 15) / 16;
   l.n = T * k;
-  l.n_flags = l.n + D / 32;
-  l.hstride = (I + 127) / 128 * 128;  // rows start on 256-byte lines
+  l.n_flags = (l.n + D / 32) * kFlagStride;
+  l.hstride = (int)align256((size_t)nst2 * kHRow);
   l.ids = take(4 * l.n);
   l.w = take(4 * l.n);
-  l.xp = take((size_t)T * D * 2);
+  l.xd = take((size_t)T * nst13 * kXRow);
+  l.xs = take((size_t)T * nst13 * 16);
   l.gt = take(16 * l.n);
   l.rows = take(8 * l.n);
-  l.row_tok = take(4 * l.n);
   l.slot_row = take(4 * l.n);
   l.head = take(16);
   l.flags = take(4 * l.n_flags);
-  l.h = take((size_t)3 * l.n * l.hstride * 2);
+  l.h = take((size_t)l.n * l.hstride);
   l.y = take((size_t)l.n * D * 4);
   l.total = off;
   return l;
@@ -634,15 +810,15 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t s) {
   p.route_scale = c.route_scale;
   p.ids = c.ids ? c.ids : reinterpret_cast<int32_t*>(ws + l.ids);
   p.w = c.w ? c.w : reinterpret_cast<float*>(ws + l.w);
-  p.xp = reinterpret_cast<uint16_t*>(ws + l.xp);
+  p.xd = ws + l.xd;
+  p.xs = ws + l.xs;
   p.gt = reinterpret_cast<int4*>(ws + l.gt);
   p.rows = reinterpret_cast<int2*>(ws + l.rows);
-  p.row_tok = reinterpret_cast<int32_t*>(ws + l.row_tok);
   p.slot_row = reinterpret_cast<int32_t*>(ws + l.slot_row);
   p.head = reinterpret_cast<int32_t*>(ws + l.head);
   p.flags = reinterpret_cast<uint32_t*>(ws + l.flags);
   p.n_flags = (int)l.n_flags;
-  const unsigned blocks = 1 + (unsigned)(((int64_t)c.T * c.D / 8 + kPlanThreads - 1) / kPlanThreads);
+  const unsigned blocks = 1 + (unsigned)((c.T * (c.D / 8) + kPlanThreads - 1) / kPlanThreads);
   const dim3 grid(blocks), block(kPlanThreads);
   if (c.E <= 64) hipLaunchKernelGGL(layer_plan_kernel<1>, grid, block, 0, s, p);
   else if (c.E <= 128) hipLaunchKernelGGL(layer_plan_kernel<2>, grid, block, 0, s, p);
@@ -655,11 +831,12 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t s) {
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(layer_plan_kernel<0>, grid, block, 0, s, p);
   }
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
 
   LayerArgs a{};
-  a.xp = p.xp;
+  a.xd = p.xd;
+  a.xs = p.xs;
   a.w1 = c.w1;
   a.w3 = c.w3;
   a.w2 = c.w2;
@@ -669,17 +846,15 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t s) {
   a.k = c.k;
   a.gt = p.gt;
   a.rows = p.rows;
-  a.row_tok = p.row_tok;
   a.slot_row = p.slot_row;
   a.w = p.w;
   a.head = p.head;
   a.flags = p.flags;
-  a.h = reinterpret_cast<uint16_t*>(ws + l.h);
-  a.hplane = l.n * l.hstride;
+  a.h = ws + l.h;
   a.hstride = l.hstride;
   a.y = reinterpret_cast<float*>(ws + l.y);
   a.out = c.out;
-  const int64_t units = l.n * (c.I / 16 + c.D / 32) + c.D / 32;
+  const int64_t units = l.n * (c.I / 32 + c.D / 32) + c.D / 32;
   int64_t wgs = (units + kWaves - 1) / kWaves;
   const int cus = device_cu_count();
   if (wgs > cus) wgs = cus;

@@ -3,13 +3,17 @@ oracle, element by element.
 
 Bound, with u = 2^-24 (half a step of fp32), every product summed in some order
 in fp32: a sum of n products is off by at most n u times the sum of their
-magnitudes, so for one expert
-  |dg| <= (D + 1) u (|W1| |x|),  |du| <= (D + 1) u (|W3| |x|)
+magnitudes.  x enters as four base-32 digits relative to its 32-block: with
+8 * 2^s <= max |x| the last digit's half step is 2^s * 32^-3 / 2 <= 2^-19 max |x|
+of the block; h as five, 2^-24 max |h|.  The digits' magnitudes add up to at most
+the value's plus one step of each (|d0| <= |q| + 1/2, later ones below 1/32 of
+the step before), so the sums' magnitudes are taken as |v| + 2^-3 blockmax / 2.
+For one expert, X = |x| + blockmax(x) / 16 (H likewise):
+  |dg| <= (D + 8) u (|W1| X) + 2^-19 |W1| blockmax(x),  |du| likewise with W3
   h = silu(g) up: |silu'| <= 1.1, and exp, add, divide and two products are
   good to 4 u together with the argument's rounding (2 u |g|, |silu'| again):
   |dh| <= 1.1 |dg| |up| + |silu(g)| |du| + 1.1 |dg| |du| + (8 + 4 |g|) u |h|
-  three bf16 parts: 2^-24 |h| more
-  |dy| <= |W2| |dh| + (3 I + 4) u |W2| |h|
+  |dy| <= |W2| |dh| + (I + 8) u |W2| H + 2^-24 |W2| blockmax(h)
 and the k weighted outputs add (k + 2) u sum |w y| (weights rounded once).
 """
 
@@ -30,6 +34,11 @@ U = 2.0**-24
 BASE = moe_inputs.TINY
 
 
+def blockmax(v):
+    """The largest magnitude of each 32-block, repeated over the block."""
+    return np.repeat(np.abs(v).reshape(v.shape[0], -1, 32).max(-1), 32, axis=1)
+
+
 def layer_ref(x_bits, ids, w, experts):
     """fp64 result and the error bound above."""
     x = bf16_bits_to_f64(x_bits)
@@ -40,14 +49,14 @@ def layer_ref(x_bits, ids, w, experts):
         t, j = np.nonzero(ids == e)
         w1, w3, w2 = (decode_ct(*m) for m in experts[int(e)])
         I = w1.shape[0]
-        xe = x[t]
+        xe, xm = x[t], blockmax(x[t])
         g, up = xe @ w1.T, xe @ w3.T
         silu = g / (1 + np.exp(-g))
         h = silu * up
-        dg, du = (D + 1) * U * (np.abs(xe) @ np.abs(w1).T), (D + 1) * U * (np.abs(xe) @ np.abs(w3).T)
-        dh = 1.1 * dg * np.abs(up) + np.abs(silu) * du + 1.1 * dg * du + (9 + 4 * np.abs(g)) * U * np.abs(h)
-        y = h @ w2.T
-        dy = dh @ np.abs(w2).T + (3 * I + 4) * U * (np.abs(h) @ np.abs(w2).T)
+        dg, du = ((D + 8) * U * ((np.abs(xe) + xm / 16) @ np.abs(m).T) + 2.0**-19 * (xm @ np.abs(m).T) for m in (w1, w3))
+        dh = 1.1 * dg * np.abs(up) + np.abs(silu) * du + 1.1 * dg * du + (8 + 4 * np.abs(g)) * U * np.abs(h)
+        y, hm = h @ w2.T, blockmax(np.abs(h) + dh)
+        dy = dh @ np.abs(w2).T + (I + 8) * U * ((np.abs(h) + hm / 16) @ np.abs(w2).T) + 2.0**-24 * (hm @ np.abs(w2).T)
         we = w[t, j].astype(np.float64)[:, None]
         np.add.at(out, t, we * y)
         np.add.at(bound, t, np.abs(we) * dy)
