@@ -37,8 +37,10 @@
 // already running and that waits for still lower ones only: by induction every
 // wait ends, however many of the workgroups are resident and whatever else
 // the device runs.  (The wait loops are bounded all the same; a wait that ran
-// out would give NaN outputs.)  A wave never waits with an unfinished unit in
-// its ring: a down unit that is not ready is held back until the ring is empty.
+// out would give NaN outputs.)  A wave waits only with its earlier units
+// finished: the weights of a down unit go into the ring whether its h is
+// complete or not, its h follows when a look at the tile's count allows it, and
+// if the unit's first stage comes up without, the wave waits then.
 //
 // Visibility.  Results (digits of h, y) are written with device-scope stores,
 // which go through the XCD's L2, and counted (device-scope add, no return) once
@@ -120,8 +122,9 @@ struct LayerPlan {
   float* w;        // [T, k]
   uint8_t* xd;     // [T][stages][kXRow] digits of x
   uint8_t* xs;     // [T][stages][16] their scale bytes
-  int4* gt;        // gate/up tiles: expert, first row, rows, tokens of the rows (a byte each)
-  int2* rows;      // grouped rows: expert, gate/up tile
+  int4* gt;        // gate/up tiles: expert, first row | rows << 16, tokens of the rows (a byte each), expert's tiles
+                   // (first | count << 16)
+  int4* rows;      // grouped rows: expert, expert's rows (first | count << 16), expert's first gate/up tile
   int32_t* slot_row;
   int32_t* head;   // [0] gate/up tiles, [1] next ticket
   uint32_t* flags;
@@ -155,7 +158,7 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
     return;
   }
   __shared__ uint32_t s_mask[K3MOE_MAX_EXPERTS_FFN];  // tokens of each expert
-  __shared__ uint32_t s_base[K3MOE_MAX_EXPERTS_FFN];  // first row | first gate/up tile << 16
+  __shared__ uint32_t s_base[K3MOE_MAX_EXPERTS_FFN];  // first row
   __shared__ int s_ids[K3MOE_MAX_LAYER_TOKENS * K3MOE_MAX_TOPK];
   __shared__ int s_sum[kPlanThreads / 64][2];
   const int lane = tid & 63, wave = tid >> 6;
@@ -207,15 +210,18 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
   for (int e = tid * per; e < min((tid + 1) * per, p.E); ++e) {
     const int m = __popc(s_mask[e]);
     if (m == 0) continue;
-    s_base[e] = (uint32_t)at[0] | (uint32_t)at[1] << 16;
+    s_base[e] = (uint32_t)at[0];
     uint32_t toks = s_mask[e];
+    const int t0 = at[1], nt = (m + kGuTileRows - 1) / kGuTileRows;
+    for (int r = 0; r < m; ++r) p.rows[at[0] + r] = make_int4(e, at[0] | m << 16, t0, 0);
     for (int r = 0; r < m; r += kGuTileRows) {
       int tk = 0;
-      for (int i = 0; i < min(kGuTileRows, m - r); ++i) {
+      const int nr = min(kGuTileRows, m - r);
+      for (int i = 0; i < nr; ++i) {
         tk |= __builtin_ctz(toks) << (8 * i);
         toks &= toks - 1u;
       }
-      p.gt[at[1]++] = make_int4(e, at[0] + r, min(kGuTileRows, m - r), tk);
+      p.gt[at[1]++] = make_int4(e, (at[0] + r) | nr << 16, tk, t0 | nt << 16);
     }
     at[0] += m;
   }
@@ -223,10 +229,7 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
   if (tid < n) {
     const int e = s_ids[tid], t = tid / p.k;
     const int rank = __popc(s_mask[e] & ((1u << t) - 1u));
-    const uint32_t b = s_base[e];
-    const int row = (int)(b & 0xFFFFu) + rank;
-    p.slot_row[tid] = row;
-    p.rows[row] = make_int2(e, (int)(b >> 16) + rank / kGuTileRows);
+    p.slot_row[tid] = (int)s_base[e] + rank;
   }
   if (tid == 0) {
     p.head[0] = tiles;
@@ -262,7 +265,7 @@ struct LayerArgs {
   const uint8_t *w1, *w3, *w2;
   int D, I, T, k;
   const int4* gt;
-  const int2* rows;
+  const int4* rows;
   const int32_t* slot_row;
   const float* w;
   int32_t* head;
@@ -273,8 +276,10 @@ struct LayerArgs {
   float* out;       // [T, D]
 };
 
+// A unit of work. row: first row of the tile (gate/up) or the row (down); rows:
+// its rows; tile: gate/up tile; toks: its tokens, a byte each.
 struct Unit {
-  int kind, fg, expert, row0, nrows, tile, toks;
+  int kind, fg, expert, row, rows, tile, toks;
 };
 
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
@@ -353,6 +358,7 @@ __device__ __forceinline__ void stage_sums(const uint8_t* st, int rho, int g, in
 
 __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves][kRing][kStageBytes];
+  __shared__ int fifo[kWaves][4][4];  // units in the ring: kind | late << 1 | fg << 2, row | rows << 16, tile
   __shared__ unsigned long long s_pool;
 
   const int lane = threadIdx.x & 63;
@@ -362,28 +368,32 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   const int nfg = a.I >> 5, nfu = a.D >> 5;
   const int n_gt = *as_const(a.head);
   const int n_gu = n_gt * nfg, n_dn = nrows * nfu;
-  const uint32_t grp13 = (uint32_t)nfu * 272, grp2 = (uint32_t)nfg * 272;  // bytes of a 16-row group
   const int nst13 = (nfu + 15) >> 4, nst2 = (nfg + 15) >> 4;
   const float rcp_fg = 1.0f / (float)nfg, rcp_fu = 1.0f / (float)nfu;
 
-  // n / d for 0 <= n < 2^23 by its reciprocal r (one step off at most)
-  auto div = [](int n, int d, float r) {
+  // n / d for 0 <= n < 2^23 by d's reciprocal r (one step off at most)
+  auto div = [](int n, int d, float r) __attribute__((always_inline)) {
     int q = (int)((float)n * r);
     q -= q * d > n ? 1 : 0;
     q += (q + 1) * d <= n ? 1 : 0;
-    return q;
+    return uni(q);
   };
+  // Units of one expert are neighbours, its tiles (rows) fastest: what reads
+  // the same weights runs at the same time, mostly in one workgroup.
   auto unit_of = [&](int t) __attribute__((always_inline)) -> Unit {
     if (t < n_gu) {
-      const int i = uni(div(t, nfg, rcp_fg));
-      const auto q = as_const(reinterpret_cast<const int32_t*>(a.gt)) + 4 * i;
-      return Unit{kGateUp, t - i * nfg, q[0], q[1], q[2], i, q[3]};
+      const auto p = as_const(reinterpret_cast<const int32_t*>(a.gt));
+      const int first = p[4 * div(t, nfg, rcp_fg) + 3];
+      const int t0 = first & 0xFFFF, nt = first >> 16;
+      const int in = t - t0 * nfg, fg = nt == 1 ? in : div(in, nt, 1.0f / (float)nt), i = t0 + in - fg * nt;
+      return Unit{kGateUp, fg, p[4 * i], p[4 * i + 1] & 0xFFFF, p[4 * i + 1] >> 16, i, p[4 * i + 2]};
     }
     t -= n_gu;
     if (t < n_dn) {
-      const int r = uni(div(t, nfu, rcp_fu));
-      const auto q = as_const(reinterpret_cast<const int32_t*>(a.rows)) + 2 * r;
-      return Unit{kDown, t - r * nfu, q[0], r, 1, q[1], 0};
+      const auto q = as_const(reinterpret_cast<const int32_t*>(a.rows)) + 4 * div(t, nfu, rcp_fu);
+      const int r0 = q[1] & 0xFFFF, nr = q[1] >> 16;
+      const int in = t - r0 * nfu, fu = nr == 1 ? in : div(in, nr, 1.0f / (float)nr), r = in - fu * nr;
+      return Unit{kDown, fu, q[0], r0 + r, 1, q[2] + r / kGuTileRows, 0};
     }
     t -= n_dn;
     return Unit{t < nfu ? kSum : kNone, t, 0, 0, 0, 0, 0};
@@ -420,130 +430,144 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
       }
     return uni(v);
   };
-  Unit iu = unit_of(claim());  // the unit being issued, or the next one
-  Unit nu{kNone, 0, 0, 0, 0, 0, 0};  // the one after it, drawn while iu's loads go out
-  bool drawn = true;
 
-  // Chunk c = 64 j + lane of a stage: byte 16 c of the first group's run, then
-  // of the second group's, `grp` bytes on in the matrix.
-  uint32_t woff[kW];
+  // Weight load j takes chunks 64 j + lane of a stage: byte 16 c of the first
+  // group's run up to chunk 271, then of the second group's, a group on in the
+  // matrix.  The instruction's own offset counts for the LDS address, too, so
+  // loads 0-3, 4-7 and 8 share a base each, and their lane offsets are
+  const int lane16 = 16 * lane;  // 0-3
+  int wofs4 = 0, wofs5 = 0;      // 4; 5-8
   const bool wlast = lane < kChunks - 64 * (kW - 1);
-  const __amdgpu_buffer_rsrc_t xr =
-      __builtin_amdgcn_make_buffer_rsrc((void*)a.xd, 0, a.T * nst13 * kXRow, 0x00020000);
-  const __amdgpu_buffer_rsrc_t xsr = __builtin_amdgcn_make_buffer_rsrc((void*)a.xs, 0, a.T * nst13 * 16, 0x00020000);
-  const __amdgpu_buffer_rsrc_t hr = __builtin_amdgcn_make_buffer_rsrc((void*)a.h, 0, nrows * a.hstride, 0x00020000);
+  static_assert(kW == 9, "three bases");
 
   // ---- issue side.  A stage is the same 512 columns of two neighbouring 16-row
   // groups of one matrix: of w2 (down), or of w1 and then of w3 (gate/up), where
   // the digits of x travel with w1.
-  const uint8_t *wb0 = nullptr, *wb1 = nullptr;  // first group of w1 and w3, or of w2
-  uint32_t grp = 0;         // bytes of a 16-row group of iu's matrix
-  uint32_t wso = 0;         // byte of the stage in it
-  int act0 = 0, act1 = 0;   // byte offsets of the stage's activations: rows of x, or (act0) the row of h
-  uint32_t sco = 0;         // per lane: scale bytes of tile row `lane`
-  int left = 0;             // stages of iu not yet issued (0: iu's loads have not begun)
-  bool bad = false;         // a bounded wait ran out
-  bool all_done = false;    // every gate/up unit has been seen counted
-  bool waited = false;      // iu's tile has been waited for
+  Unit iu = unit_of(claim());        // the unit being issued, or the next one
+  Unit nu{kNone, 0, 0, 0, 0, 0, 0};  // the one after it, drawn while iu's loads go out
+  bool drawn = true;
+  const uint8_t *wb0 = nullptr, *wb1 = nullptr;  // the next stage's weights; gate/up: and those of the stage after it
+  int grp2x = 0;             // bytes of a stage's two whole groups, less what lies before the stage
+  int act0 = 0, act1 = 0;    // where the stage's activations are: rows of x, or (act0) the row of h
+  int sco = 0;               // per lane: scale bytes of tile row `lane`
+  int left = 0;              // stages of iu not yet issued (0: iu's loads have not begun)
+  int inflight = 0, buf_i = 0, pushed = 0;
+  bool bad = false;          // a bounded wait ran out
+  bool all_done = false;     // every gate/up unit has been seen counted
+  bool has_h = false;        // iu is a down unit whose h is complete
 
-  auto prep = [&]() __attribute__((always_inline)) {
-    // (plain values first, assigned once: the compiler would merge assignments
-    // at the ends of two branches into one through memory)
-    const bool gu = iu.kind == kGateUp;
-    const uint32_t gb = gu ? grp13 : grp2;
-    const size_t off = ((size_t)iu.expert * (size_t)(2 * (gu ? nfg : nfu)) + (size_t)(2 * iu.fg)) * gb;
-    const int t0 = iu.toks & 255, t1 = (iu.toks >> 8) & 255;
-    wb0 = (gu ? a.w1 : a.w2) + off;
-    wb1 = a.w3 + off;
-    grp = gb;
-#pragma unroll
-    for (int j = 0; j < kW; ++j) {
-      const int c = 64 * j + lane;
-      woff[j] = c < kChunks / 2 ? 16u * (uint32_t)c : gb + 16u * (uint32_t)(c - kChunks / 2);
-    }
-    left = gu ? 2 * nst13 : nst2;
-    act0 = uni(gu ? t0 * nst13 * kXRow : iu.row0 * a.hstride);
-    act1 = uni(t1 * nst13 * kXRow);
-    sco = (uint32_t)((lane == 1 ? t1 : t0) * nst13) * 16;
-    wso = 0;
-    drawn = false;
-    waited = false;
+  auto seen = [&](int f) __attribute__((always_inline)) -> uint32_t {
+    return (uint32_t)uni((int)__hip_atomic_load(a.flags + f * kFlagStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
   };
-  // What a stage in flight is: bit 0 kind, 1 w3, 2 last stage of its
-  // unit, 3 shorter stage; bits 4.. its activation loads, 8.. its features;
-  // and row0 | rows << 10 | tile << 16.
-  int sd0[kRing] = {0, 0, 0}, sd1[kRing] = {0, 0, 0};
-  int inflight = 0;
-  auto load_x = [&](uint8_t* dst, int so) __attribute__((always_inline)) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (__attribute__((address_space(3))) void*)(uintptr_t)dst, 16, 16 * lane, so, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(xr, (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 1024), 16, 16 * lane,
-                                             so + 1024, 0, 0);
-  };
-  auto issue = [&](int buf) __attribute__((always_inline)) {
-    uint8_t* const dst = &lds[wave][buf][0];
-    uint8_t* const ad = dst + kWBytes;
-    const bool gu = iu.kind == kGateUp;
-    const bool half = gu && (left & 1) != 0;  // an even number of stages: w3 at the odd ones
-    const __amdgpu_buffer_rsrc_t wr =
-        __builtin_amdgcn_make_buffer_rsrc((void*)(half ? wb1 : wb0), 0, (int)(2 * grp), 0x00020000);
-#pragma unroll
-    for (int j = 0; j < kW - 1; ++j) {
-      const uint32_t vo = woff[j];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 1024 * j), 16, vo, wso,
-                                               0, kNt);
-    }
-    if (wlast) {
-      const uint32_t vo = woff[kW - 1];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          wr, (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 1024 * (kW - 1)), 16, vo, wso, 0, kNt);
-    }
-    const bool tail = wso + kMatBytes > grp;
-    const int d0 = (gu ? 0 : 1) | (half ? 2 : 0) | (left == 1 ? 4 : 0) | (tail ? 8 : 0) |
-                   (half ? 0 : gu ? 2 * iu.nrows + 1 : 3) << 4 | iu.fg << 8;
-    const int d1 = iu.row0 | iu.nrows << 10 | iu.tile << 16;
-    if (!gu) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(hr, (__attribute__((address_space(3))) void*)(uintptr_t)ad, 16, 16 * lane, act0, 0,
-                                               kDevScope);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(hr, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + 1024), 16, 16 * lane,
-                                               act0 + 1024, 0, kDevScope);
-      if (lane < (kHRow - 2048) / 16)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(hr, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + 2048), 16, 16 * lane,
-                                                 act0 + 2048, 0, kDevScope);
-    } else if (!half) {
-      load_x(ad, act0);
-      if (iu.nrows > 1) load_x(ad + kXRowLds, act1);
-      if (lane < iu.nrows)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(xsr, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + kActBytes), 16, sco, 0,
-                                                 0, 0);
-    }
-    act0 += gu ? (half ? 0 : kXRow) : kHRow;
-    act1 += half ? 0 : kXRow;
-    sco += half ? 0u : 16u;
-    wso += gu && !half ? 0u : kMatBytes;
-    sd0[2] = inflight == 2 ? d0 : sd0[2], sd1[2] = inflight == 2 ? d1 : sd1[2];
-    sd0[1] = inflight == 1 ? d0 : sd0[1], sd1[1] = inflight == 1 ? d1 : sd1[1];
-    sd0[0] = inflight == 0 ? d0 : sd0[0], sd1[0] = inflight == 0 ? d1 : sd1[0];
-    ++inflight;
-    if (--left == 0) {
-      if (!drawn) nu = unit_of(claim());
-      drawn = true;
-      iu = nu;
-    }
-  };
-  auto seen = [&](const uint32_t* f) __attribute__((always_inline)) -> uint32_t {
-    return (uint32_t)uni((int)__hip_atomic_load(f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-  };
-  // whether iu can be issued now (no waiting)
-  auto ready = [&]() __attribute__((always_inline)) -> bool {
-    if (iu.kind == kGateUp) return true;
-    if (iu.kind != kDown) return false;
-    if (all_done || waited) return true;
-    if (seen(a.flags + iu.tile * kFlagStride) < (uint32_t)nfg) return false;
-    bool all = true;  // look whether that was the last check this wave needs
+  // whether the down unit iu has its h (no waiting)
+  auto look = [&]() __attribute__((always_inline)) -> bool {
+    if (all_done) return true;
+    if (seen(iu.tile) < (uint32_t)nfg) return false;
+    bool all = true;  // whether that was the last look this wave needs
     for (int i = lane; i < n_gt; i += 64)
       all = all && __hip_atomic_load(a.flags + i * kFlagStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= (uint32_t)nfg;
     all_done = __all(all);
     return true;
+  };
+  auto wait_for = [&](int f, uint32_t need) __attribute__((always_inline)) {
+    int spins = 0;
+    while (seen(f) < need) {
+      __builtin_amdgcn_s_sleep(2);
+      if (++spins > kSpinLimit) {
+        bad = true;
+        break;
+      }
+    }
+  };
+  auto prep = [&]() __attribute__((always_inline)) {
+    // (plain values first, assigned once: the compiler would merge assignments
+    // at the ends of two branches into one through memory)
+    const bool gu = iu.kind == kGateUp;
+    const int gb = (gu ? nfu : nfg) * 272;  // bytes of a 16-row group
+    const size_t off = ((size_t)iu.expert * (size_t)(2 * (gu ? nfg : nfu)) + (size_t)(2 * iu.fg)) * (size_t)gb;
+    const int t0 = iu.toks & 255, t1 = (iu.toks >> 8) & 255;
+    wb0 = (gu ? a.w1 : a.w2) + off;
+    wb1 = a.w3 + off;
+    grp2x = 2 * gb;
+    wofs5 = gb + lane16 - 256;
+    wofs4 = lane < 16 ? 4096 + lane16 : wofs5;
+    left = gu ? 2 * nst13 : nst2;
+    act0 = gu ? t0 * nst13 * kXRow : iu.row * a.hstride;
+    act1 = t1 * nst13 * kXRow;
+    sco = (lane == 1 ? t1 : t0) * nst13 * 16;
+    has_h = gu || look();
+    int* const f = fifo[wave][pushed & 3];
+    ++pushed;
+    if (lane == 0) {
+      f[0] = iu.kind | (has_h ? 0 : 2) | iu.fg << 2;
+      f[1] = iu.row | iu.rows << 16;
+      f[2] = iu.tile;
+    }
+    drawn = false;
+  };
+  auto load_h = [&](uint8_t* dst, int at) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.h, 0, nrows * a.hstride, 0x00020000);
+    const int so = uni(at);
+    const auto l = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, kDevScope);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, kDevScope);
+    if (lane < (kHRow - 2048) / 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 2048, kDevScope);
+  };
+  auto load_x = [&](uint8_t* dst, int at) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xd, 0, a.T * nst13 * kXRow, 0x00020000);
+    const int so = uni(at);
+    const auto l = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, 0);
+  };
+  // the next stage of iu into the ring
+  auto issue = [&]() __attribute__((always_inline)) {
+    uint8_t* const dst = &lds[wave][buf_i][0];
+    uint8_t* const ad = dst + kWBytes;
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)wb0, 0, grp2x, 0x00020000);
+    const auto l0 = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
+    const auto l4 = (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 4096);
+    const auto l8 = (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 8192);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l0, 16, lane16, 0, 0, kNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l0, 16, lane16, 0, 1024, kNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l0, 16, lane16, 0, 2048, kNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l0, 16, lane16, 0, 3072, kNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs4, 0, 0, kNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs5, 0, 1024, kNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs5, 0, 2048, kNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs5, 0, 3072, kNt);
+    if (wlast) __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l8, 16, wofs5, 4096, 0, kNt);
+    --left;
+    if (iu.kind == kGateUp) {
+      if (left & 1) {  // w1 (an even number of stages, w1 and w3 by turns)
+        load_x(ad, act0);
+        act0 += kXRow;
+        if (iu.rows > 1) {
+          load_x(ad + kXRowLds, act1);
+          act1 += kXRow;
+        }
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xs, 0, a.T * nst13 * 16, 0x00020000);
+        if (lane < iu.rows)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + kActBytes), 16, sco, 0, 0, 0);
+        sco += 16;
+      }
+      const uint8_t* const next = wb0 + kMatBytes;  // of the same matrix, two stages on
+      wb0 = wb1;
+      wb1 = next;
+      grp2x -= (left & 1) ? 0 : kMatBytes;
+    } else {
+      if (has_h) load_h(ad, act0);
+      act0 += kHRow;
+      wb0 += kMatBytes;
+      grp2x -= kMatBytes;
+    }
+    ++inflight;
+    buf_i = buf_i == kRing - 1 ? 0 : buf_i + 1;
+    if (left == 0) {
+      if (!drawn) nu = unit_of(claim());
+      drawn = true;
+      iu = nu;
+    }
   };
 
   // ---- publishing
@@ -571,188 +595,181 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   const int hoff0 = hp * kPlane + 16 * (g ^ hp), hoff1 = hp * kPlane + 16 * ((4 + g) ^ hp);
   const uint32_t xsub = 0x05050505u * (uint32_t)xp, hsub = 0x05050505u * (uint32_t)hp;
 
-  int buf_i = 0, buf_c = 0;
+  int buf_c = 0, popped = 0;
   for (;;) {
-    while (inflight < kRing) {
-      if (left == 0) {
-        if (!ready()) break;
-        prep();
-      }
-      issue(buf_i);
-      buf_i = buf_i == kRing - 1 ? 0 : buf_i + 1;
+    while (inflight < kRing && iu.kind < kSum) {
+      if (left == 0) prep();
+      issue();
     }
-    if (inflight == 0) {
-      // the ring is empty and iu cannot start: count what is finished, then wait
+    if (inflight == 0) break;
+    // ---- one unit
+    const int* const f = fifo[wave][popped & 3];
+    ++popped;
+    const int f0 = uni(f[0]), f1 = uni(f[1]), tile = uni(f[2]);
+    const bool down = (f0 & 1) != 0;
+    const int row = f1 & 0xFFFF, rows = f1 >> 16, fg = f0 >> 2;
+    const int nst = down ? nst2 : 2 * nst13;
+    const int cut = (down ? nfg : nfu) & 15;  // blocks of a last, shorter stage (0: none)
+    // column rho's tile row (gate/up) and this lane's operand pieces
+    const int r = !down && rows > 1 && (rho & 4) ? kXRowLds : 0;
+    const int off0 = kWBytes + r + (down ? hoff0 : xoff0), off1 = kWBytes + r + (down ? hoff1 : xoff1);
+    const int offs = kWBytes + 4 * g + (down ? kHDigits * kPlane : kActBytes + (r ? 16 : 0));
+    const uint32_t sub = down ? hsub : xsub;
+    if (f0 & 2) {
+      // The unit's weights went ahead of its h.  Every earlier unit of this
+      // wave is finished: count them, wait for the tile, load h for the stages
+      // that are in the ring.
       flush();
-      if (iu.kind == kNone) break;
-      const uint32_t* f = a.flags + (iu.kind == kDown ? iu.tile : nrows + iu.fg) * kFlagStride;
-      const uint32_t need = iu.kind == kDown ? (uint32_t)nfg : (uint32_t)nrows;
-      int spins = 0;
-      while (seen(f) < need) {
-        __builtin_amdgcn_s_sleep(2);
-        if (++spins > kSpinLimit) {
-          bad = true;
-          break;
-        }
-      }
-      if (iu.kind == kSum) {
-        // eight lanes a token (four features each), eight tokens and 16 slots at a time
-        const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc((void*)a.y, 0, nrows * a.D * 4, 0x00020000);
-        const uint32_t f4 = (uint32_t)(32 * iu.fg + 4 * (lane & 7));
-        for (int t = lane >> 3; t < a.T; t += 8) {
-          f32x4_t sum = zero;
-          for (int j0 = 0; j0 < a.k; j0 += 16) {
-            uint32_t at[16];
-            float wt[16];
-            u32x4_t v[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int q = t * a.k + min(j0 + j, a.k - 1);
-              at[j] = (uint32_t)a.slot_row[q] * (uint32_t)a.D * 4 + 4 * f4;
-              wt[j] = a.w[q];
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = __builtin_amdgcn_raw_buffer_load_b128(yr, at[j], 0, kDevScope);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (j0 + j < a.k)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  const uint32_t bits = v[j][c];
-                  sum[c] = fmaf(wt[j], __uint_as_float(bits), sum[c]);
-                }
-          }
-          if (bad) sum[0] = sum[1] = sum[2] = sum[3] = __uint_as_float(0x7FC00000u);
-          *reinterpret_cast<f32x4_t*>(a.out + (int64_t)t * a.D + f4) = sum;
-        }
-        iu = unit_of(claim());
-      } else {
-        waited = true;
-      }
-      continue;
-    }
-
-    if (!drawn && inflight == kRing) {  // with the ring full
-      nu = unit_of(claim());
-      drawn = true;
-    }
-    // the oldest stage has landed once only the loads of the newer ones are out
-    // (activation loads of a stage: 0, 3 or 5, so these counts are exact but at
-    // a change of kind, where they wait for a little more)
-    if (inflight == 3) {
-      const int n = ((sd0[1] >> 4) & 15) + ((sd0[2] >> 4) & 15);
-      if (n >= 6) wait_vm<2 * kW + 6>();
-      else if (n >= 5) wait_vm<2 * kW + 5>();
-      else if (n >= 3) wait_vm<2 * kW + 3>();
-      else wait_vm<2 * kW>();
-    } else if (inflight == 2) {
-      wait_vm<kW>();
-    } else {
+      wait_for(tile, (uint32_t)nfg);
+      for (int j = 0, b = buf_c; j < inflight && j < nst; ++j, b = b == kRing - 1 ? 0 : b + 1)
+        load_h(&lds[wave][b][0] + kWBytes, row * a.hstride + j * kHRow);
       wait_vm<0>();
+      if (left > 0 && inflight < nst) has_h = true;  // iu is this unit
     }
-    // a unit finished three stages ago: its stores are older than these loads
-    publish(pub[2]);
-    pub[2] = pub[1];
-    pub[1] = pub[0];
-    pub[0] = -1;
-    const int d0 = sd0[0], d1 = sd1[0];
-    sd0[0] = sd0[1], sd1[0] = sd1[1];
-    sd0[1] = sd0[2], sd1[1] = sd1[2];
-    const uint8_t* const st = &lds[wave][buf_c][0];
-    buf_c = buf_c == kRing - 1 ? 0 : buf_c + 1;
-    --inflight;
-    const bool down = (d0 & 1) != 0, second = (d0 & 2) != 0;
-    const int rows = (d1 >> 10) & 3;
-    const int width = (d0 & 8) ? ((down ? nfg : nfu) & 15) : 16;
-
-    if (!second) {
-      const uint8_t* const ad = st + kWBytes;
-      const uint8_t *p0, *p1;
-      if (down) {
-        p0 = ad + hoff0, p1 = ad + hoff1;
-        bop.scale = *reinterpret_cast<const uint32_t*>(ad + kHDigits * kPlane + 4 * g) - hsub;
+    for (int s = 0; s < nst; ++s) {
+      if (inflight < kRing && iu.kind < kSum) {
+        if (left == 0) prep();
+        issue();
+      }
+      if (!drawn && left > 0) {  // with the ring full
+        nu = unit_of(claim());
+        drawn = true;
+      }
+      // The oldest stage has landed once only the loads of the newer ones are
+      // out: their weights and, within a unit, activations (gate/up: of one of
+      // two neighbouring stages; down: of both).  Fewer are assumed where that
+      // is not sure, which waits for a little more.
+      if (inflight < kRing) {
+        if (inflight == 2) wait_vm<kW>();
+        else wait_vm<0>();
+      } else if (s + 2 >= nst) {
+        wait_vm<2 * kW>();
+      } else if (!down) {
+        wait_vm<2 * kW + 3>();
       } else {
-        const int r = (rho & 4) && rows > 1 ? 1 : 0;
-        p0 = ad + r * kXRowLds + xoff0, p1 = ad + r * kXRowLds + xoff1;
-        bop.scale = *reinterpret_cast<const uint32_t*>(ad + kActBytes + 16 * r + 4 * g) - xsub;
+        wait_vm<2 * kW + 6>();
       }
-#pragma unroll
-      for (int rnd = 0; rnd < 4; ++rnd) {
-        bop.q[rnd][0] = *reinterpret_cast<const u32x4_t*>(p0 + 128 * rnd);
-        bop.q[rnd][1] = *reinterpret_cast<const u32x4_t*>(p1 + 128 * rnd);
-      }
-      if (width < 16) {  // blocks past K: whatever the buffer holds
+      // a unit finished three stages ago: its stores are older than these loads
+      publish(pub[2]);
+      pub[2] = pub[1];
+      pub[1] = pub[0];
+      pub[0] = -1;
+      const uint8_t* const st = &lds[wave][buf_c][0];
+      buf_c = buf_c == kRing - 1 ? 0 : buf_c + 1;
+      --inflight;
+      const int width = cut != 0 && (down ? s == nst - 1 : s >= nst - 2) ? cut : 16;
+      if (down || (s & 1) == 0) {
+        bop.scale = *reinterpret_cast<const uint32_t*>(st + offs) - sub;
 #pragma unroll
         for (int rnd = 0; rnd < 4; ++rnd) {
-          if (4 * rnd + (g >> 1) >= width) bop.q[rnd][0] = u32x4_t{0u, 0u, 0u, 0u};
-          if (4 * rnd + 2 + (g >> 1) >= width) bop.q[rnd][1] = u32x4_t{0u, 0u, 0u, 0u};
-          if (4 * rnd + g >= width) bop.scale = (bop.scale & ~(0xFFu << (8 * rnd))) | 127u << (8 * rnd);
+          bop.q[rnd][0] = *reinterpret_cast<const u32x4_t*>(st + off0 + 128 * rnd);
+          bop.q[rnd][1] = *reinterpret_cast<const u32x4_t*>(st + off1 + 128 * rnd);
+        }
+        if (width < 16) {  // blocks past K: whatever the buffer holds
+#pragma unroll
+          for (int rnd = 0; rnd < 4; ++rnd) {
+            if (4 * rnd + (g >> 1) >= width) bop.q[rnd][0] = u32x4_t{0u, 0u, 0u, 0u};
+            if (4 * rnd + 2 + (g >> 1) >= width) bop.q[rnd][1] = u32x4_t{0u, 0u, 0u, 0u};
+            if (4 * rnd + g >= width) bop.scale = (bop.scale & ~(0xFFu << (8 * rnd))) | 127u << (8 * rnd);
+          }
         }
       }
+      // acc[0] takes this stage; in a gate/up unit w1's and w3's sums take turns
+      if (width == 16) stage_sums<false>(st, rho, g, width, bop, acc[0][0], acc[0][1]);
+      else stage_sums<true>(st, rho, g, width, bop, acc[0][0], acc[0][1]);
+      if (!down)
+#pragma unroll
+        for (int mi = 0; mi < 2; ++mi) {
+          const f32x4_t o = acc[0][mi];
+          acc[0][mi] = acc[1][mi];
+          acc[1][mi] = o;
+        }
     }
-    // acc[0] takes this stage; in a gate/up unit w1's and w3's sums take turns
-    if (width == 16) stage_sums<false>(st, rho, g, width, bop, acc[0][0], acc[0][1]);
-    else stage_sums<true>(st, rho, g, width, bop, acc[0][0], acc[0][1]);
-    if (!down)
-#pragma unroll
-      for (int mi = 0; mi < 2; ++mi) {
-        const f32x4_t o = acc[0][mi];
-        acc[0][mi] = acc[1][mi];
-        acc[1][mi] = o;
-      }
 
-    if (d0 & 4) {
-      // lane holds, in column rho, features 4 g + v of each 16-row group
-      const int fg = d0 >> 8, row0 = d1 & 1023;
-      if (!down) {
-        float gt[8], up[8];  // feature 4 g + v of group i at 2 v + i: the digits' byte order
+    // lane holds, in column rho, features 4 g + v of each 16-row group
+    if (!down) {
+      float gt[8], up[8];  // feature 4 g + v of group i at 2 v + i: the digits' byte order
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float c = acc[0][i][v], u = acc[1][i][v];
-            gt[2 * v + i] = c + (__shfl_down(c, 1, 16) + (__shfl_down(c, 2, 16) + __shfl_down(c, 3, 16)));
-            up[2 * v + i] = u + (__shfl_down(u, 1, 16) + (__shfl_down(u, 2, 16) + __shfl_down(u, 3, 16)));
-          }
-        float h[8];
-        uint32_t top = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          h[i] = gt[i] / (1.0f + expf(-gt[i])) * up[i];
-          top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
+        for (int v = 0; v < 4; ++v) {
+          const float c = acc[0][i][v], u = acc[1][i][v];
+          gt[2 * v + i] = c + (__shfl_down(c, 1, 16) + (__shfl_down(c, 2, 16) + __shfl_down(c, 3, 16)));
+          up[2 * v + i] = u + (__shfl_down(u, 1, 16) + (__shfl_down(u, 2, 16) + __shfl_down(u, 3, 16)));
         }
-        top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-        if ((rho & 3) == 0 && (rho >> 2) < rows) {
-          const uint32_t e = digit_exp(top);
-          uint2 dg[kHDigits];
-          digits8<kHDigits>(h, e, dg);
-          uint8_t* const hb = a.h + (int64_t)(row0 + (rho >> 2)) * a.hstride + (fg >> 4) * kHRow;
+      float h[8];
+      uint32_t top = 0u;
 #pragma unroll
-          for (int p = 0; p < kHDigits; ++p) store_dev(hb + p * kPlane + digit_at(fg & 15, g, p), dg[p]);
-          if (g == 0)
-            __hip_atomic_store(hb + kHDigits * kPlane + 4 * (fg & 3) + ((fg & 15) >> 2), (uint8_t)(e - 3u), __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-        }
-        pub[0] = d1 >> 16;
-      } else {
-        f32x4_t sum[2];
-#pragma unroll
-        for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float c = acc[0][mi][v];
-            sum[mi][v] = c + (__shfl_down(c, 1, 16) + (__shfl_down(c, 2, 16) + (__shfl_down(c, 3, 16) + __shfl_down(c, 4, 16))));
-          }
-        if (rho == 0) {
-          float* y = a.y + (int64_t)row0 * a.D + 32 * fg + 4 * g;
-          if (bad) sum[0][0] = sum[1][0] = __uint_as_float(0x7FC00000u);
-#pragma unroll
-          for (int mi = 0; mi < 2; ++mi) store_dev(y + 16 * mi, sum[mi]);
-        }
-        pub[0] = nrows + fg;
+      for (int i = 0; i < 8; ++i) {
+        h[i] = gt[i] / (1.0f + expf(-gt[i])) * up[i];
+        top = max(top, __float_as_uint(h[i]) & 0x7FFFFFFFu);
       }
-      acc[0][0] = acc[0][1] = acc[1][0] = acc[1][1] = zero;
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+      if ((rho & 3) == 0 && (rho >> 2) < rows) {
+        const uint32_t e = digit_exp(top);
+        uint2 dg[kHDigits];
+        digits8<kHDigits>(h, e, dg);
+        uint8_t* const hb = a.h + (int64_t)(row + (rho >> 2)) * a.hstride + (fg >> 4) * kHRow;
+#pragma unroll
+        for (int p = 0; p < kHDigits; ++p) store_dev(hb + p * kPlane + digit_at(fg & 15, g, p), dg[p]);
+        if (g == 0)
+          __hip_atomic_store(hb + kHDigits * kPlane + 4 * (fg & 3) + ((fg & 15) >> 2), (uint8_t)(e - 3u), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+      }
+      pub[0] = tile;
+    } else {
+      f32x4_t sum[2];
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float c = acc[0][mi][v];
+          sum[mi][v] = c + (__shfl_down(c, 1, 16) + (__shfl_down(c, 2, 16) + (__shfl_down(c, 3, 16) + __shfl_down(c, 4, 16))));
+        }
+      if (rho == 0) {
+        float* const y = a.y + (int64_t)row * a.D + 32 * fg + 4 * g;
+        if (bad) sum[0][0] = sum[1][0] = __uint_as_float(0x7FC00000u);
+#pragma unroll
+        for (int mi = 0; mi < 2; ++mi) store_dev(y + 16 * mi, sum[mi]);
+      }
+      pub[0] = nrows + fg;
+    }
+    acc[0][0] = acc[0][1] = acc[1][0] = acc[1][1] = zero;
+  }
+
+  // ---- nothing left to stream: count what is finished, then the sums
+  flush();
+  for (; iu.kind == kSum; iu = unit_of(claim())) {
+    wait_for(nrows + iu.fg, (uint32_t)nrows);
+    // eight lanes a token (four features each), eight tokens and 16 slots at a time
+    const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc((void*)a.y, 0, nrows * a.D * 4, 0x00020000);
+    const uint32_t f4 = (uint32_t)(32 * iu.fg + 4 * (lane & 7));
+    for (int t = lane >> 3; t < a.T; t += 8) {
+      f32x4_t sum = zero;
+      for (int j0 = 0; j0 < a.k; j0 += 16) {
+        uint32_t at[16];
+        float wt[16];
+        u32x4_t v[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int q = t * a.k + min(j0 + j, a.k - 1);
+          at[j] = (uint32_t)a.slot_row[q] * (uint32_t)a.D * 4 + 4 * f4;
+          wt[j] = a.w[q];
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = __builtin_amdgcn_raw_buffer_load_b128(yr, at[j], 0, kDevScope);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (j0 + j < a.k)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t bits = v[j][c];
+              sum[c] = fmaf(wt[j], __uint_as_float(bits), sum[c]);
+            }
+      }
+      if (bad) sum[0] = sum[1] = sum[2] = sum[3] = __uint_as_float(0x7FC00000u);
+      *reinterpret_cast<f32x4_t*>(a.out + (int64_t)t * a.D + f4) = sum;
     }
   }
 }
@@ -781,7 +798,7 @@ LayerWorkspace layer_layout(int64_t T, int32_t D, int32_t I, int32_t k) {
   l.xd = take((size_t)T * nst13 * kXRow);
   l.xs = take((size_t)T * nst13 * 16);
   l.gt = take(16 * l.n);
-  l.rows = take(8 * l.n);
+  l.rows = take(16 * l.n);
   l.slot_row = take(4 * l.n);
   l.head = take(16);
   l.flags = take(4 * l.n_flags);
@@ -813,7 +830,7 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t s) {
   p.xd = ws + l.xd;
   p.xs = ws + l.xs;
   p.gt = reinterpret_cast<int4*>(ws + l.gt);
-  p.rows = reinterpret_cast<int2*>(ws + l.rows);
+  p.rows = reinterpret_cast<int4*>(ws + l.rows);
   p.slot_row = reinterpret_cast<int32_t*>(ws + l.slot_row);
   p.head = reinterpret_cast<int32_t*>(ws + l.head);
   p.flags = reinterpret_cast<uint32_t*>(ws + l.flags);
