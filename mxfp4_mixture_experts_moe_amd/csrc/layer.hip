@@ -25,32 +25,38 @@
 // The persistent kernel has none: a wave takes units of work from one list,
 //   1. gate/up units: 32 features of w1 and of w3 for a tile of up to two rows
 //      of one expert, over all of D;
-//   2. down units: 32 features of w2 for one grouped row, over all of I;
+//   2. down units: 32 features of w2 for a tile, over all of I;
 //   3. sum units: 32 features of out for all tokens, slots in order;
 // in that order, expert by expert, and streams their weights through a private
 // ring of three LDS stages that runs on across units.
 //
-// Hand-over.  A down unit needs every gate/up unit of its tile, a sum unit every
-// down unit of its features.  Units are taken by a global ticket (atomic add),
-// and a wave works on its units in ticket order, so a unit waits only for
+// Hand-over.  A down unit needs h from every gate/up unit of its tile, a sum unit
+// every down unit of its features.  Units are taken by a global ticket (atomic
+// add), and a wave works on its units in ticket order, so a unit waits only for
 // units of lower tickets, each of which has been taken by a wave that is
 // already running and that waits for still lower ones only: by induction every
 // wait ends, however many of the workgroups are resident and whatever else
 // the device runs.  (The wait loops are bounded all the same; a wait that ran
-// out would give NaN outputs.)  A wave waits only with its earlier units
-// finished: the weights of a down unit go into the ring whether its h is
-// complete or not, its h follows when a look at the tile's count allows it, and
-// if the unit's first stage comes up without, the wave waits then.
+// out would give NaN outputs.)
+//
+// h carries its own "here": the plan fills it with bytes that no digit and no
+// scale takes, a down unit's loads run ahead like any others, and when a
+// stage's operand comes out of LDS each of its pieces (the eight bytes of one
+// store) is compared with that filling; where one is missing the stage is
+// loaded again.  That costs about 30 vector operations a stage and no trip to
+// memory.  (Counting finished gate/up units per tile instead cost a look at the
+// count for each down unit, which waits for every load before it, and a count
+// that could go out only once the stores had completed, four stages after the
+// unit: 85 us instead of 77 for one token of 16 experts, D = 3584, I = 3072.)
 //
 // Visibility.  Results (digits of h, y) are written with device-scope stores,
-// which go through the XCD's L2, and counted (device-scope add, no return) once
-// the store has completed, that is once a later wait of the in-order
-// vector-memory counter covers it: three stages later, at no cost, or at once
-// where the ring runs dry.  A release fence would write back the whole L2
-// instead.  The reader checks the count and then reads with device-scope loads,
-// which a stale line of its own L2 cannot answer; an acquire fence per check
-// would invalidate that L2 (57 ns each, measured, for every wave of the XCD in
-// turn).  A wave checks only until it has seen every gate/up unit counted.
+// which go through the XCD's L2, and read with device-scope loads, which a stale
+// line of the reader's L2 cannot answer.  y is counted per feature group
+// (device-scope add, no return) once the stores have completed, that is once a
+// later wait of the in-order vector-memory counter covers them: three stages
+// later, at no cost, or at once where the ring runs dry.  Fences would write
+// back or invalidate a whole L2 instead (57 ns each, measured, for every wave of
+// the XCD in turn).
 #include "mx_common.h"
 #include "route_device.h"
 #include "stream_device.h"
@@ -61,9 +67,16 @@ namespace k3moe {
 namespace {
 
 constexpr int kXDigits = 4, kHDigits = 5;
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
 constexpr int kPlane = 512;     // bytes of one digit of a row's stage
 constexpr int kXRow = kXDigits * kPlane;        // x: digits of a (row, stage); its scales are apart
 constexpr int kHRow = kHDigits * kPlane + 16;   // h: digits and scales of a (row, stage)
+
+// What h holds before it is written.  A digit is an integer or NaN, so no byte
+// of it is e4m3's smallest subnormal; a scale byte is at most 252.
+constexpr uint32_t kNoDigit = 0x01010101u, kNoScale = 0xFFFFFFFFu;
 
 // Operand order.  A lane's 16 code bytes of a block hold elements j and j + 16 in
 // byte j, so digit bytes go in the order 0, 16, 1, 17, ...: element e < 16 at
@@ -110,7 +123,7 @@ __device__ __forceinline__ int digit_at(int bb, int i, int p) {
 // expert and clears the counters of the main kernel; the others write x as
 // digits.
 constexpr int kPlanThreads = 1024;
-constexpr int kGuTileRows = 2;
+constexpr int kTileRows = 2;
 
 struct LayerPlan {
   const float* logits;
@@ -122,13 +135,14 @@ struct LayerPlan {
   float* w;        // [T, k]
   uint8_t* xd;     // [T][stages][kXRow] digits of x
   uint8_t* xs;     // [T][stages][16] their scale bytes
-  int4* gt;        // gate/up tiles: expert, first row | rows << 16, tokens of the rows (a byte each), expert's tiles
-                   // (first | count << 16)
-  int4* rows;      // grouped rows: expert, expert's rows (first | count << 16), expert's first gate/up tile
+  int4* tiles;     // expert, first row | rows << 16, tokens of the rows (a byte each), the expert's tiles (first | count << 16)
   int32_t* slot_row;
-  int32_t* head;   // [0] gate/up tiles, [1] next ticket
+  int32_t* head;   // [0] tiles, [1] next ticket
   uint32_t* flags;
-  int n_flags;
+  int n_flags;     // a multiple of 4
+  u32x4_t* h;      // cleared to what no gate/up unit writes
+  int n_h;         // its 16-byte pieces
+  int x_wgs;       // workgroups that write x
 };
 
 template <int NPER>
@@ -138,6 +152,13 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
     // four lanes a block, eight elements each
     const int nb = p.D >> 5, nst = (nb + 15) >> 4;
     const int u = (int)(blockIdx.x - 1) * kPlanThreads + tid;
+    if ((int)blockIdx.x > p.x_wgs) {
+      const int c = u - p.x_wgs * kPlanThreads, f = c - p.n_h;
+      const uint32_t v = c % (kHRow / 16) == kHRow / 16 - 1 ? kNoScale : kNoDigit;
+      if (c < p.n_h) p.h[c] = u32x4_t{v, v, v, v};
+      else if (f < p.n_flags / 4) reinterpret_cast<u32x4_t*>(p.flags)[f] = u32x4_t{0u, 0u, 0u, 0u};
+      return;
+    }
     if (u >= p.T * nb * 4) return;
     const int i = u & 3, t = (u >> 2) / nb, b = (u >> 2) - t * nb;
     const uint16_t* src = p.x + (int64_t)t * p.D + 32 * b + 4 * i;
@@ -163,7 +184,6 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
   __shared__ int s_sum[kPlanThreads / 64][2];
   const int lane = tid & 63, wave = tid >> 6;
   for (int e = tid; e < p.E; e += kPlanThreads) s_mask[e] = 0u;
-  for (int i = tid; i < p.n_flags; i += kPlanThreads) p.flags[i] = 0u;
   const int n = p.T * p.k;
   if constexpr (NPER > 0) {
     __shared__ RouteScratch scratch[kPlanThreads / 64];
@@ -190,7 +210,7 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
   for (int e = tid * per; e < min((tid + 1) * per, p.E); ++e) {
     const int m = __popc(s_mask[e]);
     c[0] += m;
-    c[1] += (m + kGuTileRows - 1) / kGuTileRows;
+    c[1] += (m + kTileRows - 1) / kTileRows;
   }
   int incl[2] = {c[0], c[1]};
 #pragma unroll
@@ -212,16 +232,15 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
     if (m == 0) continue;
     s_base[e] = (uint32_t)at[0];
     uint32_t toks = s_mask[e];
-    const int t0 = at[1], nt = (m + kGuTileRows - 1) / kGuTileRows;
-    for (int r = 0; r < m; ++r) p.rows[at[0] + r] = make_int4(e, at[0] | m << 16, t0, 0);
-    for (int r = 0; r < m; r += kGuTileRows) {
+    const int t0 = at[1], nt = (m + kTileRows - 1) / kTileRows;
+    for (int r = 0; r < m; r += kTileRows) {
       int tk = 0;
-      const int nr = min(kGuTileRows, m - r);
+      const int nr = min(kTileRows, m - r);
       for (int i = 0; i < nr; ++i) {
         tk |= __builtin_ctz(toks) << (8 * i);
         toks &= toks - 1u;
       }
-      p.gt[at[1]++] = make_int4(e, (at[0] + r) | nr << 16, tk, t0 | nt << 16);
+      p.tiles[at[1]++] = make_int4(e, (at[0] + r) | nr << 16, tk, t0 | nt << 16);
     }
     at[0] += m;
   }
@@ -239,24 +258,31 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
 
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 4;            // waves per workgroup, one workgroup per CU
-constexpr int kRing = 3;             // LDS stages per wave
+constexpr int kRing = 3;             // weight stages per wave in LDS
 constexpr int kMatBytes = 16 * 272;  // a 16-row group of a whole stage: 16 rows x 16 blocks of 17 bytes
-constexpr int kRowDw = 68;           // dwords of a row of it
-constexpr int kWBytes = 2 * kMatBytes;
-constexpr int kXRowLds = kXRow + 64; // second row of a gate/up tile: four 16-byte banks on
-constexpr int kActBytes = kXRowLds + kXRow;  // also holds the kHRow bytes of a down row
-constexpr int kStageBytes = kWBytes + kActBytes + 64;  // + scale bytes of x
 constexpr int kChunks = 2 * 16 * 17; // 16-byte chunks of a stage's two groups
-constexpr int kW = (kChunks + 63) / 64;  // weight loads per stage; the last is partial
+constexpr int kW = (kChunks + 63) / 64;  // weight loads per stage
+// Every load is made by the whole wave (its last lanes may bring bytes that
+// nothing reads): a branch on the lane inside the stage loop would make the
+// compiler linearise the loop and carry the wave-uniform state in vector
+// registers.
+constexpr int kSlot = kW * 1024;       // bytes of a weight stage in LDS
+constexpr int kXRowLds = kXRow + 64;   // second row of a tile: other banks than the first
+constexpr int kHRowLds = 3 * 1024 + 128;
+constexpr int kXScales = 2 * kXRowLds;  // scale bytes of x behind its two rows
+constexpr int kActBytes = kHRowLds + 3 * 1024;  // a stage's activations: the larger of both kinds
+constexpr int kActBufs = 2;
 constexpr int kNt = 2;               // cache policy of the weight loads: nontemporal
-constexpr int kDevScope = 16;        // cache policy of a load that must see other XCDs' stores (sc1)
+constexpr int kDevScope = 16;        // cache policy of loads and stores that other XCDs must agree on (sc1)
 constexpr int kSpinLimit = 1 << 21;
 constexpr int kChunk = 4;            // tickets a workgroup draws at once
+constexpr int kNoLane = INT32_MIN;  // buffer offset past every buffer: the lane's store is dropped
 // Counters sit on lines of their own: device-scope adds to one line are served
 // one after another, 11.4 ns each (measured; to different lines they overlap).
 constexpr int kFlagStride = 32;
-static_assert(kHRow <= kActBytes, "a down row fits the activation part");
-static_assert(kWaves * kRing * kStageBytes <= 160 * 1024, "LDS");
+constexpr int kWaveLds = kRing * kSlot + kActBufs * kActBytes;
+static_assert(kHRow <= 3 * 1024 && kXScales + 1024 <= kActBytes, "activation buffers");
+static_assert(kWaves * kWaveLds + 1024 <= 160 * 1024, "LDS");
 
 enum { kGateUp = 0, kDown = 1, kSum = 2, kNone = 3 };
 
@@ -264,42 +290,58 @@ struct LayerArgs {
   const uint8_t *xd, *xs;
   const uint8_t *w1, *w3, *w2;
   int D, I, T, k;
-  const int4* gt;
-  const int4* rows;
+  const int4* tiles;
   const int32_t* slot_row;
   const float* w;
   int32_t* head;
-  uint32_t* flags;  // gate/up units done per tile ([rows]), then down units done per feature group ([D / 32])
+  uint32_t* flags;  // down units done per feature group ([D / 32])
   uint8_t* h;       // [rows][hstride] digits and scales of h, stage by stage
   int hstride;
   float* y;         // [rows][D]
   float* out;       // [T, D]
 };
 
-// A unit of work. row: first row of the tile (gate/up) or the row (down); rows:
-// its rows; tile: gate/up tile; toks: its tokens, a byte each.
+// A unit of work of a tile: its first row, its rows and their tokens (a byte each).
 struct Unit {
-  int kind, fg, expert, row, rows, tile, toks;
+  int kind, fg, expert, row, rows, toks;
 };
-
-typedef int i32x8_t __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-__device__ __forceinline__ void store_dev(uint8_t* p, uint2 v) {
-  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)v.y << 32 | v.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// The first lane's atomics (no branch on the lane: the execution mask is set
+// for the one instruction; the callers run with every lane on).
+__device__ __forceinline__ void count_dev(uint32_t* p) {
+  asm volatile("s_mov_b64 exec, 1\n\tglobal_atomic_add %0, %1, %2\n\ts_mov_b64 exec, -1" ::"v"(0), "v"(1), "s"(p) : "memory");
 }
-__device__ __forceinline__ void store_dev(float* p, f32x4_t v) {
-  uint8_t* q = reinterpret_cast<uint8_t*>(p);
-  store_dev(q, make_uint2(__float_as_uint(v[0]), __float_as_uint(v[1])));
-  store_dev(q + 8, make_uint2(__float_as_uint(v[2]), __float_as_uint(v[3])));
+__device__ __forceinline__ int draw_dev(int32_t* p, int n) {
+  int v;
+  asm volatile(
+      "s_mov_b64 exec, 1\n\tglobal_atomic_add %0, %1, %2, %3 sc0\n\ts_waitcnt vmcnt(0)\n\ts_mov_b64 exec, -1"
+      : "=&v"(v)
+      : "v"(0), "v"(n), "s"(p)
+      : "memory");
+  return uni(v);
+}
+// Compare and swap of an LDS word pair; returns what was there.
+__device__ __forceinline__ uint64_t swap_lds(uint32_t at, uint64_t was, uint64_t now) {
+  uint64_t v;
+  asm volatile("s_mov_b64 exec, 1\n\tds_cmpst_rtn_b64 %0, %1, %2, %3\n\ts_waitcnt lgkmcnt(0)\n\ts_mov_b64 exec, -1"
+               : "=&v"(v)
+               : "v"(at), "v"(was), "v"(now)
+               : "memory");
+  return (uint64_t)(uint32_t)uni((int)(v >> 32)) << 32 | (uint32_t)uni((int)(uint32_t)v);
 }
 
-// Sums of one 16-row group: codes of four rounds (block 4 rnd + g of row rho) times the staged digits.
+// Rounds.  A stage's 16 blocks go in four rounds of four, one block per lane
+// group: group j takes block 4 ((rnd + j) % 4) + j in round rnd.  (The plain
+// order 4 rnd + j would put the 64 reads of a dword, 68 dwords a row apart, into
+// 16 of the 64 banks.)  The fp8 operand's registers 0-3 of lane group g belong
+// to group g / 2's block (its half g % 2), registers 4-7 to group 2 + g / 2's.
+__device__ __forceinline__ int round_block(int rnd, int j) { return 4 * ((rnd + j) & 3) + j; }
+
 struct BOperand {
-  u32x4_t q[4][2];  // per round: positions 16 g .. of the round's first and second 64
-  uint32_t scale;   // byte rnd: scale of block 4 rnd + g
+  u32x4_t q[4][2];  // per round: registers 0-3, 4-7
+  uint32_t scale;   // byte rnd: scale of this lane group's block
 };
 template <int kRnd>
 __device__ __forceinline__ f32x4_t mfma_round(const uint32_t (&a)[4], uint32_t sa, const BOperand& b, f32x4_t c) {
@@ -309,42 +351,42 @@ __device__ __forceinline__ f32x4_t mfma_round(const uint32_t (&a)[4], uint32_t s
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 0, 0, (int)sa, kRnd, (int)b.scale);
 }
 
-// Both 16-row groups of a stage in LDS at `st`.  A block starts at byte sh of
-// its first dword: sh = g in a whole stage; (rho * width + block) * 17 % 4 in
-// the last, shorter one (kTail), whose blocks from `width` on count as zeros.
+// Both 16-row groups of a stage: this lane's blocks of row rho as five dwords
+// each.  A block starts at byte sh of its first dword: sh = g in a whole stage;
+// (rho * width + block) * 17 % 4 in the last, shorter one (kTail), whose blocks
+// from `width` on count as zeros.
 template <bool kTail>
-__device__ __forceinline__ void stage_sums(const uint8_t* st, int rho, int g, int width, const BOperand& b, f32x4_t& c0,
-                                           f32x4_t& c1) {
-  uint32_t d[2][4][5];
-  uint32_t sh[4];
+__device__ __forceinline__ int block_at(int rho, int g, int rnd, int width) {
+  const int b = round_block(rnd, g);
+  return kTail ? (rho * width + min(b, width - 1)) * 17 : rho * 272 + 17 * b;
+}
+// at[rnd]: the block's first dword in its group, in bytes.
+__device__ __forceinline__ void stage_read(const uint8_t* st, const int (&at)[4], uint32_t (&d)[2][4][5]) {
 #pragma unroll
-  for (int rnd = 0; rnd < 4; ++rnd) {
-    int at;
-    if constexpr (kTail) {
-      at = (rho * width + min(4 * rnd + g, width - 1)) * 17;
-      sh[rnd] = (uint32_t)at & 3u;
-      at >>= 2;
-    } else {
-      at = rho * kRowDw + 17 * rnd + 4 * g;
-      sh[rnd] = (uint32_t)g;
-    }
+  for (int rnd = 0; rnd < 4; ++rnd)
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
-      for (int j = 0; j < 5; ++j) d[mi][rnd][j] = reinterpret_cast<const uint32_t*>(st + mi * kMatBytes)[at + j];
-  }
+      for (int j = 0; j < 5; ++j) d[mi][rnd][j] = reinterpret_cast<const uint32_t*>(st + at[rnd] + mi * kMatBytes)[j];
+}
+template <bool kTail>
+__device__ __forceinline__ void stage_sums(const uint32_t (&d)[2][4][5], int rho, int g, int width, const BOperand& b, f32x4_t& c0,
+                                           f32x4_t& c1) {
   auto round = [&](auto rc) __attribute__((always_inline)) {
     constexpr int rnd = decltype(rc)::value;
-    const uint32_t sel = 0x04030201u + 0x01010101u * sh[rnd];
+    const uint32_t sh = kTail ? (uint32_t)block_at<kTail>(rho, g, rnd, width) & 3u : (uint32_t)g;
+    const uint32_t sel = 0x04030201u + 0x01010101u * sh;
     uint32_t a[2][4], sa[2];
 #pragma unroll
     for (int mi = 0; mi < 2; ++mi) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) a[mi][i] = __builtin_amdgcn_perm(d[mi][rnd][i + 1], d[mi][rnd][i], sel);
-      sa[mi] = d[mi][rnd][0] >> (8 * sh[rnd]);  // byte 0 counts
-      if (kTail && 4 * rnd + g >= width) {
-        a[mi][0] = a[mi][1] = a[mi][2] = a[mi][3] = 0u;
-        sa[mi] = 127u;
+      sa[mi] = d[mi][rnd][0] >> (8 * sh);  // byte 0 counts
+      if constexpr (kTail) {
+        const bool in = round_block(rnd, g) < width;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[mi][i] = in ? a[mi][i] : 0u;
+        sa[mi] = in ? sa[mi] : 127u;
       }
     }
     c0 = mfma_round<rnd>(a[0], sa[0], b, c0);
@@ -356,47 +398,46 @@ __device__ __forceinline__ void stage_sums(const uint8_t* st, int rho, int g, in
   round(std::integral_constant<int, 3>{});
 }
 
+// v of lane + kN of the same 16 lanes (0 past their end).
+template <int kN>
+__device__ __forceinline__ float row_down(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x100 + kN, 0xF, 0xF, true));
+}
+
 __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves][kRing][kStageBytes];
-  __shared__ int fifo[kWaves][4][4];  // units in the ring: kind | late << 1 | fg << 2, row | rows << 16, tile
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves][kWaveLds];
+  __shared__ int fifo[kWaves][4][2];  // units in the ring: kind | fg << 1, row | rows << 16
   __shared__ unsigned long long s_pool;
 
   const int lane = threadIdx.x & 63;
   const int wave = uni(threadIdx.x >> 6);
   const int rho = lane & 15, g = lane >> 4;
-  const int nrows = a.T * a.k;
+  uint8_t* const wl = &lds[wave][0];                   // weight stages
+  uint8_t* const al = wl + kRing * kSlot;              // activation buffers
   const int nfg = a.I >> 5, nfu = a.D >> 5;
-  const int n_gt = *as_const(a.head);
-  const int n_gu = n_gt * nfg, n_dn = nrows * nfu;
+  const int n_tiles = *as_const(a.head);
+  const int n_gu = n_tiles * nfg, n_dn = n_tiles * nfu;
   const int nst13 = (nfu + 15) >> 4, nst2 = (nfg + 15) >> 4;
-  const float rcp_fg = 1.0f / (float)nfg, rcp_fu = 1.0f / (float)nfu;
 
-  // n / d for 0 <= n < 2^23 by d's reciprocal r (one step off at most)
-  auto div = [](int n, int d, float r) __attribute__((always_inline)) {
-    int q = (int)((float)n * r);
+  // n / d for 0 <= n < 2^23 by d's reciprocal (one step off at most)
+  auto div = [](int n, int d) __attribute__((always_inline)) {
+    int q = (int)((float)n * __builtin_amdgcn_rcpf((float)d));
     q -= q * d > n ? 1 : 0;
     q += (q + 1) * d <= n ? 1 : 0;
     return uni(q);
   };
-  // Units of one expert are neighbours, its tiles (rows) fastest: what reads
-  // the same weights runs at the same time, mostly in one workgroup.
+  // Units of one expert are neighbours, its tiles fastest: what reads the same
+  // weights runs at the same time, mostly in one workgroup.
   auto unit_of = [&](int t) __attribute__((always_inline)) -> Unit {
-    if (t < n_gu) {
-      const auto p = as_const(reinterpret_cast<const int32_t*>(a.gt));
-      const int first = p[4 * div(t, nfg, rcp_fg) + 3];
-      const int t0 = first & 0xFFFF, nt = first >> 16;
-      const int in = t - t0 * nfg, fg = nt == 1 ? in : div(in, nt, 1.0f / (float)nt), i = t0 + in - fg * nt;
-      return Unit{kGateUp, fg, p[4 * i], p[4 * i + 1] & 0xFFFF, p[4 * i + 1] >> 16, i, p[4 * i + 2]};
-    }
-    t -= n_gu;
-    if (t < n_dn) {
-      const auto q = as_const(reinterpret_cast<const int32_t*>(a.rows)) + 4 * div(t, nfu, rcp_fu);
-      const int r0 = q[1] & 0xFFFF, nr = q[1] >> 16;
-      const int in = t - r0 * nfu, fu = nr == 1 ? in : div(in, nr, 1.0f / (float)nr), r = in - fu * nr;
-      return Unit{kDown, fu, q[0], r0 + r, 1, q[2] + r / kGuTileRows, 0};
-    }
-    t -= n_dn;
-    return Unit{t < nfu ? kSum : kNone, t, 0, 0, 0, 0, 0};
+    const bool gu = t < n_gu;
+    const int in = gu ? t : t - n_gu;
+    if (in >= n_dn && !gu) return Unit{in - n_dn < nfu ? kSum : kNone, in - n_dn, 0, 0, 0, 0};
+    const int per = gu ? nfg : nfu;  // units of a tile
+    const auto p = as_const(reinterpret_cast<const int32_t*>(a.tiles));
+    const int first = p[4 * div(in, per) + 3];
+    const int t0 = first & 0xFFFF, nt = first >> 16;
+    const int k = in - t0 * per, fg = nt == 1 ? k : div(k, nt), i = t0 + k - fg * nt;
+    return Unit{gu ? kGateUp : kDown, fg, p[4 * i], p[4 * i + 1] & 0xFFFF, p[4 * i + 1] >> 16, p[4 * i + 2]};
   };
 
   // Tickets: the workgroup draws kChunk consecutive ones at a time and its
@@ -406,29 +447,24 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   constexpr uint32_t kRefill = 0xFFFFFFFFu;
   if (threadIdx.x == 0) s_pool = 0ull;
   __syncthreads();
+  const uint32_t pool = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)&s_pool;
   auto claim = [&]() __attribute__((always_inline)) -> int {
-    int v = 0;
-    if (lane == 0)
-      for (;;) {
-        unsigned long long s = __hip_atomic_load(&s_pool, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        const uint32_t left = (uint32_t)(s >> 32);
-        if (left == kRefill) {
-          __builtin_amdgcn_s_sleep(1);
-        } else if (left > 0) {
-          if (__hip_atomic_compare_exchange_strong(&s_pool, &s, s + 1ull - (1ull << 32), __ATOMIC_RELAXED, __ATOMIC_RELAXED,
-                                                   __HIP_MEMORY_SCOPE_WORKGROUP)) {
-            v = (int)(uint32_t)s;
-            break;
-          }
-        } else if (__hip_atomic_compare_exchange_strong(&s_pool, &s, (unsigned long long)kRefill << 32, __ATOMIC_RELAXED,
-                                                        __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)) {
-          v = __hip_atomic_fetch_add(a.head + 1, kChunk, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          __hip_atomic_store(&s_pool, (unsigned long long)(kChunk - 1) << 32 | (uint32_t)(v + 1), __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_WORKGROUP);
-          break;
-        }
+    for (;;) {
+      const uint64_t s = __hip_atomic_load(&s_pool, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      const uint32_t next = (uint32_t)uni((int)(uint32_t)s), left = (uint32_t)uni((int)(s >> 32));
+      if (left == kRefill) {
+        __builtin_amdgcn_s_sleep(1);
+        continue;
       }
-    return uni(v);
+      const uint64_t was = (uint64_t)left << 32 | next;
+      const uint64_t now = left > 0 ? (uint64_t)(left - 1) << 32 | (next + 1) : (uint64_t)kRefill << 32;
+      if (swap_lds(pool, was, now) != was) continue;
+      if (left > 0) return (int)next;
+      const int v = draw_dev(a.head + 1, kChunk);
+      __hip_atomic_store(&s_pool, (unsigned long long)(kChunk - 1) << 32 | (uint32_t)(v + 1), __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_WORKGROUP);
+      return v;
+    }
   };
 
   // Weight load j takes chunks 64 j + lane of a stage: byte 16 c of the first
@@ -437,37 +473,29 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   // loads 0-3, 4-7 and 8 share a base each, and their lane offsets are
   const int lane16 = 16 * lane;  // 0-3
   int wofs4 = 0, wofs5 = 0;      // 4; 5-8
-  const bool wlast = lane < kChunks - 64 * (kW - 1);
   static_assert(kW == 9, "three bases");
 
   // ---- issue side.  A stage is the same 512 columns of two neighbouring 16-row
-  // groups of one matrix: of w2 (down), or of w1 and then of w3 (gate/up), where
-  // the digits of x travel with w1.
-  Unit iu = unit_of(claim());        // the unit being issued, or the next one
-  Unit nu{kNone, 0, 0, 0, 0, 0, 0};  // the one after it, drawn while iu's loads go out
-  bool drawn = true;
+  // groups of one matrix: of w2 (down), or of w1 and then of w3 (gate/up), and
+  // the digits that go with those columns, loaded with w1 for both.  Loads
+  // return in order, so what a stage waits for must not have been asked for
+  // behind what may still be on its way: weights go three stages ahead,
+  // activations two, right before the weights of the stage after theirs.
+  Unit iu{kNone, 0, 0, 0, 0, 0};  // the unit being issued
+  Unit nu = iu;                      // the one after it
+  bool drawn = false;                // whether nu has been drawn
   const uint8_t *wb0 = nullptr, *wb1 = nullptr;  // the next stage's weights; gate/up: and those of the stage after it
   int grp2x = 0;             // bytes of a stage's two whole groups, less what lies before the stage
-  int act0 = 0, act1 = 0;    // where the stage's activations are: rows of x, or (act0) the row of h
+  int act0 = 0, act1 = 0;    // where the stage's activations are, per row of the tile
   int sco = 0;               // per lane: scale bytes of tile row `lane`
-  int left = 0;              // stages of iu not yet issued (0: iu's loads have not begun)
-  int inflight = 0, buf_i = 0, pushed = 0;
+  int left = 0;              // stages of iu not yet issued (0: nu's are the next)
+  int want = 0;              // activations of the stage issued last: rows, + 4 for h; 0: none
+  int want0 = 0, want1 = 0, wantsc = 0;  // where they are
+  int inflight = 0, buf_i = 0, abuf_i = 0, pushed = 0;
   bool bad = false;          // a bounded wait ran out
-  bool all_done = false;     // every gate/up unit has been seen counted
-  bool has_h = false;        // iu is a down unit whose h is complete
 
   auto seen = [&](int f) __attribute__((always_inline)) -> uint32_t {
     return (uint32_t)uni((int)__hip_atomic_load(a.flags + f * kFlagStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
-  };
-  // whether the down unit iu has its h (no waiting)
-  auto look = [&]() __attribute__((always_inline)) -> bool {
-    if (all_done) return true;
-    if (seen(iu.tile) < (uint32_t)nfg) return false;
-    bool all = true;  // whether that was the last look this wave needs
-    for (int i = lane; i < n_gt; i += 64)
-      all = all && __hip_atomic_load(a.flags + i * kFlagStride, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= (uint32_t)nfg;
-    all_done = __all(all);
-    return true;
   };
   auto wait_for = [&](int f, uint32_t need) __attribute__((always_inline)) {
     int spins = 0;
@@ -479,7 +507,25 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
       }
     }
   };
+  auto load_h = [&](uint8_t* dst, int at) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t r =
+        __builtin_amdgcn_make_buffer_rsrc((void*)a.h, 0, a.T * a.k * a.hstride, 0x00020000);
+    const int so = uni(at);
+    const auto l = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, kDevScope);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, kDevScope);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 2048, kDevScope);
+  };
+  auto load_x = [&](uint8_t* dst, int at) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xd, 0, a.T * nst13 * kXRow, 0x00020000);
+    const int so = uni(at);
+    const auto l = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, 0);
+  };
   auto prep = [&]() __attribute__((always_inline)) {
+    iu = nu;
+    drawn = false;
     // (plain values first, assigned once: the compiler would merge assignments
     // at the ends of two branches into one through memory)
     const bool gu = iu.kind == kGateUp;
@@ -493,38 +539,36 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     wofs4 = lane < 16 ? 4096 + lane16 : wofs5;
     left = gu ? 2 * nst13 : nst2;
     act0 = gu ? t0 * nst13 * kXRow : iu.row * a.hstride;
-    act1 = t1 * nst13 * kXRow;
+    act1 = gu ? t1 * nst13 * kXRow : act0 + a.hstride;
     sco = (lane == 1 ? t1 : t0) * nst13 * 16;
-    has_h = gu || look();
     int* const f = fifo[wave][pushed & 3];
     ++pushed;
-    if (lane == 0) {
-      f[0] = iu.kind | (has_h ? 0 : 2) | iu.fg << 2;
-      f[1] = iu.row | iu.rows << 16;
-      f[2] = iu.tile;
-    }
-    drawn = false;
+    f[0] = iu.kind | iu.fg << 1;  // (every lane, the same)
+    f[1] = iu.row | iu.rows << 16;
   };
-  auto load_h = [&](uint8_t* dst, int at) __attribute__((always_inline)) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.h, 0, nrows * a.hstride, 0x00020000);
-    const int so = uni(at);
-    const auto l = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, kDevScope);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, kDevScope);
-    if (lane < (kHRow - 2048) / 16) __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 2048, kDevScope);
-  };
-  auto load_x = [&](uint8_t* dst, int at) __attribute__((always_inline)) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xd, 0, a.T * nst13 * kXRow, 0x00020000);
-    const int so = uni(at);
-    const auto l = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, 0);
-  };
-  // the next stage of iu into the ring
+  // activations of the stage issued last, then the weights of iu's next one
   auto issue = [&]() __attribute__((always_inline)) {
-    uint8_t* const dst = &lds[wave][buf_i][0];
-    uint8_t* const ad = dst + kWBytes;
-    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)wb0, 0, grp2x, 0x00020000);
+    if (want != 0) {
+      uint8_t* const ad = al + abuf_i * kActBytes;
+      if (want & 4) {
+        load_h(ad, want0);
+        if (want & 2) load_h(ad + kHRowLds, want1);
+      } else {
+        load_x(ad, want0);
+        if (want & 2) load_x(ad + kXRowLds, want1);
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xs, 0, a.T * nst13 * 16, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + kXScales), 16, wantsc, 0, 0,
+                                                 0);
+      }
+      abuf_i ^= 1;
+    }
+    want = 0;
+    if (left == 0) {
+      if (nu.kind >= kSum) return;
+      prep();
+    }
+    uint8_t* const dst = wl + buf_i * kSlot;
+    const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc((void*)wb0, 0, uni(grp2x), 0x00020000);
     const auto l0 = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
     const auto l4 = (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 4096);
     const auto l8 = (__attribute__((address_space(3))) void*)(uintptr_t)(dst + 8192);
@@ -536,50 +580,38 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs5, 0, 1024, kNt);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs5, 0, 2048, kNt);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs5, 0, 3072, kNt);
-    if (wlast) __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l8, 16, wofs5, 4096, 0, kNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l8, 16, wofs5, 4096, 0, kNt);
     --left;
-    if (iu.kind == kGateUp) {
-      if (left & 1) {  // w1 (an even number of stages, w1 and w3 by turns)
-        load_x(ad, act0);
-        act0 += kXRow;
-        if (iu.rows > 1) {
-          load_x(ad + kXRowLds, act1);
-          act1 += kXRow;
-        }
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xs, 0, a.T * nst13 * 16, 0x00020000);
-        if (lane < iu.rows)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + kActBytes), 16, sco, 0, 0, 0);
-        sco += 16;
-      }
-      const uint8_t* const next = wb0 + kMatBytes;  // of the same matrix, two stages on
-      wb0 = wb1;
-      wb1 = next;
-      grp2x -= (left & 1) ? 0 : kMatBytes;
-    } else {
-      if (has_h) load_h(ad, act0);
-      act0 += kHRow;
-      wb0 += kMatBytes;
-      grp2x -= kMatBytes;
-    }
+    const bool gu = iu.kind == kGateUp;
+    const int odd = left & 1;  // gate/up: an even number of stages, w1 where an odd number is left
+    want = gu ? (odd ? iu.rows : 0) : iu.rows + 4;
+    want0 = act0;
+    want1 = act1;
+    wantsc = sco;
+    const int on = gu && odd ? 0 : 1;  // columns go on after w3
+    const uint8_t* const next = wb0 + kMatBytes;
+    wb0 = gu ? wb1 : next;
+    wb1 = next;
+    grp2x -= on * kMatBytes;
+    act0 += on * (gu ? kXRow : kHRow);
+    act1 += on * (gu ? kXRow : kHRow);
+    sco += on * 16;
     ++inflight;
     buf_i = buf_i == kRing - 1 ? 0 : buf_i + 1;
-    if (left == 0) {
-      if (!drawn) nu = unit_of(claim());
-      drawn = true;
-      iu = nu;
-    }
   };
 
   // ---- publishing
-  int pub[3] = {-1, -1, -1};  // flags of finished units, by age in stages
+  // flags of finished units by age in stages; a unit's stores lie before the
+  // weights asked for in the next stage, which the wait three stages on leaves out
+  constexpr int kAges = 3;
+  int pub[kAges] = {-1, -1, -1};
   auto publish = [&](int f) __attribute__((always_inline)) {
-    if (f >= 0 && lane == 0)
-      (void)__hip_atomic_fetch_add(a.flags + f * kFlagStride, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (f >= 0) count_dev(a.flags + f * kFlagStride);
   };
   auto flush = [&]() __attribute__((always_inline)) {
     wait_vm<0>();
 #pragma unroll
-    for (int i = 2; i >= 0; --i) {
+    for (int i = kAges - 1; i >= 0; --i) {
       publish(pub[i]);
       pub[i] = -1;
     }
@@ -589,102 +621,144 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   f32x4_t acc[2][2] = {{zero, zero}, {zero, zero}};  // [w1 / w3 by turns][16-row group]
   BOperand bop{};
   // LDS offsets of this lane's digits.  gate/up: column 4 r + p is digit p of
-  // tile row r; columns from 8 on repeat.  down: columns 0 .. 4 are the digits.
-  const int xp = rho & 3, hp = rho < kHDigits ? rho : 0;
+  // tile row r; columns from 8 on repeat.  down: column 5 r + p likewise.
+  const int xp = rho & 3, hr = rho >= kHDigits && rho < 2 * kHDigits ? 1 : 0, hp = rho < 2 * kHDigits ? rho - hr * kHDigits : 0;
   const int xoff0 = xp * kPlane + 16 * (g ^ xp), xoff1 = xp * kPlane + 16 * ((4 + g) ^ xp);
   const int hoff0 = hp * kPlane + 16 * (g ^ hp), hoff1 = hp * kPlane + 16 * ((4 + g) ^ hp);
+  int woff[4], rot0[4], rot1[4];  // per round: this lane's block, the rounds of its operand's two blocks
+#pragma unroll
+  for (int rnd = 0; rnd < 4; ++rnd) {
+    woff[rnd] = block_at<false>(rho, g, rnd, 16) & ~3;
+    rot0[rnd] = 128 * ((rnd + (g >> 1)) & 3);
+    rot1[rnd] = 128 * ((rnd + 2 + (g >> 1)) & 3);
+  }
   const uint32_t xsub = 0x05050505u * (uint32_t)xp, hsub = 0x05050505u * (uint32_t)hp;
 
-  int buf_c = 0, popped = 0;
+  // One pass of the loop takes a stage out of the ring and asks for a later one;
+  // while the ring fills, it only asks.
+  int buf_c = 0, abuf_c = 0, popped = 0;
+  int s = 0, nst = 0;  // stage of the open unit, its stages
+  // the open unit, and this lane's operand pieces in an activation buffer
+  int row = 0, rows = 0, fg = 0, cut = 0, off0 = 0, off1 = 0, offs = 0;
+  uint32_t sub = 0;
+  bool down = false;
   for (;;) {
-    while (inflight < kRing && iu.kind < kSum) {
-      if (left == 0) prep();
-      issue();
-    }
-    if (inflight == 0) break;
-    // ---- one unit
-    const int* const f = fifo[wave][popped & 3];
-    ++popped;
-    const int f0 = uni(f[0]), f1 = uni(f[1]), tile = uni(f[2]);
-    const bool down = (f0 & 1) != 0;
-    const int row = f1 & 0xFFFF, rows = f1 >> 16, fg = f0 >> 2;
-    const int nst = down ? nst2 : 2 * nst13;
-    const int cut = (down ? nfg : nfu) & 15;  // blocks of a last, shorter stage (0: none)
-    // column rho's tile row (gate/up) and this lane's operand pieces
-    const int r = !down && rows > 1 && (rho & 4) ? kXRowLds : 0;
-    const int off0 = kWBytes + r + (down ? hoff0 : xoff0), off1 = kWBytes + r + (down ? hoff1 : xoff1);
-    const int offs = kWBytes + 4 * g + (down ? kHDigits * kPlane : kActBytes + (r ? 16 : 0));
-    const uint32_t sub = down ? hsub : xsub;
-    if (f0 & 2) {
-      // The unit's weights went ahead of its h.  Every earlier unit of this
-      // wave is finished: count them, wait for the tile, load h for the stages
-      // that are in the ring.
-      flush();
-      wait_for(tile, (uint32_t)nfg);
-      for (int j = 0, b = buf_c; j < inflight && j < nst; ++j, b = b == kRing - 1 ? 0 : b + 1)
-        load_h(&lds[wave][b][0] + kWBytes, row * a.hstride + j * kHRow);
-      wait_vm<0>();
-      if (left > 0 && inflight < nst) has_h = true;  // iu is this unit
-    }
-    for (int s = 0; s < nst; ++s) {
-      if (inflight < kRing && iu.kind < kSum) {
-        if (left == 0) prep();
-        issue();
+    if (!drawn) nu = unit_of(claim());
+    drawn = true;
+    const bool eat = inflight == kRing || (left == 0 && nu.kind >= kSum && want == 0);
+    bool shorter = false;
+    uint32_t wd[2][4][5];
+    if (eat) {
+      if (inflight == 0) break;
+      if (s == nst) {
+        // ---- the next unit
+        const int* const f = fifo[wave][popped & 3];
+        ++popped;
+        const int f0 = uni(f[0]), f1 = uni(f[1]);
+        down = (f0 & 1) != 0;
+        row = f1 & 0xFFFF;
+        rows = f1 >> 16;
+        fg = f0 >> 1;
+        s = 0;
+        nst = down ? nst2 : 2 * nst13;
+        cut = (down ? nfg : nfu) & 15;  // blocks of a last, shorter stage (0: none)
+        // column rho's tile row and digit
+        const int r = rows == 1 ? 0 : down ? hr * kHRowLds : (rho & 4) ? kXRowLds : 0;
+        off0 = r + (down ? hoff0 : xoff0);
+        off1 = r + (down ? hoff1 : xoff1);
+        offs = 4 * g + (down ? r + kHDigits * kPlane : kXScales + (r ? 16 : 0));
+        sub = down ? hsub : xsub;
       }
-      if (!drawn && left > 0) {  // with the ring full
-        nu = unit_of(claim());
-        drawn = true;
-      }
-      // The oldest stage has landed once only the loads of the newer ones are
-      // out: their weights and, within a unit, activations (gate/up: of one of
-      // two neighbouring stages; down: of both).  Fewer are assumed where that
-      // is not sure, which waits for a little more.
-      if (inflight < kRing) {
-        if (inflight == 2) wait_vm<kW>();
-        else wait_vm<0>();
-      } else if (s + 2 >= nst) {
-        wait_vm<2 * kW>();
-      } else if (!down) {
-        wait_vm<2 * kW + 3>();
-      } else {
-        wait_vm<2 * kW + 6>();
-      }
-      // a unit finished three stages ago: its stores are older than these loads
-      publish(pub[2]);
-      pub[2] = pub[1];
-      pub[1] = pub[0];
+      // The stage has landed once only loads asked for after its own are out:
+      // the weights of two stages and, before the newer of them, activations of
+      // the next stage (down; counted where that is this unit's).
+      if (inflight < kRing) wait_vm<0>();
+      else if (!down || s + 1 >= nst) wait_vm<2 * kW>();
+      else if (rows == 1) wait_vm<2 * kW + 3>();
+      else wait_vm<2 * kW + 6>();
+      publish(pub[kAges - 1]);
+#pragma unroll
+      for (int i = kAges - 1; i > 0; --i) pub[i] = pub[i - 1];
       pub[0] = -1;
-      const uint8_t* const st = &lds[wave][buf_c][0];
+      const uint8_t* const st = wl + buf_c * kSlot;
       buf_c = buf_c == kRing - 1 ? 0 : buf_c + 1;
       --inflight;
-      const int width = cut != 0 && (down ? s == nst - 1 : s >= nst - 2) ? cut : 16;
+      shorter = cut != 0 && (down ? s == nst - 1 : s >= nst - 2);
       if (down || (s & 1) == 0) {
-        bop.scale = *reinterpret_cast<const uint32_t*>(st + offs) - sub;
-#pragma unroll
-        for (int rnd = 0; rnd < 4; ++rnd) {
-          bop.q[rnd][0] = *reinterpret_cast<const u32x4_t*>(st + off0 + 128 * rnd);
-          bop.q[rnd][1] = *reinterpret_cast<const u32x4_t*>(st + off1 + 128 * rnd);
-        }
-        if (width < 16) {  // blocks past K: whatever the buffer holds
+        const uint8_t* const ad = al + abuf_c * kActBytes;
+        abuf_c ^= 1;
+        for (int spins = 0;;) {
+          bop.scale = *reinterpret_cast<const uint32_t*>(ad + offs) - sub;
 #pragma unroll
           for (int rnd = 0; rnd < 4; ++rnd) {
-            if (4 * rnd + (g >> 1) >= width) bop.q[rnd][0] = u32x4_t{0u, 0u, 0u, 0u};
-            if (4 * rnd + 2 + (g >> 1) >= width) bop.q[rnd][1] = u32x4_t{0u, 0u, 0u, 0u};
-            if (4 * rnd + g >= width) bop.scale = (bop.scale & ~(0xFFu << (8 * rnd))) | 127u << (8 * rnd);
+            bop.q[rnd][0] = *reinterpret_cast<const u32x4_t*>(ad + off0 + rot0[rnd]);
+            bop.q[rnd][1] = *reinterpret_cast<const u32x4_t*>(ad + off1 + rot1[rnd]);
           }
+          bop.scale = __builtin_amdgcn_alignbit(bop.scale, bop.scale, 8 * g);  // byte rnd: that of round_block's round
+          if (shorter) {  // blocks past K: whatever the buffer holds
+#pragma unroll
+            for (int rnd = 0; rnd < 4; ++rnd) {
+              const bool in0 = round_block(rnd, g >> 1) < cut, in1 = round_block(rnd, 2 + (g >> 1)) < cut;
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                bop.q[rnd][0][c] = in0 ? bop.q[rnd][0][c] : 0u;
+                bop.q[rnd][1][c] = in1 ? bop.q[rnd][1][c] : 0u;
+              }
+              const uint32_t byte = 0xFFu << (8 * rnd);
+              bop.scale = round_block(rnd, g) < cut ? bop.scale : (bop.scale & ~byte) | (0x7F7F7F7Fu & byte);
+            }
+          }
+          if (!down) break;
+          // h is here once no piece of it (eight digits, a scale byte) is what
+          // the plan left there; else this stage's and the next one's again
+          uint32_t least = ~0u;  // 0 where a piece is missing
+#pragma unroll
+          for (int rnd = 0; rnd < 4; ++rnd)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              least = min(least, min(bop.q[rnd][i][0] ^ kNoDigit, bop.q[rnd][i][2] ^ kNoDigit));
+          const uint32_t sc = bop.scale ^ (kNoScale - sub);
+          const bool here = (least != 0u) & (((sc - 0x01010101u) & ~sc & 0x80808080u) == 0u);
+          if (__all(here)) break;
+          if (++spins > kSpinLimit) {
+            bad = true;
+            break;
+          }
+          const int at = row * a.hstride + s * kHRow;
+          for (int j = 0; j < 2; ++j) {
+            uint8_t* const aj = al + (abuf_c ^ (1 - j)) * kActBytes;
+            if (j == 1 && (inflight == 0 || s + 1 >= nst)) break;
+            load_h(aj, at + j * kHRow);
+            if (rows > 1) load_h(aj + kHRowLds, at + a.hstride + j * kHRow);
+          }
+          wait_vm<0>();
         }
       }
-      // acc[0] takes this stage; in a gate/up unit w1's and w3's sums take turns
-      if (width == 16) stage_sums<false>(st, rho, g, width, bop, acc[0][0], acc[0][1]);
-      else stage_sums<true>(st, rho, g, width, bop, acc[0][0], acc[0][1]);
-      if (!down)
+      if (!shorter) {
+        stage_read(st, woff, wd);
+      } else {
+        int at[4];
 #pragma unroll
-        for (int mi = 0; mi < 2; ++mi) {
-          const f32x4_t o = acc[0][mi];
-          acc[0][mi] = acc[1][mi];
-          acc[1][mi] = o;
-        }
+        for (int rnd = 0; rnd < 4; ++rnd) at[rnd] = block_at<true>(rho, g, rnd, cut) & ~3;
+        stage_read(st, at, wd);
+      }
+      // the stage is in registers: its buffers take later ones, whose loads run
+      // beside the arithmetic below
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
+    issue();
+    if (!eat) continue;
+    // acc[0] takes this stage; in a gate/up unit w1's and w3's sums take turns
+    if (!shorter) stage_sums<false>(wd, rho, g, 16, bop, acc[0][0], acc[0][1]);
+    else stage_sums<true>(wd, rho, g, cut, bop, acc[0][0], acc[0][1]);
+    if (!down)
+#pragma unroll
+      for (int mi = 0; mi < 2; ++mi) {
+        const f32x4_t o = acc[0][mi];
+        acc[0][mi] = acc[1][mi];
+        acc[1][mi] = o;
+      }
+    if (++s < nst) continue;
 
     // lane holds, in column rho, features 4 g + v of each 16-row group
     if (!down) {
@@ -694,8 +768,8 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float c = acc[0][i][v], u = acc[1][i][v];
-          gt[2 * v + i] = c + (__shfl_down(c, 1, 16) + (__shfl_down(c, 2, 16) + __shfl_down(c, 3, 16)));
-          up[2 * v + i] = u + (__shfl_down(u, 1, 16) + (__shfl_down(u, 2, 16) + __shfl_down(u, 3, 16)));
+          gt[2 * v + i] = c + (row_down<1>(c) + (row_down<2>(c) + row_down<3>(c)));
+          up[2 * v + i] = u + (row_down<1>(u) + (row_down<2>(u) + row_down<3>(u)));
         }
       float h[8];
       uint32_t top = 0u;
@@ -706,18 +780,18 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
       }
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-      if ((rho & 3) == 0 && (rho >> 2) < rows) {
-        const uint32_t e = digit_exp(top);
-        uint2 dg[kHDigits];
-        digits8<kHDigits>(h, e, dg);
-        uint8_t* const hb = a.h + (int64_t)(row + (rho >> 2)) * a.hstride + (fg >> 4) * kHRow;
+      const uint32_t e = digit_exp(top);
+      uint2 dg[kHDigits];
+      digits8<kHDigits>(h, e, dg);
+      const __amdgpu_buffer_rsrc_t hb = __builtin_amdgcn_make_buffer_rsrc((void*)a.h, 0, a.T * a.k * a.hstride, 0x00020000);
+      const bool mine = ((rho & 3) == 0) & ((rho >> 2) < rows);
+      const int at = ((row + (rho >> 2)) * a.hstride + (fg >> 4) * kHRow) | (mine ? 0 : kNoLane);
+      typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
-        for (int p = 0; p < kHDigits; ++p) store_dev(hb + p * kPlane + digit_at(fg & 15, g, p), dg[p]);
-        if (g == 0)
-          __hip_atomic_store(hb + kHDigits * kPlane + 4 * (fg & 3) + ((fg & 15) >> 2), (uint8_t)(e - 3u), __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-      }
-      pub[0] = tile;
+      for (int p = 0; p < kHDigits; ++p)
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{dg[p].x, dg[p].y}, hb, at + p * kPlane + digit_at(fg & 15, g, p), 0, kDevScope);
+      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(e - 3u), hb,
+                                           (at + kHDigits * kPlane + 4 * (fg & 3) + ((fg & 15) >> 2)) | (g == 0 ? 0 : kNoLane), 0, kDevScope);
     } else {
       f32x4_t sum[2];
 #pragma unroll
@@ -725,26 +799,30 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const float c = acc[0][mi][v];
-          sum[mi][v] = c + (__shfl_down(c, 1, 16) + (__shfl_down(c, 2, 16) + (__shfl_down(c, 3, 16) + __shfl_down(c, 4, 16))));
+          sum[mi][v] = c + (row_down<1>(c) + (row_down<2>(c) + (row_down<3>(c) + row_down<4>(c))));
         }
-      if (rho == 0) {
-        float* const y = a.y + (int64_t)row * a.D + 32 * fg + 4 * g;
-        if (bad) sum[0][0] = sum[1][0] = __uint_as_float(0x7FC00000u);
+      const __amdgpu_buffer_rsrc_t yb = __builtin_amdgcn_make_buffer_rsrc((void*)a.y, 0, a.T * a.k * a.D * 4, 0x00020000);
+      const bool second = (rho == kHDigits) & (rows > 1);
+      const int at = (4 * ((row + (second ? 1 : 0)) * a.D + 32 * fg + 4 * g)) | ((rho == 0) | second ? 0 : kNoLane);
 #pragma unroll
-        for (int mi = 0; mi < 2; ++mi) store_dev(y + 16 * mi, sum[mi]);
+      for (int mi = 0; mi < 2; ++mi) {
+        u32x4_t v;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = bad ? 0x7FC00000u : __float_as_uint(sum[mi][c]);
+        __builtin_amdgcn_raw_buffer_store_b128(v, yb, at + 64 * mi, 0, kDevScope);
       }
-      pub[0] = nrows + fg;
+      pub[0] = fg;
     }
     acc[0][0] = acc[0][1] = acc[1][0] = acc[1][1] = zero;
   }
 
   // ---- nothing left to stream: count what is finished, then the sums
   flush();
-  for (; iu.kind == kSum; iu = unit_of(claim())) {
-    wait_for(nrows + iu.fg, (uint32_t)nrows);
+  for (; nu.kind == kSum; nu = unit_of(claim())) {
+    wait_for(nu.fg, (uint32_t)n_tiles);
     // eight lanes a token (four features each), eight tokens and 16 slots at a time
-    const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc((void*)a.y, 0, nrows * a.D * 4, 0x00020000);
-    const uint32_t f4 = (uint32_t)(32 * iu.fg + 4 * (lane & 7));
+    const __amdgpu_buffer_rsrc_t yr = __builtin_amdgcn_make_buffer_rsrc((void*)a.y, 0, a.T * a.k * a.D * 4, 0x00020000);
+    const uint32_t f4 = (uint32_t)(32 * nu.fg + 4 * (lane & 7));
     for (int t = lane >> 3; t < a.T; t += 8) {
       f32x4_t sum = zero;
       for (int j0 = 0; j0 < a.k; j0 += 16) {
@@ -777,7 +855,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct LayerWorkspace {
-  size_t ids, w, xd, xs, gt, rows, slot_row, head, flags, h, y, total;
+  size_t ids, w, xd, xs, tiles, slot_row, head, flags, h, y, total;
   int64_t n, n_flags;
   int hstride;
 };
@@ -791,14 +869,13 @@ LayerWorkspace layer_layout(int64_t T, int32_t D, int32_t I, int32_t k) {
   };
   const int nst13 = (D / 32 + 15) / 16, nst2 = (I / 32 + 15) / 16;
   l.n = T * k;
-  l.n_flags = (l.n + D / 32) * kFlagStride;
-  l.hstride = (int)align256((size_t)nst2 * kHRow);
+  l.n_flags = (int64_t)(D / 32) * kFlagStride;
+  l.hstride = nst2 * kHRow;
   l.ids = take(4 * l.n);
   l.w = take(4 * l.n);
   l.xd = take((size_t)T * nst13 * kXRow);
   l.xs = take((size_t)T * nst13 * 16);
-  l.gt = take(16 * l.n);
-  l.rows = take(16 * l.n);
+  l.tiles = take(16 * l.n);
   l.slot_row = take(4 * l.n);
   l.head = take(16);
   l.flags = take(4 * l.n_flags);
@@ -829,13 +906,15 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t s) {
   p.w = c.w ? c.w : reinterpret_cast<float*>(ws + l.w);
   p.xd = ws + l.xd;
   p.xs = ws + l.xs;
-  p.gt = reinterpret_cast<int4*>(ws + l.gt);
-  p.rows = reinterpret_cast<int4*>(ws + l.rows);
+  p.tiles = reinterpret_cast<int4*>(ws + l.tiles);
   p.slot_row = reinterpret_cast<int32_t*>(ws + l.slot_row);
   p.head = reinterpret_cast<int32_t*>(ws + l.head);
   p.flags = reinterpret_cast<uint32_t*>(ws + l.flags);
   p.n_flags = (int)l.n_flags;
-  const unsigned blocks = 1 + (unsigned)((c.T * (c.D / 8) + kPlanThreads - 1) / kPlanThreads);
+  p.h = reinterpret_cast<u32x4_t*>(ws + l.h);
+  p.n_h = (int)(l.n * (l.hstride / 16));
+  p.x_wgs = (int)((c.T * (c.D / 8) + kPlanThreads - 1) / kPlanThreads);
+  const unsigned blocks = 1u + (unsigned)p.x_wgs + (unsigned)((p.n_h + p.n_flags / 4 + kPlanThreads - 1) / kPlanThreads);
   const dim3 grid(blocks), block(kPlanThreads);
   if (c.E <= 64) hipLaunchKernelGGL(layer_plan_kernel<1>, grid, block, 0, s, p);
   else if (c.E <= 128) hipLaunchKernelGGL(layer_plan_kernel<2>, grid, block, 0, s, p);
@@ -861,8 +940,7 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t s) {
   a.I = c.I;
   a.T = c.T;
   a.k = c.k;
-  a.gt = p.gt;
-  a.rows = p.rows;
+  a.tiles = p.tiles;
   a.slot_row = p.slot_row;
   a.w = p.w;
   a.head = p.head;
