@@ -50,8 +50,11 @@
 // unit: 85 us instead of 77 for one token of 16 experts, D = 3584, I = 3072.)
 //
 // Visibility.  Results (digits of h, y) are written with device-scope stores,
-// which go through the XCD's L2, and read with device-scope loads, which a stale
-// line of the reader's L2 cannot answer.  y is counted per feature group
+// which go through the XCD's L2.  h is read through the caches at first (the
+// features of a down matrix read the same rows over and over), where a line may
+// be older than the last store to it, but not older than the plan; the check
+// finds that, and the second look is a device-scope load, which no stale line
+// answers.  y is read with device-scope loads only, and counted per feature group
 // (device-scope add, no return) once the stores have completed, that is once a
 // later wait of the in-order vector-memory counter covers them: three stages
 // later, at no cost, or at once where the ring runs dry.  Fences would write
@@ -275,6 +278,7 @@ constexpr int kActBufs = 2;
 constexpr int kNt = 2;               // cache policy of the weight loads: nontemporal
 constexpr int kDevScope = 16;        // cache policy of loads and stores that other XCDs must agree on (sc1)
 constexpr int kSpinLimit = 1 << 21;
+constexpr int kDrawAt = 0;           // a unit's last stages not yet asked for when the next ticket is drawn
 constexpr int kChunk = 4;            // tickets a workgroup draws at once
 constexpr int kNoLane = INT32_MIN;  // buffer offset past every buffer: the lane's store is dropped
 // Counters sit on lines of their own: device-scope adds to one line are served
@@ -507,14 +511,21 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
       }
     }
   };
-  auto load_h = [&](uint8_t* dst, int at) __attribute__((always_inline)) {
+  // (again: the caches' copy turned out to be old)
+  auto load_h = [&](uint8_t* dst, int at, bool again) __attribute__((always_inline)) {
     const __amdgpu_buffer_rsrc_t r =
         __builtin_amdgcn_make_buffer_rsrc((void*)a.h, 0, a.T * a.k * a.hstride, 0x00020000);
     const int so = uni(at);
     const auto l = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, kDevScope);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, kDevScope);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 2048, kDevScope);
+    if (again) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, kDevScope);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, kDevScope);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 2048, kDevScope);
+    } else {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 2048, 0);
+    }
   };
   auto load_x = [&](uint8_t* dst, int at) __attribute__((always_inline)) {
     const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xd, 0, a.T * nst13 * kXRow, 0x00020000);
@@ -551,8 +562,8 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     if (want != 0) {
       uint8_t* const ad = al + abuf_i * kActBytes;
       if (want & 4) {
-        load_h(ad, want0);
-        if (want & 2) load_h(ad + kHRowLds, want1);
+        load_h(ad, want0, false);
+        if (want & 2) load_h(ad + kHRowLds, want1, false);
       } else {
         load_x(ad, want0);
         if (want & 2) load_x(ad + kXRowLds, want1);
@@ -643,8 +654,12 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   uint32_t sub = 0;
   bool down = false;
   for (;;) {
-    if (!drawn) nu = unit_of(claim());
-    drawn = true;
+    // as late as the draw's way there and back allows: a ticket taken early keeps
+    // waves that are free from work that could begin
+    if (!drawn && left <= kDrawAt) {
+      nu = unit_of(claim());
+      drawn = true;
+    }
     const bool eat = inflight == kRing || (left == 0 && nu.kind >= kSum && want == 0);
     bool shorter = false;
     uint32_t wd[2][4][5];
@@ -728,8 +743,8 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
           for (int j = 0; j < 2; ++j) {
             uint8_t* const aj = al + (abuf_c ^ (1 - j)) * kActBytes;
             if (j == 1 && (inflight == 0 || s + 1 >= nst)) break;
-            load_h(aj, at + j * kHRow);
-            if (rows > 1) load_h(aj + kHRowLds, at + a.hstride + j * kHRow);
+            load_h(aj, at + j * kHRow, true);
+            if (rows > 1) load_h(aj + kHRowLds, at + a.hstride + j * kHRow, true);
           }
           wait_vm<0>();
         }
