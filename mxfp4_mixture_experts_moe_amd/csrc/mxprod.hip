@@ -63,18 +63,19 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float v) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows.  A workgroup of eight waves takes groups of 16 weight rows; the
-// waves of a group split K in pieces of 512 (16 blocks: 256 bytes of every
-// row), lane (row rho, quarter g) of a wave loads its row's blocks 4g .. 4g+3
-// of the piece (64 bytes, four lanes 256 in order) and their four scale bytes
-// (one dword), which feed four 16x16x128 instructions.  kw waves share a group
-// (as many as K has pieces, at most eight), 8 / kw groups run side by side; the
-// kw partial sums meet in LDS.  The workgroups are persistent: rows of A are
-// staged (and quantised) once each.
-constexpr int kFewThreads = 512;
-constexpr int kFewWaves = kFewThreads / 64;
+// Few rows.  A workgroup takes groups of 16 weight rows; the waves of a group
+// split K in pieces of 512 (16 blocks: 256 bytes of every row), and lane (row
+// rho, quarter g) of a wave loads blocks g, 4 + g, 8 + g and 12 + g of its row's
+// piece (each load takes 64 bytes of a row in four lanes) and the piece's 16
+// scale bytes, which feed four 16x16x128 instructions.  kw waves share a group,
+// as many as give each the same number of pieces with at most eight waves;
+// 8 / kw groups run side by side; the kw partial sums meet in LDS.  The
+// workgroups are persistent, so rows of A are staged (and quantised) once each,
+// and the pieces of the next two turns are on their way across rounds.
+constexpr int kFewWaves = 8;  // at most, per workgroup
 constexpr int kFewRows = 16;
 constexpr int kFewLds = 80 * 1024;  // two workgroups share a CU
+constexpr int kFewAhead = 2;  // pieces a wave asks for ahead
 
 struct FewArgs {
   const uint8_t* x;  // float rows [M, K] (kX >= 0), or packed codes [M, K/2]
@@ -82,100 +83,148 @@ struct FewArgs {
   const uint8_t* w;
   const uint8_t* ws;
   int M, N, nb;      // nb = K / 32
-  int kw;            // waves per group
+  int kw, rw;        // waves per group, groups side by side
+  int per;           // pieces per wave and group
   int saturate;
   int arow, srow;    // LDS bytes per row of codes and of scales
   void* out;
 };
 
-template <int kX, bool kBf16>
-__global__ __launch_bounds__(kFewThreads, 4) void mx_few_kernel(FewArgs a) {
+// kTail: K is no multiple of 512, so a row's last piece is shorter (and
+// scale rows are not 16-byte aligned).
+template <int kX, bool kBf16, bool kTail>
+__global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kFewLds];
   uint8_t* const codes = lds;                      // [M][arow]
   uint8_t* const scales = lds + a.M * a.arow;      // [M][srow]
   float* const red = reinterpret_cast<float*>(lds + ((a.M * (a.arow + a.srow) + 15) & ~15));  // [2][8 waves][256]
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x, lane = tid & 63, threads = 64 * a.kw * a.rw;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rho = lane & 15, g = lane >> 4;
   const int nb = a.nb, nss = (nb + 15) >> 4;
 
-  // this wave's items: pieces s0, s0 + kw, ... of groups g0, g0 + step, ...
-  const int rw = kFewWaves / a.kw, s0 = wave % a.kw, gw = wave / a.kw;
+  // this wave's turns: pieces s0, s0 + kw, ... of groups g0, g0 + step, ...
+  const int gw = __builtin_amdgcn_readfirstlane(wave / a.kw), s0 = wave - gw * a.kw;
   const int ngroups = (a.N + 15) >> 4;
-  const int64_t rowb = (int64_t)nb * 16;
-  auto load = [&](int grp, int ss, mx_u32x4 (&q)[4], uint32_t& sc) {
-    const int64_t row = min(16 * grp + rho, a.N - 1);
-    const uint8_t* p = a.w + row * rowb;
-    const uint8_t* ps = a.ws + row * nb;
-    if (16 * ss + 16 <= nb) {
+  struct Piece {
+    mx_u32x4 q[4], sc;  // sc: 16 scale bytes; kTail: four dwords of one byte, this lane's blocks'
+  };
+  // Piece ss of group grp, without a branch: one around the loads would make the
+  // wait for a piece a wait for all that was asked for since.  What lies outside
+  // (groups past the last, rows past N, pieces and blocks past K) is outside the
+  // buffer: zeros that cost no traffic.
+  const uint32_t rowb = (uint32_t)nb * 16;
+  auto load = [&](int g_, int s_, Piece& d) __attribute__((always_inline)) {
+    const int grp = __builtin_amdgcn_readfirstlane(g_), ss = __builtin_amdgcn_readfirstlane(s_);
+    const int rows = __builtin_amdgcn_readfirstlane(min(max(a.N - 16 * grp, 0), ss < nss ? 16 : 0));
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + (int64_t)grp * 16 * rowb), 0, rows * rowb, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(a.ws + (int64_t)grp * 16 * nb), 0, rows * nb, 0x00020000);
+    const uint32_t b = (uint32_t)(16 * ss + g), row = (uint32_t)rho * nb;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = __builtin_nontemporal_load(reinterpret_cast<const mx_u32x4*>(p + 256 * ss + 64 * g) + i);
-      sc = load_u32(ps + 16 * ss + 4 * g);
-    } else {  // the last piece: blocks past K are zeros of scale 1
-      const int n = nb - 16 * ss - 4 * g;
-      sc = load_tail(ps, 16 * ss + 4 * g, nb);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at = !kTail || b + 4 * i < (uint32_t)nb ? row + b + 4 * i : 0x0FFFFFFFu;
+      d.q[i] = __builtin_amdgcn_raw_buffer_load_b128(rw, 16 * at, 0, 0);
+      if constexpr (kTail) d.sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, at, 0, 0);
+    }
+    if constexpr (!kTail) d.sc = __builtin_amdgcn_raw_buffer_load_b128(rs, row + 16 * ss, 0, 0);
+  };
+  const int gstep = (int)gridDim.x * a.rw;
+  const int rounds = __builtin_amdgcn_readfirstlane((ngroups + gstep - 1) / gstep);  // the same for every wave: the barriers below
+  int grp = (int)blockIdx.x * a.rw + gw, done = 0;   // done: turns of this round behind us
+  int lgrp = grp, ldone = 0;                         // the same of the next piece to ask for
+  Piece ring[kFewAhead];
+  auto ask = [&](Piece& d) __attribute__((always_inline)) {
+    load(lgrp, s0 + ldone * a.kw, d);
+    if (++ldone == a.per) ldone = 0, lgrp += gstep;
+  };
+  // A, kBatch units a thread at a time: eight float elements (four lanes hold a
+  // block), or a packed block.  The first batch is asked for ahead of the
+  // weights (loads return in order), the rest behind them.
+  constexpr int kBatch = kX < 0 ? 4 : kX == K3MOE_DTYPE_F32 ? 4 : 8, kRaw = kX == K3MOE_DTYPE_F32 ? 2 : 1;
+  const int units = a.M * nb * (kX < 0 ? 1 : 4);
+  mx_u32x4 raw[kBatch][kRaw];
+  uint32_t rsc[kBatch];
+  auto fetch = [&](int u0) __attribute__((always_inline)) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q[i] = mx_u32x4{0u, 0u, 0u, 0u};
-        if (i < n) q[i] = *(reinterpret_cast<const mx_u32x4*>(p + 256 * ss + 64 * g) + i);
+    for (int b = 0; b < kBatch; ++b) {
+      const int u = u0 + b * threads + tid, uc = u < units ? u : kX < 0 ? units - 1 : units - 4 + (tid & 3);
+#pragma unroll
+      for (int h = 0; h < kRaw; ++h) raw[b][h] = reinterpret_cast<const mx_u32x4*>(a.x)[(int64_t)uc * kRaw + h];
+      if constexpr (kX < 0) rsc[b] = a.xs[uc];
+    }
+  };
+  auto stage = [&](int u0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (u0 + b * threads >= units) break;
+      const int u = u0 + b * threads + tid;
+      if constexpr (kX >= 0) {
+        float v[8];
+        mx_load8<kX>(&raw[b][0], v);
+        const uint32_t e = mx_scale_byte(mx_block_top(v), a.saturate != 0);
+        const uint32_t c = mx_codes(v, e);
+        const int m = u / (nb * 4), r = u - m * (nb * 4);
+        if (u < units) {
+          *reinterpret_cast<uint32_t*>(codes + m * a.arow + 4 * r) = c;
+          if ((tid & 3) == 0) scales[m * a.srow + (r >> 2)] = (uint8_t)e;
+        }
+      } else {
+        const int m = u / nb, r = u - m * nb;
+        if (u < units) {
+          *reinterpret_cast<mx_u32x4*>(codes + m * a.arow + 16 * r) = raw[b][0];
+          scales[m * a.srow + r] = (uint8_t)rsc[b];
+        }
       }
     }
   };
-  const int gstep = (int)gridDim.x * rw;
-  int grp = (int)blockIdx.x * rw + gw, ss = s0;
-  mx_u32x4 q[4], qn[4];
-  uint32_t sc = 0, scn = 0;
-  load(min(grp, ngroups - 1), ss, q, sc);  // in flight while A is staged
-
-  const int units = a.M * nb * 4;  // eight elements each; four lanes hold a block
-  for (int u0 = 0; u0 < units; u0 += kFewThreads) {
-    const int u = u0 + tid;
-    const int uc = u < units ? u : units - 4 + (tid & 3);
-    const int m = uc / (nb * 4), r = uc - m * (nb * 4);
-    if constexpr (kX >= 0) {
-      float v[8];
-      mx_load8<kX>(a.x + (int64_t)uc * (kX == K3MOE_DTYPE_F32 ? 32 : 16), v);
-      const uint32_t e = mx_scale_byte(mx_block_top(v), a.saturate != 0);
-      const uint32_t c = mx_codes(v, e);
-      if (u < units) {
-        *reinterpret_cast<uint32_t*>(codes + m * a.arow + 4 * r) = c;
-        if ((tid & 3) == 0) scales[m * a.srow + (r >> 2)] = (uint8_t)e;
-      }
-    } else if (u < units) {
-      *reinterpret_cast<uint32_t*>(codes + m * a.arow + 4 * r) = reinterpret_cast<const uint32_t*>(a.x)[u];
-      if ((tid & 3) == 0) scales[m * a.srow + (r >> 2)] = a.xs[u >> 2];
-    }
+  fetch(0);
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kFewAhead; ++i) ask(ring[i]);
+  asm volatile("" ::: "memory");
+  stage(0);
+  for (int u0 = kBatch * threads; u0 < units; u0 += kBatch * threads) {
+    fetch(u0);
+    stage(u0);
   }
   if ((nb & 15) != 0)  // scales past K, up to the piece's end
-    for (int i = tid; i < a.M * 16; i += kFewThreads)
+    for (int i = tid; i < a.M * 16; i += threads)
       if (nb + (i & 15) < 16 * nss) scales[(i >> 4) * a.srow + nb + (i & 15)] = 127;
   __syncthreads();
 
   const int mrow = min(rho, a.M - 1);  // columns past M repeat the last row and are never stored
   const uint8_t* const brow = codes + mrow * a.arow;
   const uint8_t* const bsc = scales + mrow * a.srow;
-  int par = 0;
-  const int rounds = (ngroups + gstep - 1) / gstep;  // the same for every wave: the barriers below
-  for (int rd = 0; rd < rounds; ++rd, grp += gstep) {
-    f32x4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = acc0;
-    for (; ss < nss; ss += a.kw) {
-      const bool more = ss + a.kw < nss;
-      const int gn = more ? grp : grp + gstep;
-      load(min(gn, ngroups - 1), more ? ss + a.kw : s0, qn, scn);
-      const uint32_t bs = *reinterpret_cast<const uint32_t*>(bsc + 16 * ss + 4 * g);
-      mx_u32x4 b[4];
+  // byte g of four dwords, as one
+  const uint32_t pick = 0x0c0c0400u + 0x0101u * (uint32_t)g;
+  auto bytes = [&](mx_u32x4 v) __attribute__((always_inline)) -> uint32_t {
+    return __builtin_amdgcn_perm(v[1], v[0], pick) | __builtin_amdgcn_perm(v[3], v[2], pick) << 16;
+  };
+  f32x4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = acc0;
+  int par = 0, rd = 0;
+  auto turn = [&](Piece& cur) __attribute__((always_inline)) {
+    const int ss = s0 + done * a.kw, sl = min(ss, nss - 1);
+    mx_u32x4 b[4], bs4;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) b[i] = *reinterpret_cast<const mx_u32x4*>(brow + 16 * min(16 * ss + 4 * g + i, nb - 1));
-      acc0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(q[0]), operand(b[0]), acc0, kFp4, kFp4, 0, (int)sc, 0, (int)bs);
-      acc1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(q[1]), operand(b[1]), acc1, kFp4, kFp4, 1, (int)sc, 1, (int)bs);
-      acc0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(q[2]), operand(b[2]), acc0, kFp4, kFp4, 2, (int)sc, 2, (int)bs);
-      acc1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(q[3]), operand(b[3]), acc1, kFp4, kFp4, 3, (int)sc, 3, (int)bs);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = qn[i];
-      sc = scn;
+    for (int i = 0; i < 4; ++i) {
+      b[i] = *reinterpret_cast<const mx_u32x4*>(brow + 16 * min(16 * sl + 4 * i + g, nb - 1));
+      bs4[i] = *reinterpret_cast<const uint32_t*>(bsc + 16 * sl + 4 * i);
     }
-    ss = s0;
+    const uint32_t bs = bytes(bs4);
+    uint32_t sc;
+    if constexpr (kTail)
+      sc = (cur.sc[0] | cur.sc[1] << 8) | (cur.sc[2] | cur.sc[3] << 8) << 16;
+    else
+      sc = bytes(cur.sc);
+    acc0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(cur.q[0]), operand(b[0]), acc0, kFp4, kFp4, 0, (int)sc, 0, (int)bs);
+    acc1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(cur.q[1]), operand(b[1]), acc1, kFp4, kFp4, 1, (int)sc, 1, (int)bs);
+    acc0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(cur.q[2]), operand(b[2]), acc0, kFp4, kFp4, 2, (int)sc, 2, (int)bs);
+    acc1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand(cur.q[3]), operand(b[3]), acc1, kFp4, kFp4, 3, (int)sc, 3, (int)bs);
+    ask(cur);
+    if (++done < a.per) return;
+    done = 0;
     f32x4 sum = acc0 + acc1;
+    acc0 = acc1 = f32x4{0.f, 0.f, 0.f, 0.f};
     if (a.kw > 1) {
       float* const slot = red + (par * kFewWaves + wave) * 256;
       *reinterpret_cast<f32x4*>(slot + 4 * lane) = sum;
@@ -199,6 +248,15 @@ __global__ __launch_bounds__(kFewThreads, 4) void mx_few_kernel(FewArgs a) {
         for (int v = 0; v < 4; ++v)
           if (n + v < a.N) store_out<kBf16>(a.out, at + v, sum[v]);
       }
+    }
+    grp += gstep;
+    ++rd;
+  };
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < kFewAhead; ++i) {
+      turn(ring[i]);
+      if (rd == rounds) return;
     }
   }
 }
@@ -422,14 +480,18 @@ size_t few_lds(int64_t M, int nb) { return (size_t)M * (few_arow(nb) + few_srow(
 
 template <int kX>
 hipError_t launch_few(const FewArgs& a, bool bf16, hipStream_t s) {
-  const int ngroups = (a.N + 15) / 16, rw = kFewWaves / a.kw;
-  const int64_t wgs = (ngroups + rw - 1) / rw;
-  const int64_t most = 2 * device_cu_count();
-  const dim3 grid((unsigned)(wgs < most ? wgs : most)), block(kFewThreads);
-  if (bf16)
-    hipLaunchKernelGGL((mx_few_kernel<kX, true>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((mx_few_kernel<kX, false>), grid, block, 0, s, a);
+  // the fewest rounds that two workgroups per CU allow, and as few workgroups as
+  // that leaves: all have the same number of rounds, and A is staged less often
+  const int ngroups = (a.N + 15) / 16, most = 2 * device_cu_count() * a.rw;
+  const int rounds = (ngroups + most - 1) / most;
+  const int64_t wgs = (ngroups + (int64_t)rounds * a.rw - 1) / ((int64_t)rounds * a.rw);
+  const dim3 grid((unsigned)wgs), block((unsigned)(64 * a.kw * a.rw));
+  auto go = [&](auto b, auto t) { hipLaunchKernelGGL((mx_few_kernel<kX, decltype(b)::value, decltype(t)::value>), grid, block, 0, s, a); };
+  const bool tail = a.nb % 16 != 0;
+  if (bf16 && tail) go(std::true_type{}, std::true_type{});
+  else if (bf16) go(std::true_type{}, std::false_type{});
+  else if (tail) go(std::false_type{}, std::true_type{});
+  else go(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 
@@ -459,7 +521,9 @@ hipError_t launch_mx_few(const void* x, int x_dtype, const uint8_t* xs, const ui
   a.N = N;
   a.nb = K / 32;
   const int nss = (a.nb + 15) / 16;
-  a.kw = nss >= 8 ? 8 : nss >= 4 ? 4 : nss >= 2 ? 2 : 1;
+  a.per = (nss + kFewWaves - 1) / kFewWaves;
+  a.kw = (nss + a.per - 1) / a.per;
+  a.rw = kFewWaves / a.kw;
   a.saturate = saturate;
   a.arow = few_arow(a.nb);
   a.srow = few_srow(a.nb);
