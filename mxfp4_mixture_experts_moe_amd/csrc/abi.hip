@@ -588,13 +588,11 @@ int mxfp4_matmul(const uint8_t* a_packed, const uint8_t* a_scale, const uint8_t*
     return K3MOE_ERR_ALIGN;
   const bool bf16 = out_dtype == K3MOE_DTYPE_BF16;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (mx_few_supported(M, (int)(K / 32)))
-    return device_status(launch_mx_few(a_packed, -1, a_scale, w_packed, w_scale, M, (int)N, (int)K, 0, bf16, out, s));
-  return device_status(launch_mx_tiles(a_packed, a_scale, w_packed, w_scale, M, (int)N, (int)K, bf16, out, s));
+  return device_status(launch_mx_product(a_packed, a_scale, w_packed, w_scale, M, (int)N, (int)K, bf16, out, s));
 }
 
 size_t mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
-  if (!mx_product_ok(M, N, K) || M == 0 || N == 0 || mx_few_supported(M, (int)(K / 32))) return 0;
+  if (!mx_product_ok(M, N, K) || M == 0 || N == 0 || mx_few_fused(M, K)) return 0;
   return align_up((size_t)M * (K / 2), 256) + align_up((size_t)M * (K / 32), 256);
 }
 
@@ -618,7 +616,7 @@ int mxfp4_linear(const void* x, int32_t x_dtype, const uint8_t* w_packed, const 
   uint8_t* const as = ap + align_up((size_t)M * (K / 2), 256);
   const hipError_t e = launch_quantize(x, x_dtype, M * K, saturate, ap, as, s);
   if (e != hipSuccess) return K3MOE_ERR_DEVICE;
-  return device_status(launch_mx_tiles(ap, as, w_packed, w_scale, M, (int)N, (int)K, bf16, out, s));
+  return device_status(launch_mx_product(ap, as, w_packed, w_scale, M, (int)N, (int)K, bf16, out, s));
 }
 
 size_t moe_mxfp4_layer_workspace_size(int64_t T, int32_t D, int32_t I, int32_t E, int32_t k) {

@@ -71,13 +71,14 @@ hipError_t launch_quantize(const void* x, int x_dtype, int64_t n, int saturate, 
                            hipStream_t s);
 hipError_t launch_unpack(const uint8_t* packed, const uint8_t* scale, int64_t n, int out_bf16, void* out,
                          hipStream_t s);
-// Products of microscaled 4-bit matrices: the few-row kernel (A packed when xs
-// is set, else float rows it quantises itself) and the tile kernels.
-bool mx_few_supported(int64_t M, int nb);
+// Products of microscaled 4-bit matrices: of packed rows (few rows or tiles),
+// and of a few float rows that the kernel quantises itself (A packed when xs is
+// set) where mx_few_fused says so.
+bool mx_few_fused(int64_t M, int64_t K);
 hipError_t launch_mx_few(const void* x, int x_dtype, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int64_t M,
                          int N, int K, int saturate, bool out_bf16, void* out, hipStream_t s);
-hipError_t launch_mx_tiles(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t M, int N,
-                           int K, bool out_bf16, void* out, hipStream_t s);
+hipError_t launch_mx_product(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t M, int N,
+                             int K, bool out_bf16, void* out, hipStream_t s);
 
 // Stage-tiled order of an MXFP4 matrix of N rows x nb 17-byte blocks (the
 // order mxfp4_tile writes and the FFN kernels read): rows in groups of 16 and

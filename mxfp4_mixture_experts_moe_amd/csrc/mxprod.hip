@@ -71,10 +71,15 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float v) {
 // as many as give each the same number of pieces with at most eight waves;
 // 8 / kw groups run side by side; the kw partial sums meet in LDS.  The
 // workgroups are persistent, so rows of A are staged (and quantised) once each,
-// and the pieces of the next two turns are on their way across rounds.
+// and the pieces of the next two turns are on their way across rounds.  More
+// than 16 rows of A (packed) go 16 at a time, side by side in the grid.
 constexpr int kFewWaves = 8;  // at most, per workgroup
 constexpr int kFewRows = 16;
 constexpr int kFewLds = 80 * 1024;  // two workgroups share a CU
+// The linear layer quantises rows in every workgroup up to this many elements,
+// by a launch of its own beyond (about 3 us: 8 x 3584, 3.4 us more than the
+// packed product in the kernel; 8 x 7168, 4.4; 4 x 7168, 0.9; 16 x 7168, 9).
+constexpr int64_t kFewFused = 32768;
 constexpr int kFewAhead = 2;  // pieces a wave asks for ahead
 
 struct FewArgs {
@@ -82,7 +87,8 @@ struct FewArgs {
   const uint8_t* xs; // scales of packed rows
   const uint8_t* w;
   const uint8_t* ws;
-  int M, N, nb;      // nb = K / 32
+  int64_t M;
+  int N, nb;         // nb = K / 32
   int kw, rw;        // waves per group, groups side by side
   int per;           // pieces per wave and group
   int saturate;
@@ -95,9 +101,11 @@ struct FewArgs {
 template <int kX, bool kBf16, bool kTail>
 __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kFewLds];
-  uint8_t* const codes = lds;                      // [M][arow]
-  uint8_t* const scales = lds + a.M * a.arow;      // [M][srow]
-  float* const red = reinterpret_cast<float*>(lds + ((a.M * (a.arow + a.srow) + 15) & ~15));  // [2][8 waves][256]
+  const int64_t m0 = (int64_t)blockIdx.y * kFewRows;
+  const int M = (int)(a.M - m0 < kFewRows ? a.M - m0 : kFewRows);
+  uint8_t* const codes = lds;                    // [M][arow]
+  uint8_t* const scales = lds + M * a.arow;      // [M][srow]
+  float* const red = reinterpret_cast<float*>(lds + ((M * (a.arow + a.srow) + 15) & ~15));  // [2][8 waves][256]
   const int tid = threadIdx.x, lane = tid & 63, threads = 64 * a.kw * a.rw;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int rho = lane & 15, g = lane >> 4;
@@ -137,62 +145,69 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
     load(lgrp, s0 + ldone * a.kw, d);
     if (++ldone == a.per) ldone = 0, lgrp += gstep;
   };
-  // A, kBatch units a thread at a time: eight float elements (four lanes hold a
-  // block), or a packed block.  The first batch is asked for ahead of the
-  // weights (loads return in order), the rest behind them.
-  constexpr int kBatch = kX < 0 ? 4 : kX == K3MOE_DTYPE_F32 ? 4 : 8, kRaw = kX == K3MOE_DTYPE_F32 ? 2 : 1;
-  const int units = a.M * nb * (kX < 0 ? 1 : 4);
+  // A, a unit per thread and turn, kBatch turns at a time.  Float rows: units of
+  // eight elements (four lanes hold a block), a row at a time, which spares a
+  // division per unit; packed ones: blocks, all rows' in order.  The first batch
+  // is asked for ahead of the weights (loads return in order), the rest behind
+  // them.
+  constexpr bool kFlat = kX < 0;
+  constexpr int kBatch = kFlat || kX == K3MOE_DTYPE_F32 ? 4 : 8, kRaw = kX == K3MOE_DTYPE_F32 ? 2 : 1;
+  const int rows = kFlat ? 1 : M, units = kFlat ? M * nb : 4 * nb;  // of a row
+  const int turns = __builtin_amdgcn_readfirstlane((units + threads - 1) / threads);
   mx_u32x4 raw[kBatch][kRaw];
   uint32_t rsc[kBatch];
-  auto fetch = [&](int u0) __attribute__((always_inline)) {
+  int fm = 0, ft = 0, sm = 0, st = 0;  // row and turn to fetch and to stage next
+  auto fetch = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int u = u0 + b * threads + tid, uc = u < units ? u : kX < 0 ? units - 1 : units - 4 + (tid & 3);
+      const int u = min(ft * threads + tid, kFlat ? units - 1 : units - 4 + (tid & 3));
+      const int64_t at = kFlat ? m0 * nb + u : (m0 + min(fm, rows - 1)) * units + u;
 #pragma unroll
-      for (int h = 0; h < kRaw; ++h) raw[b][h] = reinterpret_cast<const mx_u32x4*>(a.x)[(int64_t)uc * kRaw + h];
-      if constexpr (kX < 0) rsc[b] = a.xs[uc];
+      for (int h = 0; h < kRaw; ++h) raw[b][h] = reinterpret_cast<const mx_u32x4*>(a.x)[at * kRaw + h];
+      if constexpr (kFlat) rsc[b] = a.xs[at];
+      if (++ft == turns) ft = 0, ++fm;
     }
   };
-  auto stage = [&](int u0) __attribute__((always_inline)) {
+  auto stage = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      if (u0 + b * threads >= units) break;
-      const int u = u0 + b * threads + tid;
-      if constexpr (kX >= 0) {
-        float v[8];
-        mx_load8<kX>(&raw[b][0], v);
-        const uint32_t e = mx_scale_byte(mx_block_top(v), a.saturate != 0);
-        const uint32_t c = mx_codes(v, e);
-        const int m = u / (nb * 4), r = u - m * (nb * 4);
-        if (u < units) {
-          *reinterpret_cast<uint32_t*>(codes + m * a.arow + 4 * r) = c;
-          if ((tid & 3) == 0) scales[m * a.srow + (r >> 2)] = (uint8_t)e;
-        }
-      } else {
+      if (sm >= rows) break;
+      const int u = st * threads + tid;
+      if constexpr (kFlat) {
         const int m = u / nb, r = u - m * nb;
         if (u < units) {
           *reinterpret_cast<mx_u32x4*>(codes + m * a.arow + 16 * r) = raw[b][0];
           scales[m * a.srow + r] = (uint8_t)rsc[b];
         }
+      } else {
+        float v[8];
+        mx_load8<kX>(&raw[b][0], v);
+        const uint32_t e = mx_scale_byte(mx_block_top(v), a.saturate != 0);
+        const uint32_t c = mx_codes(v, e);
+        if (u < units) {
+          *reinterpret_cast<uint32_t*>(codes + sm * a.arow + 4 * u) = c;
+          if ((tid & 3) == 0) scales[sm * a.srow + (u >> 2)] = (uint8_t)e;
+        }
       }
+      if (++st == turns) st = 0, ++sm;
     }
   };
-  fetch(0);
+  fetch();
   asm volatile("" ::: "memory");
 #pragma unroll
   for (int i = 0; i < kFewAhead; ++i) ask(ring[i]);
   asm volatile("" ::: "memory");
-  stage(0);
-  for (int u0 = kBatch * threads; u0 < units; u0 += kBatch * threads) {
-    fetch(u0);
-    stage(u0);
+  stage();
+  while (sm < rows) {
+    fetch();
+    stage();
   }
   if ((nb & 15) != 0)  // scales past K, up to the piece's end
-    for (int i = tid; i < a.M * 16; i += threads)
+    for (int i = tid; i < M * 16; i += threads)
       if (nb + (i & 15) < 16 * nss) scales[(i >> 4) * a.srow + nb + (i & 15)] = 127;
   __syncthreads();
 
-  const int mrow = min(rho, a.M - 1);  // columns past M repeat the last row and are never stored
+  const int mrow = min(rho, M - 1);  // columns past M repeat the last row and are never stored
   const uint8_t* const brow = codes + mrow * a.arow;
   const uint8_t* const bsc = scales + mrow * a.srow;
   // byte g of four dwords, as one
@@ -233,9 +248,9 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
         for (int i = 1; i < a.kw; ++i) sum += *reinterpret_cast<const f32x4*>(slot + 256 * i + 4 * lane);
       par ^= 1;
     }
-    if (s0 == 0 && grp < ngroups && rho < a.M) {
+    if (s0 == 0 && grp < ngroups && rho < M) {
       const int n = 16 * grp + 4 * g;
-      const int64_t at = (int64_t)rho * a.N + n;
+      const int64_t at = (m0 + rho) * a.N + n;
       if (n + 4 <= a.N && (a.N & 3) == 0) {
         if constexpr (kBf16) {
           typedef __bf16 b4 __attribute__((ext_vector_type(4)));
@@ -270,7 +285,6 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
 // c ^ ((r >> 2) & 3) of the row's 64 bytes, so the 16-lane groups of a read
 // touch every bank once.  Scales go straight to registers, eight bytes (two
 // steps) of a row at a time.
-constexpr int kTileThreads = 256;
 constexpr int kXcds = 8;
 
 struct TileArgs {
@@ -289,11 +303,12 @@ __device__ __forceinline__ void wait_vm() {
 // refilled after it) and its loads of the next step's buffer have landed.
 __device__ __forceinline__ void ring_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int B, bool kBf16>
-__global__ __launch_bounds__(kTileThreads) void mx_tile_kernel(TileArgs t) {
-  constexpr int kT = B / 64;              // 32-row operand tiles per wave and side
+template <int B, int kWaves, bool kStaged, bool kBf16>
+__global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
+  constexpr int kWm = kWaves / 2;         // waves along M; two along N
+  constexpr int kTm = B / (32 * kWm), kTn = B / 64;  // 32-row operand tiles per wave
   constexpr int kStageDw = 2 * B * 16;    // dwords of a stage: B rows of A, B rows of W, 64 bytes each
-  constexpr int kLoads = 2 * B / 64;      // 1 KB loads per wave and stage
+  constexpr int kLoads = 2 * B / (16 * kWaves);  // 1 KB loads per wave and stage
   // one array per buffer, so that the compiler sees that a read of one buffer
   // does not depend on the loads in flight into the others
   __shared__ __attribute__((aligned(256))) uint32_t l0[kStageDw], l1[kStageDw], l2[kStageDw], l3[kStageDw];
@@ -323,9 +338,9 @@ __global__ __launch_bounds__(kTileThreads) void mx_tile_kernel(TileArgs t) {
   const int nrows = t.N - n0 < B ? t.N - n0 : B;
   const int nsteps = (nb + 3) >> 2;
 
-  // loads: wave w fills LDS rows 2B/4 * w ..; a 1 KB load holds 16 rows
-  const bool from_a = wave < 2;
-  const int lrow0 = (wave & 1) * (B / 2);  // first row within A or W
+  // loads: wave w fills LDS rows 2B / kWaves * w ..; a 1 KB load holds 16 rows
+  const bool from_a = wave < kWaves / 2;
+  const int lrow0 = wave % (kWaves / 2) * (2 * B / kWaves);  // first row within A or W
   const uint8_t* const src = from_a ? t.a + m0 * rowb : t.w + (int64_t)n0 * rowb;
   const int srows = from_a ? mrows : nrows;
   const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)src, 0, (int)(srows * rowb), 0x00020000);
@@ -337,7 +352,7 @@ __global__ __launch_bounds__(kTileThreads) void mx_tile_kernel(TileArgs t) {
     voff[j] = (uint32_t)min(r, srows - 1) * rowb + 16 * c;
   }
   auto issue = [&](int step, uint32_t* buf) {
-    uint32_t* dst = buf + (B / 2) * wave * 16;
+    uint32_t* dst = buf + (2 * B / kWaves) * wave * 16;
     const int so = 64 * step;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j) {
@@ -347,50 +362,62 @@ __global__ __launch_bounds__(kTileThreads) void mx_tile_kernel(TileArgs t) {
   };
 
   // scales of this lane's rows
-  const uint8_t* ap[kT];
-  const uint8_t* wp[kT];
+  const uint8_t* ap[kTm];
+  const uint8_t* wp[kTn];
 #pragma unroll
-  for (int i = 0; i < kT; ++i) {
-    ap[i] = t.as + (m0 + min(wm * (B / 2) + 32 * i + r32, mrows - 1)) * nb;
-    wp[i] = t.ws + (int64_t)(n0 + min(wn * (B / 2) + 32 * i + r32, nrows - 1)) * nb;
-  }
-  uint2 sa[kT], sw[kT];  // eight scale bytes of the next pair of steps
+  for (int i = 0; i < kTm; ++i) ap[i] = t.as + (m0 + min(wm * (B / kWm) + 32 * i + r32, mrows - 1)) * nb;
+#pragma unroll
+  for (int i = 0; i < kTn; ++i) wp[i] = t.ws + (int64_t)(n0 + min(wn * (B / 2) + 32 * i + r32, nrows - 1)) * nb;
+  uint2 sa[kTm], sw[kTn];  // eight scale bytes of the next pair of steps (kStaged: of this one)
   auto load_scales = [&](int pair) {
 #pragma unroll
-    for (int i = 0; i < kT; ++i) {
-      sa[i] = load_u64(ap[i] + 8 * pair);
-      sw[i] = load_u64(wp[i] + 8 * pair);
-    }
+    for (int i = 0; i < kTm; ++i) sa[i] = load_u64(ap[i] + 8 * pair);
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) sw[i] = load_u64(wp[i] + 8 * pair);
   };
+  // kStaged: 16 bytes (four steps) of each of the tile's rows through LDS
+  constexpr int kScaleLoads = 2 * B / 64;  // of 64 rows; one per wave (some twice where there are more waves)
+  __shared__ __attribute__((aligned(256))) uint32_t lsc[kStaged ? 2 * 2 * B * 4 : 1];
+  const int sload = wave % kScaleLoads;
+  const bool s_a = sload < kScaleLoads / 2;
+  const int slrows = s_a ? mrows : nrows;
+  const __amdgpu_buffer_rsrc_t rsc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(s_a ? t.as + m0 * nb : t.ws + (int64_t)n0 * nb), 0, slrows * nb, 0x00020000);
+  const int svoff = min(sload % (kScaleLoads / 2) * 64 + lane, slrows - 1) * nb;
+  auto issue_scales = [&](int group) {
+    uint32_t* dst = lsc + (group & 1) * 2 * B * 4 + sload * 256;
+    const int so = 16 * group, vo = svoff;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsc, dst, 16, vo, so, 0, 0);
+  };
+  mx_u32x4 ga[kTm], gw[kTn];
   const uint32_t ssel = h ? 0x07060302u : 0x05040100u;  // bytes 2h, 2h+1 of both steps
-  uint32_t ca[kT], cw[kT];
+  uint32_t ca[kTm], cw[kTn];
 
-  f32x16 acc[kT][kT];
+  f32x16 acc[kTm][kTn];
 #pragma unroll
-  for (int i = 0; i < kT; ++i)
+  for (int i = 0; i < kTm; ++i)
 #pragma unroll
-    for (int j = 0; j < kT; ++j) acc[i][j] = f32x16{};
+    for (int j = 0; j < kTn; ++j) acc[i][j] = f32x16{};
 
   const uint32_t pos[2] = {16u * (uint32_t)((2 * h) ^ ((lane >> 2) & 3)), 16u * (uint32_t)((2 * h + 1) ^ ((lane >> 2) & 3))};
-  const uint32_t arow = (uint32_t)(wm * (B / 2) + r32) * 64, wrow = (uint32_t)(B + wn * (B / 2) + r32) * 64;
+  const uint32_t arow = (uint32_t)(wm * (B / kWm) + r32) * 64, wrow = (uint32_t)(B + wn * (B / 2) + r32) * 64;
   // Instruction kk (0, 1) of a step held in `buf`; scale byte `sel` of ca / cw.
   // keep: false zeroes this lane's block of A (blocks past K).
   auto part = [&](const uint32_t* buf, auto kc, auto selc, bool keep) {
     constexpr int kk = decltype(kc)::value, sel = decltype(selc)::value;
     const uint8_t* const l = reinterpret_cast<const uint8_t*>(buf);
-    mx_u32x4 fa[kT], fw[kT];
+    mx_u32x4 fa[kTm], fw[kTn];
 #pragma unroll
-    for (int i = 0; i < kT; ++i) {
-      fa[i] = *reinterpret_cast<const mx_u32x4*>(l + arow + 2048 * i + pos[kk]);
-      fw[i] = *reinterpret_cast<const mx_u32x4*>(l + wrow + 2048 * i + pos[kk]);
-    }
+    for (int i = 0; i < kTm; ++i) fa[i] = *reinterpret_cast<const mx_u32x4*>(l + arow + 2048 * i + pos[kk]);
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) fw[i] = *reinterpret_cast<const mx_u32x4*>(l + wrow + 2048 * i + pos[kk]);
     if (!keep)
 #pragma unroll
-      for (int i = 0; i < kT; ++i) fa[i] = mx_u32x4{0u, 0u, 0u, 0u};
+      for (int i = 0; i < kTm; ++i) fa[i] = mx_u32x4{0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int i = 0; i < kT; ++i)
+    for (int i = 0; i < kTm; ++i)
 #pragma unroll
-      for (int j = 0; j < kT; ++j)
+      for (int j = 0; j < kTn; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand(fa[i]), operand(fw[j]), acc[i][j], kFp4, kFp4,
                                                                     sel, (int)ca[i], sel, (int)cw[j]);
   };
@@ -409,14 +436,31 @@ __global__ __launch_bounds__(kTileThreads) void mx_tile_kernel(TileArgs t) {
   const int last_pair = 2 * full - 1;
   auto step = [&](auto uc, int q, uint32_t* cur, uint32_t* refill) {
     constexpr int u = decltype(uc)::value;
-    wait_vm<2 * kLoads + 2 * kT>();
+    if constexpr (kStaged)
+      wait_vm<2 * kLoads + (u == 1 || u == 2 ? 1 : 0)>();
+    else
+      wait_vm<2 * kLoads + kTm + kTn>();
     ring_barrier();
-    if constexpr (u % 2 == 0) {
+    if constexpr (kStaged && u == 0) {
+      const uint32_t* const l = lsc + ((q >> 2) & 1) * 2 * B * 4;
 #pragma unroll
-      for (int i = 0; i < kT; ++i) {
-        ca[i] = __builtin_amdgcn_perm(sa[i].y, sa[i].x, ssel);
-        cw[i] = __builtin_amdgcn_perm(sw[i].y, sw[i].x, ssel);
-      }
+      for (int i = 0; i < kTm; ++i) ga[i] = *reinterpret_cast<const mx_u32x4*>(l + 4 * (wm * (B / kWm) + 32 * i + r32));
+#pragma unroll
+      for (int i = 0; i < kTn; ++i) gw[i] = *reinterpret_cast<const mx_u32x4*>(l + 4 * (B + wn * (B / 2) + 32 * i + r32));
+      asm volatile("" ::: "memory");
+      issue_scales((q >> 2) + 1);
+      asm volatile("" ::: "memory");
+    }
+    if constexpr (kStaged && u % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < kTm; ++i) ca[i] = __builtin_amdgcn_perm(ga[i][u + 1], ga[i][u], ssel);
+#pragma unroll
+      for (int i = 0; i < kTn; ++i) cw[i] = __builtin_amdgcn_perm(gw[i][u + 1], gw[i][u], ssel);
+    } else if constexpr (u % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < kTm; ++i) ca[i] = __builtin_amdgcn_perm(sa[i].y, sa[i].x, ssel);
+#pragma unroll
+      for (int i = 0; i < kTn; ++i) cw[i] = __builtin_amdgcn_perm(sw[i].y, sw[i].x, ssel);
       load_scales(min((q >> 1) + 1, last_pair));
       asm volatile("" ::: "memory");
     }
@@ -424,9 +468,11 @@ __global__ __launch_bounds__(kTileThreads) void mx_tile_kernel(TileArgs t) {
     part(cur, C0{}, std::integral_constant<int, 2 * (u % 2)>{}, true);
     part(cur, C1{}, std::integral_constant<int, 2 * (u % 2) + 1>{}, true);
   };
+  if constexpr (kStaged) issue_scales(0);
+  asm volatile("" ::: "memory");
   issue(0, l0);
   issue(1, l1);
-  if (full > 0) load_scales(0);
+  if (!kStaged && full > 0) load_scales(0);
   asm volatile("" ::: "memory");
   issue(2, l2);
   for (int q = 0; q < 4 * full; q += 4) {
@@ -449,24 +495,23 @@ __global__ __launch_bounds__(kTileThreads) void mx_tile_kernel(TileArgs t) {
     const int b0 = 4 * (4 * full + u);
     const uint32_t* const buf = u == 0 ? l0 : u == 1 ? l1 : u == 2 ? l2 : l3;
 #pragma unroll
-    for (int i = 0; i < kT; ++i) {
-      ca[i] = load_tail(ap[i], b0 + 2 * h, nb);
-      cw[i] = load_tail(wp[i], b0 + 2 * h, nb);
-    }
+    for (int i = 0; i < kTm; ++i) ca[i] = load_tail(ap[i], b0 + 2 * h, nb);
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) cw[i] = load_tail(wp[i], b0 + 2 * h, nb);
     part(buf, C0{}, C0{}, b0 + 2 * h < nb);
     part(buf, C1{}, C1{}, b0 + 2 * h + 1 < nb);
   }
 
   // lane holds column n = lane % 32, rows 8 * (v / 4) + 4 * h + v % 4
 #pragma unroll
-  for (int i = 0; i < kT; ++i)
+  for (int i = 0; i < kTm; ++i)
 #pragma unroll
-    for (int j = 0; j < kT; ++j) {
+    for (int j = 0; j < kTn; ++j) {
       const int n = wn * (B / 2) + 32 * j + r32;
       if (n >= nrows) continue;
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int m = wm * (B / 2) + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+        const int m = wm * (B / kWm) + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
         if (m < mrows) store_out<kBf16>(t.out, (m0 + m) * (int64_t)t.N + n0 + n, acc[i][j][v]);
       }
     }
@@ -476,16 +521,17 @@ __global__ __launch_bounds__(kTileThreads) void mx_tile_kernel(TileArgs t) {
 // units, so 16 rows start in different banks), rows of scales, partial sums.
 int few_arow(int nb) { return 16 * (nb | 1); }
 int few_srow(int nb) { return (nb + 15) / 16 * 16 + 4; }
-size_t few_lds(int64_t M, int nb) { return (size_t)M * (few_arow(nb) + few_srow(nb)) + 12 + 2 * kFewWaves * 256 * sizeof(float); }
+size_t few_lds(int64_t M, int nb) { return (size_t)(M < kFewRows ? M : kFewRows) * (few_arow(nb) + few_srow(nb)) + 12 + 2 * kFewWaves * 256 * sizeof(float); }
 
 template <int kX>
 hipError_t launch_few(const FewArgs& a, bool bf16, hipStream_t s) {
   // the fewest rounds that two workgroups per CU allow, and as few workgroups as
   // that leaves: all have the same number of rounds, and A is staged less often
+  const unsigned chunks = (unsigned)((a.M + kFewRows - 1) / kFewRows);
   const int ngroups = (a.N + 15) / 16, most = 2 * device_cu_count() * a.rw;
   const int rounds = (ngroups + most - 1) / most;
   const int64_t wgs = (ngroups + (int64_t)rounds * a.rw - 1) / ((int64_t)rounds * a.rw);
-  const dim3 grid((unsigned)wgs), block((unsigned)(64 * a.kw * a.rw));
+  const dim3 grid((unsigned)wgs, chunks), block((unsigned)(64 * a.kw * a.rw));
   auto go = [&](auto b, auto t) { hipLaunchKernelGGL((mx_few_kernel<kX, decltype(b)::value, decltype(t)::value>), grid, block, 0, s, a); };
   const bool tail = a.nb % 16 != 0;
   if (bf16 && tail) go(std::true_type{}, std::true_type{});
@@ -495,20 +541,34 @@ hipError_t launch_few(const FewArgs& a, bool bf16, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int B>
+template <int B, int kWaves>
 hipError_t launch_square(const TileArgs& t, bool bf16, hipStream_t s) {
   const int64_t total = ((t.M + B - 1) / B) * ((t.N + B - 1) / B);
-  const dim3 grid((unsigned)total), block(kTileThreads);
-  if (bf16)
-    hipLaunchKernelGGL((mx_tile_kernel<B, true>), grid, block, 0, s, t);
-  else
-    hipLaunchKernelGGL((mx_tile_kernel<B, false>), grid, block, 0, s, t);
+  const dim3 grid((unsigned)total), block(kWaves * 64);
+  auto go = [&](auto st, auto b) {
+    hipLaunchKernelGGL((mx_tile_kernel<B, kWaves, decltype(st)::value, decltype(b)::value>), grid, block, 0, s, t);
+  };
+  const bool staged = t.nb % 16 == 0;
+  if (staged && bf16) go(std::true_type{}, std::true_type{});
+  else if (staged) go(std::true_type{}, std::false_type{});
+  else if (bf16) go(std::false_type{}, std::true_type{});
+  else go(std::false_type{}, std::false_type{});
   return hipGetLastError();
 }
 
 }  // namespace
 
-bool mx_few_supported(int64_t M, int nb) { return M <= kFewRows && few_lds(M, nb) <= kFewLds; }
+// Waves per group and groups side by side of the few-row kernel.
+static void few_split(int nb, int& per, int& kw, int& rw) {
+  const int nss = (nb + 15) / 16;
+  per = (nss + kFewWaves - 1) / kFewWaves;
+  kw = (nss + per - 1) / per;
+  rw = kFewWaves / kw;
+}
+
+bool mx_few_fused(int64_t M, int64_t K) {
+  return M <= kFewRows && M * K <= kFewFused && few_lds(M, (int)(K / 32)) <= kFewLds;
+}
 
 hipError_t launch_mx_few(const void* x, int x_dtype, const uint8_t* xs, const uint8_t* w, const uint8_t* ws, int64_t M,
                          int N, int K, int saturate, bool out_bf16, void* out, hipStream_t s) {
@@ -517,13 +577,10 @@ hipError_t launch_mx_few(const void* x, int x_dtype, const uint8_t* xs, const ui
   a.xs = xs;
   a.w = w;
   a.ws = ws;
-  a.M = (int)M;
+  a.M = M;
   a.N = N;
   a.nb = K / 32;
-  const int nss = (a.nb + 15) / 16;
-  a.per = (nss + kFewWaves - 1) / kFewWaves;
-  a.kw = (nss + a.per - 1) / a.per;
-  a.rw = kFewWaves / a.kw;
+  few_split(a.nb, a.per, a.kw, a.rw);
   a.saturate = saturate;
   a.arow = few_arow(a.nb);
   a.srow = few_srow(a.nb);
@@ -534,8 +591,17 @@ hipError_t launch_mx_few(const void* x, int x_dtype, const uint8_t* xs, const ui
   return launch_few<K3MOE_DTYPE_F16>(a, out_bf16, s);
 }
 
-hipError_t launch_mx_tiles(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t M, int N,
-                           int K, bool out_bf16, void* out, hipStream_t s) {
+// Few rows: all that fit the kernel.  More, with a long K: where the groups of
+// every 16 rows are resident at once (77 x 1003 x 4128: 32 tiles of 64 x 64, 13.0
+// us, or 315 workgroups of the few-row kernel, 7.7; 128 x 1024 x 1024, short,
+// 4.3 or 6.3).
+hipError_t launch_mx_product(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t M, int N,
+                             int K, bool out_bf16, void* out, hipStream_t s) {
+  int per, kw, rw;
+  few_split(K / 32, per, kw, rw);
+  const int64_t cus = device_cu_count(), wgs = ((N + 15) / 16 + rw - 1) / rw;
+  if (few_lds(M, K / 32) <= kFewLds && (M <= kFewRows || (K >= 4096 && (M + kFewRows - 1) / kFewRows * wgs <= 2 * cus)))
+    return launch_mx_few(a, -1, as, w, ws, M, N, K, 0, out_bf16, out, s);
   TileArgs t{};
   t.a = a;
   t.as = as;
@@ -545,11 +611,10 @@ hipError_t launch_mx_tiles(const uint8_t* a, const uint8_t* as, const uint8_t* w
   t.N = N;
   t.nb = K / 32;
   t.out = out;
-  const int64_t cus = device_cu_count();
   auto tiles = [&](int64_t B) { return ((M + B - 1) / B) * ((N + B - 1) / B); };
-  if (tiles(256) >= cus) return launch_square<256>(t, out_bf16, s);
-  if (tiles(128) >= cus) return launch_square<128>(t, out_bf16, s);
-  return launch_square<64>(t, out_bf16, s);
+  if (tiles(256) >= cus) return launch_square<256, 8>(t, out_bf16, s);
+  if (tiles(128) >= cus) return launch_square<128, 8>(t, out_bf16, s);
+  return launch_square<64, 4>(t, out_bf16, s);
 }
 
 }  // namespace k3moe
