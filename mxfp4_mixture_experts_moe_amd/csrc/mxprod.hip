@@ -180,10 +180,8 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
           scales[m * a.srow + r] = (uint8_t)rsc[b];
         }
       } else {
-        float v[8];
-        mx_load8<kX>(&raw[b][0], v);
-        const uint32_t e = mx_scale_byte(mx_block_top(v), a.saturate != 0);
-        const uint32_t c = mx_codes(v, e);
+        uint32_t e;
+        const uint32_t c = mx_quant8<kX>(raw[b], a.saturate != 0, e);
         if (u < units) {
           *reinterpret_cast<uint32_t*>(codes + sm * a.arow + 4 * u) = c;
           if ((tid & 3) == 0) scales[sm * a.srow + (u >> 2)] = (uint8_t)e;

@@ -18,25 +18,27 @@ namespace k3moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 4;  // groups of eight elements per thread and round
+constexpr int kPer = 2;  // groups of eight elements per thread and round (4: 54 us instead of 52, 8: 58, for 16384 x 7168 bf16)
 
 template <int kType>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const uint8_t* __restrict__ x, int64_t n8, int saturate,
                                                             uint32_t* __restrict__ packed, uint8_t* __restrict__ scale) {
-  constexpr int kBytes = kType == K3MOE_DTYPE_F32 ? 32 : 16;
+  constexpr int kRaw = kType == K3MOE_DTYPE_F32 ? 2 : 1;
   // n8 is a multiple of 4, so the four lanes of a block are in or out together
   for (int64_t b = (int64_t)blockIdx.x * (kThreads * kPer); b < n8; b += (int64_t)gridDim.x * (kThreads * kPer)) {
-    float v[kPer][8];
+    mx_u32x4 raw[kPer][kRaw];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int64_t i = b + u * kThreads + threadIdx.x;
-      mx_load8<kType>(x + (i < n8 ? i : n8 - 4 + (threadIdx.x & 3)) * kBytes, v[u]);
+      const int64_t j = i < n8 ? i : n8 - 4 + (threadIdx.x & 3);
+#pragma unroll
+      for (int h = 0; h < kRaw; ++h) raw[u][h] = reinterpret_cast<const mx_u32x4*>(x)[j * kRaw + h];
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int64_t i = b + u * kThreads + threadIdx.x;
-      const uint32_t e = mx_scale_byte(mx_block_top(v[u]), saturate != 0);
-      const uint32_t c = mx_codes(v[u], e);
+      uint32_t e;
+      const uint32_t c = mx_quant8<kType>(raw[u], saturate != 0, e);
       if (i < n8) {
         packed[i] = c;
         if ((threadIdx.x & 3) == 0) scale[i >> 2] = (uint8_t)e;
