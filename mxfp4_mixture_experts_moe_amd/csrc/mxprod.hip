@@ -124,7 +124,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
   const uint32_t rowb = (uint32_t)nb * 16;
   auto load = [&](int g_, int s_, Piece& d) __attribute__((always_inline)) {
     const int grp = __builtin_amdgcn_readfirstlane(g_), ss = __builtin_amdgcn_readfirstlane(s_);
-    const int rows = __builtin_amdgcn_readfirstlane(min(max(a.N - 16 * grp, 0), ss < nss ? 16 : 0));
+    const int rows = __builtin_amdgcn_readfirstlane(grp < ngroups && ss < nss ? min(a.N - 16 * grp, 16) : 0);
     const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + (int64_t)grp * 16 * rowb), 0, rows * rowb, 0x00020000);
     const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(a.ws + (int64_t)grp * 16 * nb), 0, rows * nb, 0x00020000);
     const uint32_t b = (uint32_t)(16 * ss + g), row = (uint32_t)rho * nb;
@@ -249,7 +249,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
     if (s0 == 0 && grp < ngroups && rho < M) {
       const int n = 16 * grp + 4 * g;
       const int64_t at = (m0 + rho) * a.N + n;
-      if (n + 4 <= a.N && (a.N & 3) == 0) {
+      if (n <= a.N - 4 && (a.N & 3) == 0) {
         if constexpr (kBf16) {
           typedef __bf16 b4 __attribute__((ext_vector_type(4)));
           *reinterpret_cast<b4*>(static_cast<__bf16*>(a.out) + at) = b4{(__bf16)sum[0], (__bf16)sum[1], (__bf16)sum[2], (__bf16)sum[3]};
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
       } else {
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          if (n + v < a.N) store_out<kBf16>(a.out, at + v, sum[v]);
+          if (n < a.N - v) store_out<kBf16>(a.out, at + v, sum[v]);
       }
     }
     grp += gstep;
@@ -319,7 +319,8 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
   // logical order, which walks groups of four tile rows column by column.
   const int mt = (int)((t.M + B - 1) / B), nt = (t.N + B - 1) / B;
   const int64_t total = (int64_t)mt * nt;
-  int64_t id = blockIdx.x;
+  int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (id >= total) return;
   {
     const int64_t q = total / kXcds, r = total % kXcds, x = id % kXcds, j = id / kXcds;
     id = x * q + (x < r ? x : r) + j;
@@ -542,7 +543,8 @@ hipError_t launch_few(const FewArgs& a, bool bf16, hipStream_t s) {
 template <int B, int kWaves>
 hipError_t launch_square(const TileArgs& t, bool bf16, hipStream_t s) {
   const int64_t total = ((t.M + B - 1) / B) * ((t.N + B - 1) / B);
-  const dim3 grid((unsigned)total), block(kWaves * 64);
+  const int64_t gx = total < (1 << 20) ? total : 1 << 20;  // (a grid dimension has fewer than 2^32 threads)
+  const dim3 grid((unsigned)gx, (unsigned)((total + gx - 1) / gx)), block(kWaves * 64);
   auto go = [&](auto st, auto b) {
     hipLaunchKernelGGL((mx_tile_kernel<B, kWaves, decltype(st)::value, decltype(b)::value>), grid, block, 0, s, t);
   };

@@ -67,7 +67,8 @@ def test_matmul_checks(k3):
 
 def test_linear_checks_and_workspace(k3):
     f, size = k3.lib.mxfp4_linear, k3.mxfp4_linear_workspace_size
-    assert size(1, 100, 7168) == 0 and size(16, 100, 7168) == 0 and size(0, 5, 32) == 0 and size(4, 4, 33) == 0
+    assert size(1, 100, 7168) == 0 and size(16, 100, 2048) == 0 and size(0, 5, 32) == 0 and size(4, 4, 33) == 0
+    assert size(16, 100, 2080) > 0  # beyond 32 Ki elements the rows are quantised by a launch of their own
     assert size(17, 100, 7168) == 17 * 3584 + -(17 * 3584) % 256 + 17 * 224 + -(17 * 224) % 256
     assert size(16, 8, 65536) >= 16 * 65536 // 2  # codes of 16 such rows do not fit in LDS
     assert f(A, F32, A, A, 40, 4, 64, 1, F32, A, None, 0, None) == ERR_NULL
@@ -91,3 +92,24 @@ def test_binding_refuses(k3):
         k3.mxfp4_matmul(u8, u8[:, :2], u8, u8[:, :2])
     with pytest.raises(ValueError):
         k3.mxfp4_linear(x, u8, u8[:, :2])
+
+
+def test_layer_checks_and_workspace(k3):
+    f, size = k3.lib.moe_mxfp4_layer, k3.moe_mxfp4_layer_workspace_size
+    T, D, I, E, k = 3, 64, 96, 8, 2
+    need = size(T, D, I, E, k)
+    assert need > 0 and size(0, D, I, E, k) == 0 and size(17, D, I, E, k) == 0 and size(T, 65, I, E, k) == 0
+    call = lambda p, T=T, D=D, I=I, E=E, k=k, act=0, out=A, ids=A, w=A, ws=A, n=need: f(  # noqa: E731
+        *p, T, D, I, E, k, 1, 1.0, act, out, ids, w, ws, n, None)
+    ok = [A] * 6  # x, logits, bias, w1, w3, w2
+    for i in (0, 1, 3, 4, 5):
+        assert call(ok[:i] + [None] + ok[i + 1:]) == ERR_NULL
+    for i in range(6):
+        assert call(ok[:i] + [A + 4] + ok[i + 1:]) == ERR_ALIGN
+    assert call(ok, out=None) == ERR_NULL and call(ok, ws=None) == ERR_NULL
+    assert call(ok, out=A + 4) == call(ok, ids=A + 4) == call(ok, w=A + 4) == call(ok, ws=A + 8) == ERR_ALIGN
+    assert call(ok, n=need - 1) == ERR_WORKSPACE
+    assert call(ok, act=1) == ERR_UNSUPPORTED
+    for bad in (dict(T=17), dict(T=-1), dict(D=48), dict(I=0), dict(D=65536 + 32), dict(E=0), dict(k=9), dict(k=0), dict(E=8193)):
+        assert call(ok, **bad) == ERR_SHAPE, bad
+    assert call([None] * 6, T=0, out=None, ids=None, w=None, ws=None, n=0) == OK

@@ -227,3 +227,38 @@ def test_streams_and_graph(k3):
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, k3.mxfp4_linear(x, wp, ws)), i
+
+
+@pytest.mark.parametrize("M,N,K", [(17, 40, 4096), (33, 100, 4128), (77, 60, 7168), (64, 4, 8192), (48, 260, 4160), (200, 17, 4096)])
+def test_rows_sixteen_at_a_time_exact(k3, M, N, K):
+    """More than 16 rows of a long K and few columns: 16 rows side by side, ragged at the last ones and at N."""
+    test_matmul_exact(k3, M, N, K)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 33, 6592), (12, 100, 4128), (16, 50, 7168), (9, 40, 32768), (40, 70, 5120)])
+def test_linear_rows_quantised_first(k3, M, N, K):
+    test_linear_is_quantize_then_matmul(k3, "bf16", M, N, K, True)
+
+
+@pytest.mark.parametrize("M,N,K", [(300, 500, 1024), (513, 2100, 512), (140, 8300, 1536), (2100, 4200, 512), (2049, 4100, 544)])
+def test_matmul_tiles_exact(k3, M, N, K):
+    """Every tile size, with the scales of whole 512 columns and of shorter ones."""
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    rnd = lambda *s: torch.randint(0, 256, s, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    ap, wp, as_, ws = rnd(M, K // 2), rnd(N, K // 2), rnd(M, K // 32) % 2 + 126, rnd(N, K // 32) % 2 + 127
+    ref = (k3.mxfp4_unpack(ap, as_).double() @ k3.mxfp4_unpack(wp, ws).double().t().contiguous()).float()
+    assert torch.equal(k3.mxfp4_matmul(ap, as_, wp, ws), ref)
+
+
+@pytest.mark.parametrize("M,K", [(3, 672), (16, 7168), (40, 7168)])
+def test_nonfinite_blocks_of_few_rows(k3, M, K):
+    """A block that is not a number gives NaN in its row or column alone, also where K's last piece is short."""
+    g = np.random.default_rng(M + K)
+    N = 70
+    (ap, as_), (wp, ws) = pair(g, M, K, 126, 127), pair(g, N, K, 127, 128)
+    ref = torch.from_numpy(mx4.product_ref(ap, as_, wp, ws)).float()
+    as_[M - 1, K // 32 - 1], ws[N - 1, K // 32 - 1], ws[5, 0] = 255, 255, 255
+    got = k3.mxfp4_matmul(*(to_dev_u8(t) for t in (ap, as_, wp, ws))).cpu()
+    nan = torch.zeros((M, N), dtype=torch.bool)
+    nan[M - 1], nan[:, N - 1], nan[:, 5] = True, True, True
+    assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], ref[~nan])
