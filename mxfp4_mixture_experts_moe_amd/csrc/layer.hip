@@ -476,7 +476,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   // matrix.  The instruction's own offset counts for the LDS address, too, so
   // loads 0-3, 4-7 and 8 share a base each, and their lane offsets are
   const int lane16 = 16 * lane;  // 0-3
-  int wofs4 = 0, wofs5 = 0;      // 4; 5-8
+  int wofs4 = 0, wofs5 = 0, wofs8 = 0;  // 4; 5-7; 8 (half of it past the stage: not asked for)
   static_assert(kW == 9, "three bases");
 
   // ---- issue side.  A stage is the same 512 columns of two neighbouring 16-row
@@ -548,6 +548,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     grp2x = 2 * gb;
     wofs5 = gb + lane16 - 256;
     wofs4 = lane < 16 ? 4096 + lane16 : wofs5;
+    wofs8 = lane < 32 ? wofs5 + 4096 : kNoLane;
     left = gu ? 2 * nst13 : nst2;
     act0 = gu ? t0 * nst13 * kXRow : iu.row * a.hstride;
     act1 = gu ? t1 * nst13 * kXRow : act0 + a.hstride;
@@ -591,7 +592,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs5, 0, 1024, kNt);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs5, 0, 2048, kNt);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l4, 16, wofs5, 0, 3072, kNt);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l8, 16, wofs5, 4096, 0, kNt);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, l8, 16, wofs8, 0, 0, kNt);
     --left;
     const bool gu = iu.kind == kGateUp;
     const int odd = left & 1;  // gate/up: an even number of stages, w1 where an odd number is left
