@@ -188,6 +188,10 @@ def _raw_stream(index: int) -> int:
     return torch.cuda.current_stream(index).cuda_stream
 
 
+# the same handle without a Stream object around it (0.1 us instead of 1.2), where torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 def moe_route_topk(logits: torch.Tensor, bias: torch.Tensor | None, k: int, normalize: bool = True,
                    route_scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None):
     """Sigmoid + bias top-k routing. logits f32 [T, E], bias f32 [E] or None.
@@ -288,11 +292,11 @@ def _mx_pair(packed: torch.Tensor, scale: torch.Tensor, name: str, dims: int | N
     """Checks a microscaled pair; returns K."""
     _dev(packed, name, torch.uint8)
     _dev(scale, name, torch.uint8)
-    ps, ss = packed.shape, scale.shape
+    ps = packed.shape
     if not ps or (dims is not None and len(ps) != dims):
         raise ValueError(f"{name}: packed must have {dims or 'at least 1'} dimensions")
     K = ps[-1] * 2
-    if ss[:-1] != ps[:-1] or ss[-1] * 32 != K:
+    if scale.shape != (*ps[:-1], K // 32) or K % 32:
         raise ValueError(f"{name}: scale must be [..., R, K/32] for packed [..., R, K/2]")
     if scale.get_device() != packed.get_device():
         raise ValueError(f"{name}: packed and scale are on different devices")
@@ -320,13 +324,15 @@ def mxfp4_quantize(x: torch.Tensor, saturate: bool = True, packed: torch.Tensor 
     if K % 32:
         raise ValueError("K must be a multiple of 32")
     lead = x.shape[:-1]
+    given = packed is not None or scale is not None
     if packed is None:
-        packed = torch.empty((*lead, K // 2), dtype=torch.uint8, device=x.device)
+        packed = x.new_empty((*lead, K // 2), dtype=torch.uint8)
     if scale is None:
-        scale = torch.empty((*lead, K // 32), dtype=torch.uint8, device=x.device)
-    if _mx_pair(packed, scale, "output") != K or packed.shape[:-1] != lead:
-        raise ValueError("packed must be [..., R, K/2] for x [..., R, K]")
-    _same_device(x, packed=packed)
+        scale = x.new_empty((*lead, K // 32), dtype=torch.uint8)
+    if given:
+        if _mx_pair(packed, scale, "output") != K or packed.shape[:-1] != lead:
+            raise ValueError("packed must be [..., R, K/2] for x [..., R, K]")
+        _same_device(x, packed=packed)
     R = x.numel() // K if K else 0
     _launch("mxfp4_quantize", x.device, x.data_ptr(), _FLOAT_CODES[x.dtype], R, K, int(bool(saturate)), packed.data_ptr(),
             scale.data_ptr())
@@ -340,11 +346,12 @@ def mxfp4_unpack(packed: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dty
     K = _mx_pair(packed, scale, "input")
     code = _out_code(out_dtype)
     if out is None:
-        out = torch.empty((*packed.shape[:-1], K), dtype=out_dtype, device=packed.device)
-    _dev(out, "out", out_dtype)
-    if out.numel() != packed.numel() * 2:
-        raise ValueError("out has the wrong size")
-    _same_device(packed, out=out)
+        out = packed.new_empty((*packed.shape[:-1], K), dtype=out_dtype)
+    else:
+        _dev(out, "out", out_dtype)
+        if out.numel() != packed.numel() * 2:
+            raise ValueError("out has the wrong size")
+        _same_device(packed, out=out)
     R = packed.numel() * 2 // K if K else 0
     _launch("mxfp4_unpack", packed.device, packed.data_ptr(), scale.data_ptr(), R, K, code, out.data_ptr())
     return out
@@ -360,10 +367,11 @@ def mxfp4_matmul(a_packed: torch.Tensor, a_scale: torch.Tensor, w_packed: torch.
     M, N = a_packed.shape[0], w_packed.shape[0]
     code = _out_code(out_dtype)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=a_packed.device)
-    _dev(out, "out", out_dtype)
-    if out.shape != (M, N):
-        raise ValueError("out must be [M, N]")
+        out = a_packed.new_empty((M, N), dtype=out_dtype)
+    else:
+        _dev(out, "out", out_dtype)
+        if out.shape != (M, N):
+            raise ValueError("out must be [M, N]")
     _same_device(a_packed, W=w_packed, out=out)
     _launch("mxfp4_matmul", a_packed.device, a_packed.data_ptr(), a_scale.data_ptr(), w_packed.data_ptr(), w_scale.data_ptr(),
             M, N, K, code, out.data_ptr())
@@ -387,14 +395,15 @@ def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
     M, N = x.shape[0], w_packed.shape[0]
     code = _out_code(out_dtype)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=x.device)
-    _dev(out, "out", out_dtype)
-    if out.shape != (M, N):
-        raise ValueError("out must be [M, N]")
+        out = x.new_empty((M, N), dtype=out_dtype)
+    else:
+        _dev(out, "out", out_dtype)
+        if out.shape != (M, N):
+            raise ValueError("out must be [M, N]")
     need = mxfp4_linear_workspace_size(M, N, K)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    if workspace is not None:
+        workspace = x.new_empty(need, dtype=torch.uint8)
+    elif workspace is not None:
         _dev(workspace, "workspace", torch.uint8)
     _same_device(x, W=w_packed, out=out, workspace=workspace)
     _launch("mxfp4_linear", x.device, x.data_ptr(), _FLOAT_CODES[x.dtype], w_packed.data_ptr(), w_scale.data_ptr(), M, N, K,
@@ -433,19 +442,20 @@ def moe_mxfp4_layer(x: torch.Tensor, logits: torch.Tensor, bias: torch.Tensor | 
         raise ValueError("expert weights have inconsistent shapes")
     dev = x.device
     if out is None:
-        out = torch.empty((T, D), dtype=torch.float32, device=dev)
+        out = x.new_empty((T, D), dtype=torch.float32)
     if ids is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+        ids = x.new_empty((T, k), dtype=torch.int32)
     if weights is None:
-        weights = torch.empty((T, k), dtype=torch.float32, device=dev)
+        weights = x.new_empty((T, k), dtype=torch.float32)
     _dev(out, "out", torch.float32)
     _dev(ids, "ids", torch.int32)
     _dev(weights, "weights", torch.float32)
     if out.shape != (T, D) or ids.shape != (T, k) or weights.shape != (T, k):
         raise ValueError("out must be [T, D], ids and weights [T, k]")
     if workspace is None:
-        workspace = torch.empty(max(moe_mxfp4_layer_workspace_size(T, D, I, E, k), 1), dtype=torch.uint8, device=dev)
-    _dev(workspace, "workspace", torch.uint8)
+        workspace = x.new_empty(max(moe_mxfp4_layer_workspace_size(T, D, I, E, k), 1), dtype=torch.uint8)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
     _same_device(x, logits=logits, bias=bias, w1=w1, w3=w3, w2=w2, out=out, ids=ids, weights=weights, workspace=workspace)
     _launch("moe_mxfp4_layer", dev, x.data_ptr(), logits.data_ptr(), _ptr(bias), w1.data_ptr(), w3.data_ptr(), w2.data_ptr(), T, D,
             I, E, k, int(bool(normalize)), float(route_scale), act, out.data_ptr(), ids.data_ptr(), weights.data_ptr(),
