@@ -78,9 +78,9 @@ int mxfp4_matmul(const uint8_t* a_packed, const uint8_t* a_scale, const uint8_t*
 /*
  * mxfp4_linear — float rows times a microscaled weight matrix: the rows are
  * quantised as mxfp4_quantize does (x_dtype, saturate) and multiplied as
- * mxfp4_matmul does, with the same bits as the two calls. Up to 16 rows whose
- * codes fit a workgroup's LDS take one launch (the kernel quantises its rows
- * itself); more rows are quantised into the workspace first.
+ * mxfp4_matmul does, with the same bits as the two calls. Up to 16 rows of
+ * together at most 32768 elements take one launch (the kernel quantises its
+ * rows itself); more are quantised into the workspace first.
  *   workspace  mxfp4_linear_workspace_size() bytes (0: may be NULL); contents
  *              on entry do not matter and are clobbered
  */
@@ -109,11 +109,12 @@ int mxfp4_linear(const void* x, int32_t x_dtype, const uint8_t* w_packed, const 
  *   workspace  moe_mxfp4_layer_workspace_size() bytes; contents on entry do
  *            not matter and are clobbered
  *
- * Precision: bf16 x, exact weights, fp32 accumulation; h = SiLU(g) * u in fp32
- * enters the down product as three bf16 parts (24 significant bits); the k
- * expert outputs are summed in fp32 in slot order (deterministic, no atomics
- * on values). moe_mxfp4_ffn rounds h to about 16 bits, so the two agree to
- * that. More than 1024 experts take a third launch (the router's own).
+ * Precision: exact weights, fp32 accumulation. x and h = SiLU(g) * u (fp32)
+ * enter the products in fixed point per 32-element block: x to 2^-19 of the
+ * block's largest magnitude (elements down to 2^-11 of it exactly), h to 2^-24
+ * of it. The k expert outputs are summed in fp32 in slot order (deterministic,
+ * no atomics on values). moe_mxfp4_ffn rounds h to about 16 bits, so the two
+ * agree to that. More than 1024 experts take a third launch (the router's own).
  * Sizes: 0 <= T <= K3MOE_MAX_LAYER_TOKENS (T == 0 is a no-op), D, I, E and k
  * as for moe_mxfp4_ffn. Calls that overlap (two streams, two graphs) need
  * workspaces of their own.

@@ -30,6 +30,14 @@
 // in that order, expert by expert, and streams their weights through a private
 // ring of three LDS stages that runs on across units.
 //
+// Measured (graph replay; 16 experts a token, D = 3584, I = 3072): one token 66
+// us, 281 MB of weights (plan 6.5, first weights in LDS 6 to 8 us into the second
+// launch, the stream at 5.6 TB/s, sums 4); eight tokens 286 us, 1.58 GB, 5.5
+// TB/s; the two calls moe_route_topk and moe_mxfp4_ffn take 64 and 291 us there.
+// 13 tokens, 5 of 61 experts, D = 1056, I = 736: 36 us against 186; one token,
+// 2 of 8 experts, D = 128, I = 256: 18 us against 22.  What bounds it: the bytes
+// with many tokens, plan, first loads and sums with one.
+//
 // Hand-over.  A down unit needs h from every gate/up unit of its tile, a sum unit
 // every down unit of its features.  Units are taken by a global ticket (atomic
 // add), and a wave works on its units in ticket order, so a unit waits only for
@@ -278,8 +286,7 @@ constexpr int kActBufs = 2;
 constexpr int kNt = 2;               // cache policy of the weight loads: nontemporal
 constexpr int kDevScope = 16;        // cache policy of loads and stores that other XCDs must agree on (sc1)
 constexpr int kSpinLimit = 1 << 21;
-constexpr int kDrawAt = 0;           // a unit's last stages not yet asked for when the next ticket is drawn
-constexpr int kChunk = 4;            // tickets a workgroup draws at once
+constexpr int kChunk = 4;            // tickets a workgroup draws at once (2 or 8: 73 us instead of 70 for one token, D = 3584, I = 3072)
 constexpr int kNoLane = INT32_MIN;  // buffer offset past every buffer: the lane's store is dropped
 // Counters sit on lines of their own: device-scope adds to one line are served
 // one after another, 11.4 ns each (measured; to different lines they overlap).
@@ -655,9 +662,10 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   uint32_t sub = 0;
   bool down = false;
   for (;;) {
-    // as late as the draw's way there and back allows: a ticket taken early keeps
-    // waves that are free from work that could begin
-    if (!drawn && left <= kDrawAt) {
+    // the next ticket, once all stages of this unit have been asked for: one
+    // drawn at the unit's start kept free waves from work that could begin (77
+    // us instead of 70 for one token of 16 experts, D = 3584, I = 3072)
+    if (!drawn && left == 0) {
       nu = unit_of(claim());
       drawn = true;
     }
