@@ -16,6 +16,8 @@
 // lanes hold one block: its maximum takes two quad permutes, no LDS.
 #include "mx_common.h"
 
+#include <type_traits>
+
 namespace k3moe {
 namespace {
 
@@ -49,51 +51,56 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const uint8_t* __res
   }
 }
 
+// A lane's unit is what fills one 16-byte store: eight bf16 elements (a dword of
+// codes) or four fp32 ones (half a dword), so that a wave writes whole lines;
+// they go past the caches (43 us instead of 49 for 16384 x 7168 to bf16).
 template <bool kBf16>
-__global__ __launch_bounds__(kThreads) void unpack_kernel(const uint32_t* __restrict__ packed,
-                                                          const uint8_t* __restrict__ scale, int64_t n8,
-                                                          void* __restrict__ out) {
-  for (int64_t b = (int64_t)blockIdx.x * (kThreads * kPer); b < n8; b += (int64_t)gridDim.x * (kThreads * kPer)) {
+__global__ __launch_bounds__(kThreads) void unpack_kernel(const uint8_t* __restrict__ packed,
+                                                          const uint8_t* __restrict__ scale, int64_t units,
+                                                          mx_u32x4* __restrict__ out) {
+  typedef std::conditional_t<kBf16, uint32_t, uint16_t> Codes;
+  constexpr int kShift = kBf16 ? 2 : 3;  // units of a block
+  for (int64_t b = (int64_t)blockIdx.x * (kThreads * kPer); b < units; b += (int64_t)gridDim.x * (kThreads * kPer)) {
     uint32_t q[kPer], e[kPer];
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int64_t i = b + u * kThreads + threadIdx.x;
-      const int64_t j = i < n8 ? i : n8 - 1;
-      q[u] = packed[j];
-      e[u] = scale[j >> 2];
+      const int64_t j = i < units ? i : units - 1;
+      q[u] = reinterpret_cast<const Codes*>(packed)[j];
+      e[u] = scale[j >> kShift];
     }
 #pragma unroll
     for (int u = 0; u < kPer; ++u) {
       const int64_t i = b + u * kThreads + threadIdx.x;
-      if (i >= n8) continue;
+      if (i >= units) continue;
       const float s = mx_scale_f32(e[u] == 255u ? 127u : e[u]);
       typedef float f2 __attribute__((ext_vector_type(2)));
-      f2 p[4];
+      f2 p[kBf16 ? 4 : 2];
       p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 0);
       p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 1);
-      p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 2);
-      p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 3);
+      if constexpr (kBf16) {
+        p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 2);
+        p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 3);
+      }
       if (e[u] == 255u) {
         const float nan = __uint_as_float(0x7FC00000u);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) p[c] = f2{nan, nan};
+        for (int c = 0; c < (kBf16 ? 4 : 2); ++c) p[c] = f2{nan, nan};
       }
-      if constexpr (kBf16) {
-        mx_u32x4 r;  // every value of finite scale is exact in bf16: its upper half is the number
+      mx_u32x4 r;
+      if constexpr (kBf16) {  // every value of finite scale is exact in bf16: its upper half is the number
 #pragma unroll
         for (int c = 0; c < 4; ++c) r[c] = __builtin_amdgcn_perm(__float_as_uint(p[c][1]), __float_as_uint(p[c][0]), 0x07060302u);
-        static_cast<mx_u32x4*>(out)[i] = r;
       } else {
-        float4* o = static_cast<float4*>(out) + 2 * i;
-        o[0] = make_float4(p[0][0], p[0][1], p[1][0], p[1][1]);
-        o[1] = make_float4(p[2][0], p[2][1], p[3][0], p[3][1]);
+        r = mx_u32x4{__float_as_uint(p[0][0]), __float_as_uint(p[0][1]), __float_as_uint(p[1][0]), __float_as_uint(p[1][1])};
       }
+      __builtin_nontemporal_store(r, out + i);
     }
   }
 }
 
-unsigned copy_grid(int64_t n8) {
-  const int64_t g = (n8 + kThreads * kPer - 1) / (kThreads * kPer);
+unsigned copy_grid(int64_t units) {
+  const int64_t g = (units + kThreads * kPer - 1) / (kThreads * kPer);
   const int64_t most = (int64_t)1 << 20;
   return (unsigned)(g < most ? g : most);
 }
@@ -117,13 +124,13 @@ hipError_t launch_quantize(const void* x, int x_dtype, int64_t n, int saturate, 
 
 hipError_t launch_unpack(const uint8_t* packed, const uint8_t* scale, int64_t n, int out_bf16, void* out,
                          hipStream_t s) {
-  const int64_t n8 = n / 8;
-  const dim3 grid(copy_grid(n8)), block(kThreads);
-  const auto pp = reinterpret_cast<const uint32_t*>(packed);
+  const int64_t units = n / (out_bf16 ? 8 : 4);
+  const dim3 grid(copy_grid(units)), block(kThreads);
+  const auto o = static_cast<mx_u32x4*>(out);
   if (out_bf16)
-    hipLaunchKernelGGL(unpack_kernel<true>, grid, block, 0, s, pp, scale, n8, out);
+    hipLaunchKernelGGL(unpack_kernel<true>, grid, block, 0, s, packed, scale, units, o);
   else
-    hipLaunchKernelGGL(unpack_kernel<false>, grid, block, 0, s, pp, scale, n8, out);
+    hipLaunchKernelGGL(unpack_kernel<false>, grid, block, 0, s, packed, scale, units, o);
   return hipGetLastError();
 }
 
