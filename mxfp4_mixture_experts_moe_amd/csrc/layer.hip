@@ -456,7 +456,10 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   // are left, or kRefill while the wave that found none fetches more; that wave
   // is running and waits only for its add to return).
   constexpr uint32_t kRefill = 0xFFFFFFFFu;
-  if (threadIdx.x == 0) s_pool = 0ull;
+  if (wave == 0) {  // the first draw, while the other waves set out
+    const int v = draw_dev(a.head + 1, kChunk);
+    __hip_atomic_store(&s_pool, (unsigned long long)kChunk << 32 | (uint32_t)v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  }
   __syncthreads();
   const uint32_t pool = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)&s_pool;
   auto claim = [&]() __attribute__((always_inline)) -> int {
@@ -755,6 +758,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
             load_h(aj, at + j * kHRow, true);
             if (rows > 1) load_h(aj + kHRowLds, at + a.hstride + j * kHRow, true);
           }
+          __builtin_amdgcn_s_sleep(1);
           wait_vm<0>();
         }
       }
