@@ -315,7 +315,9 @@ template <int B, int kWaves, bool kStaged, bool kBf16>
 __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
   constexpr int kWm = kWaves / 2;         // waves along M; two along N
   constexpr int kTm = B / (32 * kWm), kTn = B / 64;  // 32-row operand tiles per wave
-  constexpr int kStageDw = 2 * B * 16;    // dwords of a stage: B rows of A, B rows of W, 64 bytes each
+  constexpr int kS = kStaged && B == 64 ? 2 : 1;  // steps of a stage
+  constexpr int kStepDw = 2 * B * 16;     // dwords of a step: B rows of A, B rows of W, 64 bytes each
+  constexpr int kStageDw = kS * kStepDw;
   constexpr int kLoads = 2 * B / (16 * kWaves);  // 1 KB loads per wave and stage
   // one array per buffer, so that the compiler sees that a read of one buffer
   // does not depend on the loads in flight into the others
@@ -352,7 +354,6 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
   const int lrow0 = wave % (kWaves / 2) * (2 * B / kWaves);  // first row within A or W
   const uint8_t* const src = from_a ? t.a + m0 * rowb : t.w + (int64_t)n0 * rowb;
   const int srows = from_a ? mrows : nrows;
-  const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)src, 0, (int)(srows * rowb), 0x00020000);
   uint32_t voff[kLoads];
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
@@ -360,13 +361,19 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
     const int c = (lane & 3) ^ ((r >> 2) & 3);
     voff[j] = (uint32_t)min(r, srows - 1) * rowb + 16 * c;
   }
+  // (steps past K are outside the buffer: zeros that cost no traffic)
   auto issue = [&](int step, uint32_t* buf) {
-    uint32_t* dst = buf + (2 * B / kWaves) * wave * 16;
-    const int so = 64 * step;
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc((void*)src, 0, step < nsteps ? (int)(srows * rowb) : 0, 0x00020000);
 #pragma unroll
-    for (int j = 0; j < kLoads; ++j) {
-      const uint32_t vo = voff[j];  // (an array element passed straight makes the host pass drop the kernel's launch stub)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst + 256 * j, 16, vo, so, 0, 0);
+    for (int st = 0; st < kS; ++st) {
+      uint32_t* dst = buf + st * kStepDw + (2 * B / kWaves) * wave * 16;
+      const int so = 64 * (step + st);
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) {
+        const uint32_t vo = voff[j];  // (an array element passed straight makes the host pass drop the kernel's launch stub)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst + 256 * j, 16, vo, so, 0, 0);
+      }
     }
   };
 
@@ -435,18 +442,18 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
   using C2 = std::integral_constant<int, 2>;
   using C3 = std::integral_constant<int, 3>;
 
-  // Whole groups of four steps.  Every step issues the loads of three steps on
-  // (past K they read other bytes of the tile's rows or nothing; no step uses
-  // them), every second one the scales of the next pair, without a branch, so
-  // the number of loads in flight is the same everywhere: when step q starts,
-  // the loads after its own are those of steps q+1 and q+2 and one set of
-  // scales.
+  // Whole groups of four steps, a stage of kS of them at a time.  Every stage
+  // issues the loads of three stages on, the first of a group (kStaged; else
+  // every second one) the scales of the next steps but those, without a branch,
+  // so the number of loads in flight is the same everywhere: when a stage
+  // starts, the loads after its own are those of the next two stages and up to
+  // one set of scales.
   const int full = nb >> 4;
   const int last_pair = 2 * full - 1;
-  auto step = [&](auto uc, int q, uint32_t* cur, uint32_t* refill) {
-    constexpr int u = decltype(uc)::value;
+  auto stage = [&](auto uc, int q, uint32_t* cur, uint32_t* refill) {
+    constexpr int u = decltype(uc)::value;  // the stage's first step in its group
     if constexpr (kStaged)
-      wait_vm<2 * kLoads + (u == 1 || u == 2 ? 1 : 0)>();
+      wait_vm<2 * kS * kLoads + (u == kS || (kS == 1 && u == 2) ? 1 : 0)>();
     else
       wait_vm<2 * kLoads + kTm + kTn>();
     ring_barrier();
@@ -473,22 +480,36 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
       load_scales(min((q >> 1) + 1, last_pair));
       asm volatile("" ::: "memory");
     }
-    issue(q + 3, refill);
+    issue(q + 3 * kS, refill);
     part(cur, C0{}, std::integral_constant<int, 2 * (u % 2)>{}, true);
     part(cur, C1{}, std::integral_constant<int, 2 * (u % 2) + 1>{}, true);
+    if constexpr (kS == 2) {
+      part(cur + kStepDw, C0{}, C2{}, true);
+      part(cur + kStepDw, C1{}, C3{}, true);
+    }
   };
   if constexpr (kStaged) issue_scales(0);
   asm volatile("" ::: "memory");
   issue(0, l0);
-  issue(1, l1);
+  issue(kS, l1);
   if (!kStaged && full > 0) load_scales(0);
   asm volatile("" ::: "memory");
-  issue(2, l2);
-  for (int q = 0; q < 4 * full; q += 4) {
-    step(C0{}, q, l0, l3);
-    step(C1{}, q + 1, l1, l0);
-    step(C2{}, q + 2, l2, l1);
-    step(C3{}, q + 3, l3, l2);
+  issue(2 * kS, l2);
+  if constexpr (kS == 1) {
+    for (int q = 0; q < 4 * full; q += 4) {
+      stage(C0{}, q, l0, l3);
+      stage(C1{}, q + 1, l1, l0);
+      stage(C2{}, q + 2, l2, l1);
+      stage(C3{}, q + 3, l3, l2);
+    }
+  } else {
+    for (int q = 0; q < 4 * full; q += 8) {
+      stage(C0{}, q, l0, l3);
+      stage(C2{}, q + 2, l1, l0);
+      if (q + 4 == 4 * full) break;
+      stage(C0{}, q + 4, l2, l1);
+      stage(C2{}, q + 6, l3, l2);
+    }
   }
 
   // The rest of K, up to four steps: three of them are already on their way.
