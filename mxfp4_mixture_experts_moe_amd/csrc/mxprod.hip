@@ -643,8 +643,12 @@ hipError_t launch_mx_product(const uint8_t* a, const uint8_t* as, const uint8_t*
   t.nb = K / 32;
   t.out = out;
   auto tiles = [&](int64_t B) { return ((M + B - 1) / B) * ((N + B - 1) / B); };
-  if (tiles(256) >= cus) return launch_square<256, 8>(t, out_bf16, s);
-  if (tiles(128) >= cus) return launch_square<128, 8>(t, out_bf16, s);
+  // the largest tile that gives every CU one and that either side more than half
+  // fills (64 x 33792 x 7168: 64-row tiles 33 us, half-empty ones of 128 39;
+  // 2048 x 2048 x 4096: 128, 18 us, 64, 26; 512 x 7168 x 7168: both 38)
+  const int64_t side = M < N ? M : N;
+  if (side > 128 && tiles(256) >= cus) return launch_square<256, 8>(t, out_bf16, s);
+  if (side > 64 && tiles(128) >= cus) return launch_square<128, 8>(t, out_bf16, s);
   return launch_square<64, 4>(t, out_bf16, s);
 }
 
