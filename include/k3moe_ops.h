@@ -115,6 +115,9 @@ int mxfp4_linear(const void* x, int32_t x_dtype, const uint8_t* w_packed, const 
  * of it. The k expert outputs are summed in fp32 in slot order (deterministic,
  * no atomics on values). moe_mxfp4_ffn rounds h to about 16 bits, so the two
  * agree to that. More than 1024 experts take a third launch (the router's own).
+ * An expert's weights are streamed once per two of its tokens, so tokens that
+ * mostly choose different experts gain; where many share one, moe_route_topk and
+ * moe_mxfp4_ffn stream less.
  * Sizes: 0 <= T <= K3MOE_MAX_LAYER_TOKENS (T == 0 is a no-op), D, I, E and k
  * as for moe_mxfp4_ffn. Calls that overlap (two streams, two graphs) need
  * workspaces of their own.
