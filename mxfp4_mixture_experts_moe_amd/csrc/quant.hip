@@ -11,9 +11,10 @@
 // Both kernels are copies with a conversion on the way: bound by the bytes
 // they read and write (16384 x 7168 bf16: quantise 48-52 us, 5.7-6.2 TB/s;
 // decode to bf16 43 us, 6.9 TB/s; a plain copy of 1 GiB runs at 5.1 TB/s).  8 x
-// 7168 takes 2-3 us either way, a launch.  A lane owns eight consecutive elements (one dword of
-// codes), so a bf16 row is read 16 bytes a lane in order and four neighbouring
-// lanes hold one block: its maximum takes two quad permutes, no LDS.
+// 7168 takes 2-3 us either way, a launch.  A lane owns eight consecutive
+// elements (one dword of codes), so a bf16 row is read 16 bytes a lane in order
+// and four neighbouring lanes hold one block: its maximum takes two quad
+// permutes, no LDS.
 #include "mx_common.h"
 
 #include <type_traits>
