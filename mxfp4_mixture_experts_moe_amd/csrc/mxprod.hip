@@ -16,9 +16,9 @@
 //     the launch and the way of A through LDS);
 //   tiles: square output tiles, both operands staged through a ring of LDS
 //     buffers by direct global -> LDS loads; bound by the matrix cores for
-//     large products (4096 x 4096 x 7168: 71 us, 3.4 PFLOP/s, the matrix cores
-//     busy 0.62 of the time) and by load latency for small ones (128 x 7168 x
-//     3584: 7.8 us).
+//     large products (4096 x 4096 x 7168: 68 us, 3.5 PFLOP/s, the matrix cores
+//     busy 0.54 of a CU's time) and by load latency for small ones (128 x 7168 x
+//     3584: 7.8-8.3 us).
 #include "mx_common.h"
 
 #include <type_traits>
@@ -283,16 +283,21 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
 
 // ---------------------------------------------------------------------------
 // Tiles.  A workgroup (2 x 2 waves, 4 x 2 for the larger tiles) owns a B x B
-// tile of C; K goes in steps of 128 (four blocks: 64 bytes of every row) through
-// a ring of four LDS buffers filled by direct global -> LDS loads, three steps
-// ahead.  Lane (row r = lane % 32, half h) of a 32x32x64 instruction kk takes
-// block 2h + kk of the step.  The 16-byte block c of LDS row r sits at position
-// c ^ ((r >> 2) & 3) of the row's 64 bytes, so the 16-lane groups of a read
-// touch every bank once (no conflicts counted).  Scales: where rows of them are
-// 16-byte aligned (kStaged), 16 bytes (four steps) of every row go through LDS,
-// too, one load per wave and four steps; else each lane loads eight bytes (two
-// steps) of its rows.  The latter is a load of 32 lines for every operand tile
-// and wave: 89 us instead of 71 for 4096 x 4096 x 7168.
+// tile of C; K goes in steps of 128 (four blocks: 64 bytes of every row), in
+// stages of one or two steps, through a ring of LDS buffers filled by direct
+// global -> LDS loads.  Lane (row r = lane % 32, half h) of a 32x32x64
+// instruction kk of a step takes its block 2h + kk.  The 16-byte blocks of an
+// LDS row are permuted by the row (place()), so that the 16-lane groups of a
+// read touch every bank once (no conflicts counted).
+//   kStaged (K a multiple of 512): stages of two steps, so a row's piece is a
+//     whole 128-byte line (33 x 33792 x 7168: 28 us, with lines in two halves
+//     31; 1024 x 7168 x 3584: 25 and 28), a ring of four, for the larger tiles
+//     of two (128 KB, or 64 for two workgroups on a CU); scales, 16 bytes (four
+//     steps) of every row, go through LDS, too, one load per wave and four steps.
+//   else: stages of one step, a ring of four, and each lane loads eight scale
+//     bytes (two steps) of its rows, which are not aligned.  That is a load of 32
+//     lines for every operand tile and wave: 89 us instead of 71 for 4096 x 4096
+//     x 7168.
 constexpr int kXcds = 8;
 
 struct TileArgs {
@@ -315,13 +320,16 @@ template <int B, int kWaves, bool kStaged, bool kBf16>
 __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
   constexpr int kWm = kWaves / 2;         // waves along M; two along N
   constexpr int kTm = B / (32 * kWm), kTn = B / 64;  // 32-row operand tiles per wave
-  constexpr int kS = kStaged && B == 64 ? 2 : 1;  // steps of a stage
-  constexpr int kStepDw = 2 * B * 16;     // dwords of a step: B rows of A, B rows of W, 64 bytes each
-  constexpr int kStageDw = kS * kStepDw;
-  constexpr int kLoads = 2 * B / (16 * kWaves);  // 1 KB loads per wave and stage
+  constexpr int kS = kStaged ? 2 : 1;     // steps of a stage
+  constexpr int kRow = 64 * kS;           // bytes of a row of a stage
+  constexpr int kRing = kStaged && B >= 128 ? 2 : 4;
+  constexpr int kStageDw = 2 * B * kRow / 4;  // B rows of A, B rows of W
+  constexpr int kLoadRows = 1024 / kRow;  // of a 1 KB load
+  constexpr int kLoads = 2 * B / (kLoadRows * kWaves);  // per wave and stage
   // one array per buffer, so that the compiler sees that a read of one buffer
   // does not depend on the loads in flight into the others
-  __shared__ __attribute__((aligned(256))) uint32_t l0[kStageDw], l1[kStageDw], l2[kStageDw], l3[kStageDw];
+  __shared__ __attribute__((aligned(256))) uint32_t l0[kStageDw], l1[kStageDw], l2[kRing > 2 ? kStageDw : 1],
+      l3[kRing > 2 ? kStageDw : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -349,31 +357,29 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
   const int nrows = t.N - n0 < B ? t.N - n0 : B;
   const int nsteps = (nb + 3) >> 2;
 
-  // loads: wave w fills LDS rows 2B / kWaves * w ..; a 1 KB load holds 16 rows
+  // loads: wave w fills LDS rows 2B / kWaves * w ..
   const bool from_a = wave < kWaves / 2;
   const int lrow0 = wave % (kWaves / 2) * (2 * B / kWaves);  // first row within A or W
   const uint8_t* const src = from_a ? t.a + m0 * rowb : t.w + (int64_t)n0 * rowb;
   const int srows = from_a ? mrows : nrows;
+  // position of 16-byte chunk c in LDS row r
+  auto place = [](int c, int r) { return kS == 2 ? c ^ ((r >> 1) & 7) : c ^ ((r >> 2) & 3); };
   uint32_t voff[kLoads];
 #pragma unroll
   for (int j = 0; j < kLoads; ++j) {
-    const int r = lrow0 + 16 * j + (lane >> 2);
-    const int c = (lane & 3) ^ ((r >> 2) & 3);
-    voff[j] = (uint32_t)min(r, srows - 1) * rowb + 16 * c;
+    const int r = lrow0 + kLoadRows * j + lane / (kRow / 16);
+    voff[j] = (uint32_t)min(r, srows - 1) * rowb + 16 * place(lane % (kRow / 16), r);
   }
   // (steps past K are outside the buffer: zeros that cost no traffic)
   auto issue = [&](int step, uint32_t* buf) {
     const __amdgpu_buffer_rsrc_t rs =
         __builtin_amdgcn_make_buffer_rsrc((void*)src, 0, step < nsteps ? (int)(srows * rowb) : 0, 0x00020000);
+    uint32_t* dst = buf + (2 * B / kWaves) * wave * (kRow / 4);
+    const int so = 64 * step;
 #pragma unroll
-    for (int st = 0; st < kS; ++st) {
-      uint32_t* dst = buf + st * kStepDw + (2 * B / kWaves) * wave * 16;
-      const int so = 64 * (step + st);
-#pragma unroll
-      for (int j = 0; j < kLoads; ++j) {
-        const uint32_t vo = voff[j];  // (an array element passed straight makes the host pass drop the kernel's launch stub)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst + 256 * j, 16, vo, so, 0, 0);
-      }
+    for (int j = 0; j < kLoads; ++j) {
+      const uint32_t vo = voff[j];  // (an array element passed straight makes the host pass drop the kernel's launch stub)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst + 256 * j, 16, vo, so, 0, 0);
     }
   };
 
@@ -402,7 +408,7 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
   const int svoff = min(sload % (kScaleLoads / 2) * 64 + lane, slrows - 1) * nb;
   auto issue_scales = [&](int group) {
     uint32_t* dst = lsc + (group & 1) * 2 * B * 4 + sload * 256;
-    const int so = 16 * group, vo = svoff;
+    const int so = 16 * min(group, (nb >> 4) - 1), vo = svoff;  // (past the last: that again, not used)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsc, dst, 16, vo, so, 0, 0);
   };
   mx_u32x4 ga[kTm], gw[kTn];
@@ -415,18 +421,21 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
 #pragma unroll
     for (int j = 0; j < kTn; ++j) acc[i][j] = f32x16{};
 
-  const uint32_t pos[2] = {16u * (uint32_t)((2 * h) ^ ((lane >> 2) & 3)), 16u * (uint32_t)((2 * h + 1) ^ ((lane >> 2) & 3))};
-  const uint32_t arow = (uint32_t)(wm * (B / kWm) + r32) * 64, wrow = (uint32_t)(B + wn * (B / 2) + r32) * 64;
-  // Instruction kk (0, 1) of a step held in `buf`; scale byte `sel` of ca / cw.
-  // keep: false zeroes this lane's block of A (blocks past K).
+  uint32_t pos[2 * kS];  // of the chunk of each instruction of a stage
+#pragma unroll
+  for (int i = 0; i < 2 * kS; ++i) pos[i] = 16u * (uint32_t)place(4 * (i >> 1) + 2 * h + (i & 1), r32);
+  const uint32_t arow = (uint32_t)(wm * (B / kWm) + r32) * kRow, wrow = (uint32_t)(B + wn * (B / 2) + r32) * kRow;
+  // Instruction kk (0, 1: the first step's, 2, 3: the second's) of a stage held
+  // in `buf`; scale byte `sel` of ca / cw.  keep: false zeroes this lane's block
+  // of A (blocks past K).
   auto part = [&](const uint32_t* buf, auto kc, auto selc, bool keep) {
     constexpr int kk = decltype(kc)::value, sel = decltype(selc)::value;
     const uint8_t* const l = reinterpret_cast<const uint8_t*>(buf);
     mx_u32x4 fa[kTm], fw[kTn];
 #pragma unroll
-    for (int i = 0; i < kTm; ++i) fa[i] = *reinterpret_cast<const mx_u32x4*>(l + arow + 2048 * i + pos[kk]);
+    for (int i = 0; i < kTm; ++i) fa[i] = *reinterpret_cast<const mx_u32x4*>(l + arow + 32 * kRow * i + pos[kk]);
 #pragma unroll
-    for (int i = 0; i < kTn; ++i) fw[i] = *reinterpret_cast<const mx_u32x4*>(l + wrow + 2048 * i + pos[kk]);
+    for (int i = 0; i < kTn; ++i) fw[i] = *reinterpret_cast<const mx_u32x4*>(l + wrow + 32 * kRow * i + pos[kk]);
     if (!keep)
 #pragma unroll
       for (int i = 0; i < kTm; ++i) fa[i] = mx_u32x4{0u, 0u, 0u, 0u};
@@ -443,17 +452,17 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
   using C3 = std::integral_constant<int, 3>;
 
   // Whole groups of four steps, a stage of kS of them at a time.  Every stage
-  // issues the loads of three stages on, the first of a group (kStaged; else
+  // issues the loads of kRing - 1 stages on, the first of a group (kStaged; else
   // every second one) the scales of the next steps but those, without a branch,
   // so the number of loads in flight is the same everywhere: when a stage
-  // starts, the loads after its own are those of the next two stages and up to
-  // one set of scales.
+  // starts, the loads after its own are those of kRing - 2 stages and up to one
+  // set of scales.
   const int full = nb >> 4;
   const int last_pair = 2 * full - 1;
   auto stage = [&](auto uc, int q, uint32_t* cur, uint32_t* refill) {
     constexpr int u = decltype(uc)::value;  // the stage's first step in its group
     if constexpr (kStaged)
-      wait_vm<2 * kS * kLoads + (u == kS || (kS == 1 && u == 2) ? 1 : 0)>();
+      wait_vm<(kRing - 2) * kLoads + (kRing > 2 && u != 0 ? 1 : 0)>();
     else
       wait_vm<2 * kLoads + kTm + kTn>();
     ring_barrier();
@@ -480,22 +489,28 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
       load_scales(min((q >> 1) + 1, last_pair));
       asm volatile("" ::: "memory");
     }
-    issue(q + 3 * kS, refill);
+    issue(q + (kRing - 1) * kS, refill);
+    asm volatile("" ::: "memory");  // the loads go out before the reads below
     part(cur, C0{}, std::integral_constant<int, 2 * (u % 2)>{}, true);
     part(cur, C1{}, std::integral_constant<int, 2 * (u % 2) + 1>{}, true);
     if constexpr (kS == 2) {
-      part(cur + kStepDw, C0{}, C2{}, true);
-      part(cur + kStepDw, C1{}, C3{}, true);
+      part(cur, C2{}, C2{}, true);
+      part(cur, C3{}, C3{}, true);
     }
   };
   if constexpr (kStaged) issue_scales(0);
   asm volatile("" ::: "memory");
   issue(0, l0);
-  issue(kS, l1);
+  if (kRing > 2) issue(kS, l1);
   if (!kStaged && full > 0) load_scales(0);
   asm volatile("" ::: "memory");
-  issue(2 * kS, l2);
-  if constexpr (kS == 1) {
+  if (kRing > 2) issue(2 * kS, l2);
+  if constexpr (kRing == 2) {
+    for (int q = 0; q < 4 * full; q += 4) {
+      stage(C0{}, q, l0, l1);
+      stage(C2{}, q + 2, l1, l0);
+    }
+  } else if constexpr (kS == 1) {
     for (int q = 0; q < 4 * full; q += 4) {
       stage(C0{}, q, l0, l3);
       stage(C1{}, q + 1, l1, l0);
@@ -513,8 +528,8 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
   }
 
   // The rest of K, up to four steps: three of them are already on their way.
-  const int rest = nsteps - 4 * full;
-  if (rest > 3) {
+  const int rest = kStaged ? 0 : nsteps - 4 * full;
+  if (!kStaged && rest > 3) {
     // the last reads of l3 are done in every wave once all have passed here
     ring_barrier();
     issue(4 * full + 3, l3);
@@ -644,8 +659,8 @@ hipError_t launch_mx_product(const uint8_t* a, const uint8_t* as, const uint8_t*
   t.out = out;
   auto tiles = [&](int64_t B) { return ((M + B - 1) / B) * ((N + B - 1) / B); };
   // the largest tile that gives every CU one and that either side more than half
-  // fills (64 x 33792 x 7168: 64-row tiles 33 us, half-empty ones of 128 39;
-  // 2048 x 2048 x 4096: 128, 18 us, 64, 26; 512 x 7168 x 7168: both 38)
+  // fills (64 x 33792 x 7168: 64-row tiles 34 us, half-empty ones of 128 39;
+  // 2048 x 2048 x 4096: 128, 18 us, 64, 26)
   const int64_t side = M < N ? M : N;
   if (side > 128 && tiles(256) >= cus) return launch_square<256, 8>(t, out_bf16, s);
   if (side > 64 && tiles(128) >= cus) return launch_square<128, 8>(t, out_bf16, s);
