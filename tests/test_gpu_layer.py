@@ -264,3 +264,9 @@ def test_from_float_weights(k3):
     a, b = k3.mxfp4_unpack(p, s).double(), k3.mxfp4_unpack(wp, wsc).double()
     got = k3.mxfp4_linear(out, wp, wsc).double()
     assert bool(((got - a @ b.t()).abs() <= D * U * (a.abs() @ b.abs().t())).all())
+
+
+@pytest.mark.parametrize("T,E,k,D,I", [(16, 64, 64, 64, 64), (16, 8192, 8, 32, 32), (16, 70, 33, 96, 64), (1, 1, 1, 65536, 32),
+                                       (2, 1, 1, 32, 65536), (16, 2, 1, 8192, 4096)])
+def test_largest_counts_and_sides(k3, T, E, k, D, I):
+    check(k3, BASE.with_(T=T, E=E, k=k, D=D, I=I, config_id=112))
