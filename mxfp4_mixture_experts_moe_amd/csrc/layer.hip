@@ -831,7 +831,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
         }
       const __amdgpu_buffer_rsrc_t yb = __builtin_amdgcn_make_buffer_rsrc((void*)a.y, 0, a.T * a.k * a.D * 4, 0x00020000);
       const bool second = (rho == kHDigits) & (rows > 1);
-      const int at = (4 * ((row + (second ? 1 : 0)) * a.D + 32 * fg + 4 * g)) | ((rho == 0) | second ? 0 : kNoLane);
+      const int at = (4 * ((row + (second ? 1 : 0)) * a.D + 32 * fg + 4 * g)) | (((rho == 0) | second) ? 0 : kNoLane);
 #pragma unroll
       for (int mi = 0; mi < 2; ++mi) {
         u32x4_t v;

@@ -41,31 +41,6 @@ __device__ __forceinline__ uint32_t mx_codes(const float (&v)[8], uint32_t e) {
   return e == 255u ? 0x77777777u : r;
 }
 
-// Eight consecutive elements of a row as fp32 (kType: K3MOE_DTYPE_*); p is
-// 16-byte aligned.
-template <int kType>
-__device__ __forceinline__ void mx_load8(const void* p, float (&v)[8]) {
-  if constexpr (kType == K3MOE_DTYPE_F32) {
-    const float4 a = static_cast<const float4*>(p)[0], b = static_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    const mx_u32x4 a = *static_cast<const mx_u32x4*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (kType == K3MOE_DTYPE_BF16) {
-        v[2 * i] = __uint_as_float(a[i] << 16);
-        v[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-      } else {
-        typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-        const uint32_t ai = a[i];  // (a bit cast of a vector element itself reads element 0)
-        const h2 h = __builtin_bit_cast(h2, ai);
-        v[2 * i] = (float)h[0];
-        v[2 * i + 1] = (float)h[1];
-      }
-    }
-  }
-}
-
 // Largest of the four lanes 4q .. 4q+3: two quad permutes.
 __device__ __forceinline__ uint32_t mx_quad_max(uint32_t m) {
   m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0xB1, 0xF, 0xF, false));  // lane ^ 1
@@ -88,7 +63,11 @@ template <int kType, int kRaw>
 __device__ __forceinline__ uint32_t mx_quant8(const mx_u32x4 (&raw)[kRaw], bool saturate, uint32_t& e) {
   if constexpr (kType == K3MOE_DTYPE_F32) {
     float v[8];
-    mx_load8<kType>(&raw[0], v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t bits = raw[i >> 2][i & 3];
+      v[i] = __uint_as_float(bits);
+    }
     e = mx_scale_byte(mx_block_top(v), saturate);
     return mx_codes(v, e);
   } else {

@@ -37,11 +37,6 @@ __device__ __forceinline__ i32x8 operand(mx_u32x4 q) {
 }
 
 // Scale bytes at p (any alignment).
-__device__ __forceinline__ uint32_t load_u32(const uint8_t* p) {
-  uint32_t v;
-  __builtin_memcpy(&v, p, 4);
-  return v;
-}
 __device__ __forceinline__ uint2 load_u64(const uint8_t* p) {
   uint2 v;
   __builtin_memcpy(&v, p, 8);
