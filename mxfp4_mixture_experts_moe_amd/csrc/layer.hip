@@ -30,12 +30,12 @@
 // in that order, expert by expert, and streams their weights through a private
 // ring of three LDS stages that runs on across units.
 //
-// Measured (graph replay; 16 experts a token, D = 3584, I = 3072): one token 66
-// us, 281 MB of weights (plan 6.5, first weights in LDS 6 to 8 us into the second
+// Measured (graph replay; 16 experts a token, D = 3584, I = 3072): one token 64
+// us, 281 MB of weights (plan 4.8, first weights in LDS 6 to 8 us into the second
 // launch, the stream at 5.6 TB/s, sums 4); eight tokens 286 us, 1.58 GB, 5.5
 // TB/s; the two calls moe_route_topk and moe_mxfp4_ffn take 64 and 291 us there.
 // 13 tokens, 5 of 61 experts, D = 1056, I = 736: 36 us against 186; one token,
-// 2 of 8 experts, D = 128, I = 256: 18 us against 22.  What bounds it: the bytes
+// 2 of 8 experts, D = 128, I = 256: 17 us against 22.  What bounds it: the bytes
 // with many tokens, plan, first loads and sums with one.
 //
 // Hand-over.  A down unit needs h from every gate/up unit of its tile, a sum unit
@@ -194,10 +194,29 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
   __shared__ int s_ids[K3MOE_MAX_LAYER_TOKENS * K3MOE_MAX_TOPK];
   __shared__ int s_sum[kPlanThreads / 64][2];
   const int lane = tid & 63, wave = tid >> 6;
-  for (int e = tid; e < p.E; e += kPlanThreads) s_mask[e] = 0u;
   const int n = p.T * p.k;
+  __shared__ RouteScratch scratch[NPER > 0 ? kPlanThreads / 64 : 1];
+  if (p.T == 1) {
+    // one token: its experts are distinct, a tile each, in slot order; one wave
+    // (4.8 us for 896 experts; grouped like more tokens 6.5)
+    if (wave != 0) return;
+    int id = 0;
+    if constexpr (NPER > 0) {
+      float g = 0.0f;
+      route_token_reg<NPER>(p.logits, p.bias, p.E, p.k, p.normalize, p.route_scale, lane, scratch[0], id, g);
+      if (lane < n) p.ids[lane] = id, p.w[lane] = g;
+    } else {
+      id = p.ids[min(lane, n - 1)];
+    }
+    if (lane < n) {
+      p.tiles[lane] = make_int4(id, lane | 1 << 16, 0, lane | 1 << 16);
+      p.slot_row[lane] = lane;
+    }
+    if (lane == 0) p.head[0] = n, p.head[1] = 0;
+    return;
+  }
+  for (int e = tid; e < p.E; e += kPlanThreads) s_mask[e] = 0u;
   if constexpr (NPER > 0) {
-    __shared__ RouteScratch scratch[kPlanThreads / 64];
     if (wave < p.T) {
       int id = 0;
       float g = 0.0f;
