@@ -270,3 +270,20 @@ def test_from_float_weights(k3):
                                        (2, 1, 1, 32, 65536), (16, 2, 1, 8192, 4096)])
 def test_largest_counts_and_sides(k3, T, E, k, D, I):
     check(k3, BASE.with_(T=T, E=E, k=k, D=D, I=I, config_id=112))
+
+
+@pytest.mark.parametrize("T,E", [(1, 8), (5, 70), (3, 1100)])
+def test_logits_that_are_no_numbers(k3, T, E):
+    """The router's ids and weights bit for bit, whatever the logits; a token's NaN weights stay its own."""
+    cfg = BASE.with_(T=T, E=E, k=4, D=64, I=64, config_id=113)
+    dev = upload_experts(cfg, expert_blocks(k3))
+    batch, z, b = inputs(cfg)
+    clean = run(k3, dev, bf16_dev(batch.x), z, b, cfg.k)
+    z[T - 1, :] = np.nan
+    z[0, 1:3] = np.inf, -np.inf
+    out, ids, w = run(k3, dev, bf16_dev(batch.x), z, b, cfg.k)
+    rids, rw = k3.moe_route_topk(torch.from_numpy(z).cuda(), torch.from_numpy(b).cuda(), cfg.k)
+    assert torch.equal(ids, rids) and torch.equal(w.view(torch.int32), rw.view(torch.int32))
+    assert torch.equal(torch.isnan(out).all(dim=1), torch.isnan(w).any(dim=1))
+    for t in range(1, T - 1):
+        assert torch.equal(out[t], clean[0][t]) and torch.equal(ids[t], clean[1][t])
