@@ -20,6 +20,7 @@
 //     busy 0.54 of a CU's time) and by load latency for small ones (128 x 7168 x
 //     3584: 7.8-8.3 us).
 #include "mx_common.h"
+#include "mx_shape.h"
 
 #include <type_traits>
 
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
 
   // this wave's turns: pieces s0, s0 + kw, ... of groups g0, g0 + step, ...
   const int gw = __builtin_amdgcn_readfirstlane(wave / a.kw), s0 = wave - gw * a.kw;
-  const int ngroups = (a.N + 15) >> 4;
+  const int ngroups = mx_groups(a.N, 16);
   struct Piece {
     mx_u32x4 q[4], sc;  // sc: 16 scale bytes; kTail: four dwords of one byte, this lane's blocks'
   };
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
     if constexpr (!kTail) d.sc = __builtin_amdgcn_raw_buffer_load_b128(rs, row + 16 * ss, 0, 0);
   };
   const int gstep = (int)gridDim.x * a.rw;
-  const int rounds = __builtin_amdgcn_readfirstlane((ngroups + gstep - 1) / gstep);  // the same for every wave: the barriers below
+  const int rounds = __builtin_amdgcn_readfirstlane(mx_few_rounds(a.N, a.rw, (int)gridDim.x));  // the same for every wave: the barriers below
   int grp = (int)blockIdx.x * a.rw + gw, done = 0;   // done: turns of this round behind us
   int lgrp = grp, ldone = 0;                         // the same of the next piece to ask for
   Piece ring[kFewAhead];
@@ -271,7 +272,7 @@ __global__ __launch_bounds__(kFewWaves * 64, 4) void mx_few_kernel(FewArgs a) {
 #pragma unroll
     for (int i = 0; i < kFewAhead; ++i) {
       turn(ring[i]);
-      if (rd == rounds) return;
+      if (rd >= rounds) return;
     }
   }
 }
@@ -297,8 +298,7 @@ constexpr int kXcds = 8;
 
 struct TileArgs {
   const uint8_t *a, *as, *w, *ws;
-  int64_t M;
-  int N, nb;
+  int M, N, nb;
   void* out;
 };
 
@@ -332,7 +332,7 @@ __global__ __launch_bounds__(kWaves * 64) void mx_tile_kernel(TileArgs t) {
 
   // Tile order: the ids an XCD gets (id % 8) are a contiguous run of the
   // logical order, which walks groups of four tile rows column by column.
-  const int mt = (int)((t.M + B - 1) / B), nt = (t.N + B - 1) / B;
+  const int mt = mx_groups(t.M, B), nt = mx_groups(t.N, B);
   const int64_t total = (int64_t)mt * nt;
   int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (id >= total) return;
@@ -565,13 +565,8 @@ size_t few_lds(int64_t M, int nb) { return (size_t)(M < kFewRows ? M : kFewRows)
 
 template <int kX>
 hipError_t launch_few(const FewArgs& a, bool bf16, hipStream_t s) {
-  // the fewest rounds that two workgroups per CU allow, and as few workgroups as
-  // that leaves: all have the same number of rounds, and A is staged less often
   const unsigned chunks = (unsigned)((a.M + kFewRows - 1) / kFewRows);
-  const int ngroups = (a.N + 15) / 16, most = 2 * device_cu_count() * a.rw;
-  const int rounds = (ngroups + most - 1) / most;
-  const int64_t wgs = (ngroups + (int64_t)rounds * a.rw - 1) / ((int64_t)rounds * a.rw);
-  const dim3 grid((unsigned)wgs, chunks), block((unsigned)(64 * a.kw * a.rw));
+  const dim3 grid((unsigned)mx_few_grid(a.N, a.rw, device_cu_count()).wgs, chunks), block((unsigned)(64 * a.kw * a.rw));
   auto go = [&](auto b, auto t) { hipLaunchKernelGGL((mx_few_kernel<kX, decltype(b)::value, decltype(t)::value>), grid, block, 0, s, a); };
   const bool tail = a.nb % 16 != 0;
   if (bf16 && tail) go(std::true_type{}, std::true_type{});
@@ -583,9 +578,8 @@ hipError_t launch_few(const FewArgs& a, bool bf16, hipStream_t s) {
 
 template <int B, int kWaves>
 hipError_t launch_square(const TileArgs& t, bool bf16, hipStream_t s) {
-  const int64_t total = ((t.M + B - 1) / B) * ((t.N + B - 1) / B);
-  const int64_t gx = total < (1 << 20) ? total : 1 << 20;  // (a grid dimension has fewer than 2^32 threads)
-  const dim3 grid((unsigned)gx, (unsigned)((total + gx - 1) / gx)), block(kWaves * 64);
+  const MxTileGrid g = mx_tile_grid(t.M, t.N, B);
+  const dim3 grid(g.x, g.y), block(kWaves * 64);
   auto go = [&](auto st, auto b) {
     hipLaunchKernelGGL((mx_tile_kernel<B, kWaves, decltype(st)::value, decltype(b)::value>), grid, block, 0, s, t);
   };
@@ -640,7 +634,7 @@ hipError_t launch_mx_product(const uint8_t* a, const uint8_t* as, const uint8_t*
                              int K, bool out_bf16, void* out, hipStream_t s) {
   int per, kw, rw;
   few_split(K / 32, per, kw, rw);
-  const int64_t cus = device_cu_count(), wgs = ((N + 15) / 16 + rw - 1) / rw;
+  const int64_t cus = device_cu_count(), wgs = (mx_groups(N, 16) + rw - 1) / rw;
   if (few_lds(M, K / 32) <= kFewLds && (M <= kFewRows || (K >= 4096 && (M + kFewRows - 1) / kFewRows * wgs <= 2 * cus)))
     return launch_mx_few(a, -1, as, w, ws, M, N, K, 0, out_bf16, out, s);
   TileArgs t{};
@@ -648,11 +642,11 @@ hipError_t launch_mx_product(const uint8_t* a, const uint8_t* as, const uint8_t*
   t.as = as;
   t.w = w;
   t.ws = ws;
-  t.M = M;
+  t.M = (int)M;
   t.N = N;
   t.nb = K / 32;
   t.out = out;
-  auto tiles = [&](int64_t B) { return ((M + B - 1) / B) * ((N + B - 1) / B); };
+  auto tiles = [&](int B) { return mx_tile_grid(t.M, N, B).total; };
   // the largest tile that gives every CU one and that either side more than half
   // fills (64 x 33792 x 7168: 64-row tiles 34 us, half-empty ones of 128 39;
   // 2048 x 2048 x 4096: 128, 18 us, 64, 26)
