@@ -15,9 +15,12 @@
 // instruction adds the products of a block in a fixed-point window of about
 // 2^14 below the largest (measured; e4m3 operands of 8 binades already lose
 // bits) and everything else in fp32: digits times E2M1 codes span 0.5 .. 96 and
-// stay inside, so each column is as exact as an fp32 sum.  x takes four
-// digits (2^-19 of its block's largest; a bf16 value within 2^-11 of that is
-// exact), h five (2^-24).
+// stay inside, so each column is as exact as an fp32 sum.  Both x and h take
+// five digits: 2^-24 of the block's largest, half a step of fp32 there, and a
+// bf16 element down to 2^-17 of it is held exactly.  (Four for x, 2^-19, exact
+// down to 2^-12, cost the other elements of a block their bits where one stands
+// far above them: with channels of 2^13 times the rest that no weight reads, the
+// outputs were off by up to 18 times the bound of an fp32 sum.)
 //
 // With a few tokens the layer is a stream over the chosen experts' bytes
 // (about 4 flop per byte and row): what costs time beside the stream are its
@@ -77,13 +80,12 @@
 namespace k3moe {
 namespace {
 
-constexpr int kXDigits = 4, kHDigits = 5;
+constexpr int kDigits = 5;
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kPlane = 512;     // bytes of one digit of a row's stage
-constexpr int kXRow = kXDigits * kPlane;        // x: digits of a (row, stage); its scales are apart
-constexpr int kHRow = kHDigits * kPlane + 16;   // h: digits and scales of a (row, stage)
+constexpr int kPlane = 512;                // bytes of one digit of a row's stage
+constexpr int kRow = kDigits * kPlane + 16;  // digits and scales of a (row, stage), of x and of h
 
 // What h holds before it is written.  A digit is an integer or NaN, so no byte
 // of it is e4m3's smallest subnormal; a scale byte is at most 252.
@@ -98,15 +100,14 @@ constexpr uint32_t kNoDigit = 0x01010101u, kNoScale = 0xFFFFFFFFu;
 // 4 g + r: a lane of group g reads its four rounds as one dword.
 //
 // Eight values in that order (those of quarter i of the block: elements 4i + t
-// and 16 + 4i + t) as N digits: out[p] = eight bytes.
-template <int N>
-__device__ __forceinline__ void digits8(const float (&v)[8], uint32_t e, uint2 (&out)[N]) {
+// and 16 + 4i + t) as digits: out[p] = eight bytes.
+__device__ __forceinline__ void digits8(const float (&v)[8], uint32_t e, uint2 (&out)[kDigits]) {
   const float unit = __uint_as_float((257u - e) << 23);  // 2^(130 - e): |v| * unit < 16
   float q[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) q[i] = v[i] * unit;
 #pragma unroll
-  for (int p = 0; p < N; ++p) {
+  for (int p = 0; p < kDigits; ++p) {
     float d[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -144,8 +145,7 @@ struct LayerPlan {
   float route_scale;
   int32_t* ids;    // [T, k]
   float* w;        // [T, k]
-  uint8_t* xd;     // [T][stages][kXRow] digits of x
-  uint8_t* xs;     // [T][stages][16] their scale bytes
+  uint8_t* xd;     // [T][stages][kRow] digits and scales of x
   int4* tiles;     // expert, first row | rows << 16, tokens of the rows (a byte each), the expert's tiles (first | count << 16)
   int32_t* slot_row;
   int32_t* head;   // [0] tiles, [1] next ticket
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
     const int u = (int)(blockIdx.x - 1) * kPlanThreads + tid;
     if ((int)blockIdx.x > p.x_wgs) {
       const int c = u - p.x_wgs * kPlanThreads, f = c - p.n_h;
-      const uint32_t v = c % (kHRow / 16) == kHRow / 16 - 1 ? kNoScale : kNoDigit;
+      const uint32_t v = c % (kRow / 16) == kRow / 16 - 1 ? kNoScale : kNoDigit;
       if (c < p.n_h) p.h[c] = u32x4_t{v, v, v, v};
       else if (f < p.n_flags / 4) reinterpret_cast<u32x4_t*>(p.flags)[f] = u32x4_t{0u, 0u, 0u, 0u};
       return;
@@ -180,13 +180,12 @@ __global__ __launch_bounds__(kPlanThreads) void layer_plan_kernel(LayerPlan p) {
     v[1] = __uint_as_float(hi.x << 16), v[3] = __uint_as_float(hi.x & 0xFFFF0000u);
     v[5] = __uint_as_float(hi.y << 16), v[7] = __uint_as_float(hi.y & 0xFFFF0000u);
     const uint32_t e = digit_exp(mx_block_top(v));
-    uint2 d[kXDigits];
-    digits8<kXDigits>(v, e, d);
-    const int64_t piece = (int64_t)t * nst + (b >> 4);
+    uint2 d[kDigits];
+    digits8(v, e, d);
+    uint8_t* const piece = p.xd + ((int64_t)t * nst + (b >> 4)) * kRow;
 #pragma unroll
-    for (int q = 0; q < kXDigits; ++q)
-      *reinterpret_cast<uint2*>(p.xd + piece * kXRow + q * kPlane + digit_at(b & 15, i, q)) = d[q];
-    if (i == 0) p.xs[piece * 16 + 4 * (b & 3) + ((b & 15) >> 2)] = (uint8_t)(e - 3u);
+    for (int q = 0; q < kDigits; ++q) *reinterpret_cast<uint2*>(piece + q * kPlane + digit_at(b & 15, i, q)) = d[q];
+    if (i == 0) piece[kDigits * kPlane + 4 * (b & 3) + ((b & 15) >> 2)] = (uint8_t)(e - 3u);
     return;
   }
   __shared__ uint32_t s_mask[K3MOE_MAX_EXPERTS_FFN];  // tokens of each expert
@@ -297,10 +296,8 @@ constexpr int kW = (kChunks + 63) / 64;  // weight loads per stage
 // compiler linearise the loop and carry the wave-uniform state in vector
 // registers.
 constexpr int kSlot = kW * 1024;       // bytes of a weight stage in LDS
-constexpr int kXRowLds = kXRow + 64;   // second row of a tile: other banks than the first
-constexpr int kHRowLds = 3 * 1024 + 128;
-constexpr int kXScales = 2 * kXRowLds;  // scale bytes of x behind its two rows
-constexpr int kActBytes = kHRowLds + 3 * 1024;  // a stage's activations: the larger of both kinds
+constexpr int kRowLds = 3 * 1024 + 128;  // second row of a tile: other banks than the first
+constexpr int kActBytes = kRowLds + 3 * 1024;  // a stage's activations
 constexpr int kActBufs = 2;
 constexpr int kNt = 2;               // cache policy of the weight loads: nontemporal
 constexpr int kDevScope = 16;        // cache policy of loads and stores that other XCDs must agree on (sc1)
@@ -311,13 +308,13 @@ constexpr int kNoLane = INT32_MIN;  // buffer offset past every buffer: the lane
 // one after another, 11.4 ns each (measured; to different lines they overlap).
 constexpr int kFlagStride = 32;
 constexpr int kWaveLds = kRing * kSlot + kActBufs * kActBytes;
-static_assert(kHRow <= 3 * 1024 && kXScales + 1024 <= kActBytes, "activation buffers");
+static_assert(kRow <= 3 * 1024, "activation buffers");
 static_assert(kWaves * kWaveLds + 1024 <= 160 * 1024, "LDS");
 
 enum { kGateUp = 0, kDown = 1, kSum = 2, kNone = 3 };
 
 struct LayerArgs {
-  const uint8_t *xd, *xs;
+  const uint8_t* xd;
   const uint8_t *w1, *w3, *w2;
   int D, I, T, k;
   const int4* tiles;
@@ -434,6 +431,11 @@ __device__ __forceinline__ float row_down(float v) {
   return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x100 + kN, 0xF, 0xF, true));
 }
 
+// In column 5 r: a row's sum, its digits' columns smallest first.
+__device__ __forceinline__ float digit_sum(float c) {
+  return c + (row_down<1>(c) + (row_down<2>(c) + (row_down<3>(c) + row_down<4>(c))));
+}
+
 __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves][kWaveLds];
   __shared__ int fifo[kWaves][4][2];  // units in the ring: kind | fg << 1, row | rows << 16
@@ -505,6 +507,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   // matrix.  The instruction's own offset counts for the LDS address, too, so
   // loads 0-3, 4-7 and 8 share a base each, and their lane offsets are
   const int lane16 = 16 * lane;  // 0-3
+  const int rest16 = lane < (kRow - 2048) / 16 ? lane16 : kNoLane;  // a row of x, third load: nothing behind its scales
   int wofs4 = 0, wofs5 = 0, wofs8 = 0;  // 4; 5-7; 8 (half of it past the stage: not asked for)
   static_assert(kW == 9, "three bases");
 
@@ -520,10 +523,9 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   const uint8_t *wb0 = nullptr, *wb1 = nullptr;  // the next stage's weights; gate/up: and those of the stage after it
   int grp2x = 0;             // bytes of a stage's two whole groups, less what lies before the stage
   int act0 = 0, act1 = 0;    // where the stage's activations are, per row of the tile
-  int sco = 0;               // per lane: scale bytes of tile row `lane`
   int left = 0;              // stages of iu not yet issued (0: nu's are the next)
   int want = 0;              // activations of the stage issued last: rows, + 4 for h; 0: none
-  int want0 = 0, want1 = 0, wantsc = 0;  // where they are
+  int want0 = 0, want1 = 0;  // where they are
   int inflight = 0, buf_i = 0, abuf_i = 0, pushed = 0;
   bool bad = false;          // a bounded wait ran out
 
@@ -557,11 +559,12 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     }
   };
   auto load_x = [&](uint8_t* dst, int at) __attribute__((always_inline)) {
-    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xd, 0, a.T * nst13 * kXRow, 0x00020000);
+    const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xd, 0, a.T * nst13 * kRow, 0x00020000);
     const int so = uni(at);
     const auto l = (__attribute__((address_space(3))) void*)(uintptr_t)dst;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 0, 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, lane16, so, 1024, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, l, 16, rest16, so, 2048, 0);
   };
   auto prep = [&]() __attribute__((always_inline)) {
     iu = nu;
@@ -579,9 +582,8 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     wofs4 = lane < 16 ? 4096 + lane16 : wofs5;
     wofs8 = lane < 32 ? wofs5 + 4096 : kNoLane;
     left = gu ? 2 * nst13 : nst2;
-    act0 = gu ? t0 * nst13 * kXRow : iu.row * a.hstride;
-    act1 = gu ? t1 * nst13 * kXRow : act0 + a.hstride;
-    sco = (lane == 1 ? t1 : t0) * nst13 * 16;
+    act0 = gu ? t0 * nst13 * kRow : iu.row * a.hstride;
+    act1 = gu ? t1 * nst13 * kRow : act0 + a.hstride;
     int* const f = fifo[wave][pushed & 3];
     ++pushed;
     f[0] = iu.kind | iu.fg << 1;  // (every lane, the same)
@@ -593,13 +595,10 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
       uint8_t* const ad = al + abuf_i * kActBytes;
       if (want & 4) {
         load_h(ad, want0, false);
-        if (want & 2) load_h(ad + kHRowLds, want1, false);
+        if (want & 2) load_h(ad + kRowLds, want1, false);
       } else {
         load_x(ad, want0);
-        if (want & 2) load_x(ad + kXRowLds, want1);
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc((void*)a.xs, 0, a.T * nst13 * 16, 0x00020000);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(uintptr_t)(ad + kXScales), 16, wantsc, 0, 0,
-                                                 0);
+        if (want & 2) load_x(ad + kRowLds, want1);
       }
       abuf_i ^= 1;
     }
@@ -628,15 +627,13 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     want = gu ? (odd ? iu.rows : 0) : iu.rows + 4;
     want0 = act0;
     want1 = act1;
-    wantsc = sco;
     const int on = gu && odd ? 0 : 1;  // columns go on after w3
     const uint8_t* const next = wb0 + kMatBytes;
     wb0 = gu ? wb1 : next;
     wb1 = next;
     grp2x -= on * kMatBytes;
-    act0 += on * (gu ? kXRow : kHRow);
-    act1 += on * (gu ? kXRow : kHRow);
-    sco += on * 16;
+    act0 += on * kRow;
+    act1 += on * kRow;
     ++inflight;
     buf_i = buf_i == kRing - 1 ? 0 : buf_i + 1;
   };
@@ -661,11 +658,10 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
   f32x4_t acc[2][2] = {{zero, zero}, {zero, zero}};  // [w1 / w3 by turns][16-row group]
   BOperand bop{};
-  // LDS offsets of this lane's digits.  gate/up: column 4 r + p is digit p of
-  // tile row r; columns from 8 on repeat.  down: column 5 r + p likewise.
-  const int xp = rho & 3, hr = rho >= kHDigits && rho < 2 * kHDigits ? 1 : 0, hp = rho < 2 * kHDigits ? rho - hr * kHDigits : 0;
-  const int xoff0 = xp * kPlane + 16 * (g ^ xp), xoff1 = xp * kPlane + 16 * ((4 + g) ^ xp);
-  const int hoff0 = hp * kPlane + 16 * (g ^ hp), hoff1 = hp * kPlane + 16 * ((4 + g) ^ hp);
+  // LDS offsets of this lane's digits: column 5 r + p is digit p of tile row r;
+  // columns from 10 on repeat.
+  const int dr = rho >= kDigits && rho < 2 * kDigits ? 1 : 0, dp = rho < 2 * kDigits ? rho - dr * kDigits : 0;
+  const int doff0 = dp * kPlane + 16 * (g ^ dp), doff1 = dp * kPlane + 16 * ((4 + g) ^ dp);
   int woff[4], rot0[4], rot1[4];  // per round: this lane's block, the rounds of its operand's two blocks
 #pragma unroll
   for (int rnd = 0; rnd < 4; ++rnd) {
@@ -673,7 +669,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
     rot0[rnd] = 128 * ((rnd + (g >> 1)) & 3);
     rot1[rnd] = 128 * ((rnd + 2 + (g >> 1)) & 3);
   }
-  const uint32_t xsub = 0x05050505u * (uint32_t)xp, hsub = 0x05050505u * (uint32_t)hp;
+  const uint32_t sub = 0x05050505u * (uint32_t)dp;
 
   // One pass of the loop takes a stage out of the ring and asks for a later one;
   // while the ring fills, it only asks.
@@ -681,7 +677,6 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
   int s = 0, nst = 0;  // stage of the open unit, its stages
   // the open unit, and this lane's operand pieces in an activation buffer
   int row = 0, rows = 0, fg = 0, cut = 0, off0 = 0, off1 = 0, offs = 0;
-  uint32_t sub = 0;
   bool down = false;
   for (;;) {
     // the next ticket, once all stages of this unit have been asked for: one
@@ -709,11 +704,10 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
         nst = down ? nst2 : 2 * nst13;
         cut = (down ? nfg : nfu) & 15;  // blocks of a last, shorter stage (0: none)
         // column rho's tile row and digit
-        const int r = rows == 1 ? 0 : down ? hr * kHRowLds : (rho & 4) ? kXRowLds : 0;
-        off0 = r + (down ? hoff0 : xoff0);
-        off1 = r + (down ? hoff1 : xoff1);
-        offs = 4 * g + (down ? r + kHDigits * kPlane : kXScales + (r ? 16 : 0));
-        sub = down ? hsub : xsub;
+        const int r = rows == 1 ? 0 : dr * kRowLds;
+        off0 = r + doff0;
+        off1 = r + doff1;
+        offs = r + kDigits * kPlane + 4 * g;
       }
       // The stage has landed once only loads asked for after its own are out:
       // the weights of two stages and, before the newer of them, activations of
@@ -770,12 +764,12 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
             bad = true;
             break;
           }
-          const int at = row * a.hstride + s * kHRow;
+          const int at = row * a.hstride + s * kRow;
           for (int j = 0; j < 2; ++j) {
             uint8_t* const aj = al + (abuf_c ^ (1 - j)) * kActBytes;
             if (j == 1 && (inflight == 0 || s + 1 >= nst)) break;
-            load_h(aj, at + j * kHRow, true);
-            if (rows > 1) load_h(aj + kHRowLds, at + a.hstride + j * kHRow, true);
+            load_h(aj, at + j * kRow, true);
+            if (rows > 1) load_h(aj + kRowLds, at + a.hstride + j * kRow, true);
           }
           __builtin_amdgcn_s_sleep(1);
           wait_vm<0>();
@@ -807,16 +801,17 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
       }
     if (++s < nst) continue;
 
-    // lane holds, in column rho, features 4 g + v of each 16-row group
+    // lane holds, in column rho, features 4 g + v of each 16-row group; those of
+    // columns 0 and 5 hold the tile's rows
+    const bool second = (rho == kDigits) & (rows > 1), mine = (rho == 0) | second;
     if (!down) {
       float gt[8], up[8];  // feature 4 g + v of group i at 2 v + i: the digits' byte order
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
-          const float c = acc[0][i][v], u = acc[1][i][v];
-          gt[2 * v + i] = c + (row_down<1>(c) + (row_down<2>(c) + row_down<3>(c)));
-          up[2 * v + i] = u + (row_down<1>(u) + (row_down<2>(u) + row_down<3>(u)));
+          gt[2 * v + i] = digit_sum(acc[0][i][v]);
+          up[2 * v + i] = digit_sum(acc[1][i][v]);
         }
       float h[8];
       uint32_t top = 0u;
@@ -828,29 +823,24 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
       top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
       top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
       const uint32_t e = digit_exp(top);
-      uint2 dg[kHDigits];
-      digits8<kHDigits>(h, e, dg);
+      uint2 dg[kDigits];
+      digits8(h, e, dg);
       const __amdgpu_buffer_rsrc_t hb = __builtin_amdgcn_make_buffer_rsrc((void*)a.h, 0, a.T * a.k * a.hstride, 0x00020000);
-      const bool mine = ((rho & 3) == 0) & ((rho >> 2) < rows);
-      const int at = ((row + (rho >> 2)) * a.hstride + (fg >> 4) * kHRow) | (mine ? 0 : kNoLane);
+      const int at = ((row + (second ? 1 : 0)) * a.hstride + (fg >> 4) * kRow) | (mine ? 0 : kNoLane);
       typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
-      for (int p = 0; p < kHDigits; ++p)
+      for (int p = 0; p < kDigits; ++p)
         __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{dg[p].x, dg[p].y}, hb, at + p * kPlane + digit_at(fg & 15, g, p), 0, kDevScope);
       __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(e - 3u), hb,
-                                           (at + kHDigits * kPlane + 4 * (fg & 3) + ((fg & 15) >> 2)) | (g == 0 ? 0 : kNoLane), 0, kDevScope);
+                                           (at + kDigits * kPlane + 4 * (fg & 3) + ((fg & 15) >> 2)) | (g == 0 ? 0 : kNoLane), 0, kDevScope);
     } else {
       f32x4_t sum[2];
 #pragma unroll
       for (int mi = 0; mi < 2; ++mi)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float c = acc[0][mi][v];
-          sum[mi][v] = c + (row_down<1>(c) + (row_down<2>(c) + (row_down<3>(c) + row_down<4>(c))));
-        }
+        for (int v = 0; v < 4; ++v) sum[mi][v] = digit_sum(acc[0][mi][v]);
       const __amdgpu_buffer_rsrc_t yb = __builtin_amdgcn_make_buffer_rsrc((void*)a.y, 0, a.T * a.k * a.D * 4, 0x00020000);
-      const bool second = (rho == kHDigits) & (rows > 1);
-      const int at = (4 * ((row + (second ? 1 : 0)) * a.D + 32 * fg + 4 * g)) | (((rho == 0) | second) ? 0 : kNoLane);
+      const int at = (4 * ((row + (second ? 1 : 0)) * a.D + 32 * fg + 4 * g)) | (mine ? 0 : kNoLane);
 #pragma unroll
       for (int mi = 0; mi < 2; ++mi) {
         u32x4_t v;
@@ -902,7 +892,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct LayerWorkspace {
-  size_t ids, w, xd, xs, tiles, slot_row, head, flags, h, y, total;
+  size_t ids, w, xd, tiles, slot_row, head, flags, h, y, total;
   int64_t n, n_flags;
   int hstride;
 };
@@ -917,11 +907,10 @@ LayerWorkspace layer_layout(int64_t T, int32_t D, int32_t I, int32_t k) {
   const int nst13 = (D / 32 + 15) / 16, nst2 = (I / 32 + 15) / 16;
   l.n = T * k;
   l.n_flags = (int64_t)(D / 32) * kFlagStride;
-  l.hstride = nst2 * kHRow;
+  l.hstride = nst2 * kRow;
   l.ids = take(4 * l.n);
   l.w = take(4 * l.n);
-  l.xd = take((size_t)T * nst13 * kXRow);
-  l.xs = take((size_t)T * nst13 * 16);
+  l.xd = take((size_t)T * nst13 * kRow);
   l.tiles = take(16 * l.n);
   l.slot_row = take(4 * l.n);
   l.head = take(16);
@@ -952,7 +941,6 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t s) {
   p.ids = c.ids ? c.ids : reinterpret_cast<int32_t*>(ws + l.ids);
   p.w = c.w ? c.w : reinterpret_cast<float*>(ws + l.w);
   p.xd = ws + l.xd;
-  p.xs = ws + l.xs;
   p.tiles = reinterpret_cast<int4*>(ws + l.tiles);
   p.slot_row = reinterpret_cast<int32_t*>(ws + l.slot_row);
   p.head = reinterpret_cast<int32_t*>(ws + l.head);
@@ -979,7 +967,6 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t s) {
 
   LayerArgs a{};
   a.xd = p.xd;
-  a.xs = p.xs;
   a.w1 = c.w1;
   a.w3 = c.w3;
   a.w2 = c.w2;

@@ -3,7 +3,8 @@ oracle, element by element.
 
 Bound, with u = 2^-24 (half a step of fp32), every product summed in some order
 in fp32: a sum of n products is off by at most n u times the sum of their
-magnitudes.  x enters as four base-32 digits relative to its 32-block: with
+magnitudes.  x enters as base-32 digits relative to its 32-block, for which the
+bound allows four (the layer takes five): with
 8 * 2^s <= max |x| the last digit's half step is 2^s * 32^-3 / 2 <= 2^-19 max |x|
 of the block; h as five, 2^-24 max |h|.  The digits' magnitudes add up to at most
 the value's plus one step of each (|d0| <= |q| + 1/2, later ones below 1/32 of
