@@ -68,7 +68,9 @@
 // answers.  y is read with device-scope loads only, and counted per feature group
 // (device-scope add, no return) once the stores have completed, that is once a
 // later wait of the in-order vector-memory counter covers them: three stages
-// later, at no cost, or at once where the ring runs dry.  Fences would write
+// later, at no cost, or at once where the ring runs dry.  On the reading side the
+// wave's branch on the count holds the loads of y back; that the compiler does,
+// too, takes a barrier to it (a relaxed load orders nothing).  Fences would write
 // back or invalidate a whole L2 instead (57 ns each, measured, for every wave of
 // the XCD in turn).
 #include "mx_common.h"
@@ -541,6 +543,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void layer_main_kernel(LayerArgs a)
         break;
       }
     }
+    asm volatile("" ::: "memory");  // what the count stands for is loaded behind it
   };
   // (again: the caches' copy turned out to be old)
   auto load_h = [&](uint8_t* dst, int at, bool again) __attribute__((always_inline)) {

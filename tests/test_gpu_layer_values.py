@@ -1,5 +1,5 @@
-"""moe_mxfp4_layer on values that its number formats have to cope with: a few
-channels of x far above the rest.
+"""moe_mxfp4_layer on values that its number formats have to cope with (a few
+channels of x far above the rest) and over workspaces of NaN.
 
 Bound for such x, with u = 2^-24 (half a step of fp32).  A 32-block of x enters
 as five base-32 digits, the first of step 2^s with max |x| < 2^(s + 4), so the
@@ -78,3 +78,18 @@ def test_wide_channels_leave_the_others_their_bits(k3, T, D, I):
     err = np.abs(out.cpu().double().numpy() - ref)
     print(f"[layer] wide channels T={T} D={D} I={I}: worst error / bound {np.max(err / bound):.3f}", flush=True)
     assert np.all(err <= bound)
+
+
+@pytest.mark.parametrize("T,E,k,D,I", [(1, 8, 2, 2048, 64), (4, 8, 8, 64, 2048), (9, 16, 4, 1056, 736)])
+def test_sums_read_finished_rows_alone(k3, T, E, k, D, I):
+    """Few sums behind long down units, and many behind short ones, over workspaces whose every float is NaN: no sum
+    takes a row of y that its down unit has not written yet, in any of the calls."""
+    g = torch.Generator().manual_seed(T + D)
+    dev, _ = experts(k3, g, E, D, I, [])
+    x, z = torch.randn((T, D), generator=g).bfloat16().cuda(), torch.randn((T, E), generator=g).cuda()
+    want = k3.moe_mxfp4_layer(x, z, None, *dev, k)[0]
+    assert bool(torch.isfinite(want).all())
+    work = torch.empty(k3.moe_mxfp4_layer_workspace_size(T, D, I, E, k), dtype=torch.uint8, device="cuda")
+    for i in range(24):
+        work.fill_(255)
+        assert torch.equal(k3.moe_mxfp4_layer(x, z, None, *dev, k, workspace=work)[0], want), i
