@@ -40,7 +40,7 @@ typedef enum {
   K3MOE_ERR_NULL = -1,        /* a required pointer is NULL */
   K3MOE_ERR_SHAPE = -2,       /* a size argument is out of range or inconsistent */
   K3MOE_ERR_ALIGN = -3,       /* a device pointer is not 16-byte aligned */
-  K3MOE_ERR_WORKSPACE = -4,   /* workspace smaller than moe_mxfp4_ffn_workspace_size() */
+  K3MOE_ERR_WORKSPACE = -4,   /* workspace smaller than the call's ..._workspace_size() */
   K3MOE_ERR_UNSUPPORTED = -5, /* unknown enum value (activation, output dtype) */
   K3MOE_ERR_DEVICE = -6,      /* the HIP runtime refused a launch (e.g. no gfx950 device) */
   K3MOE_ERR_TOO_LARGE = -7    /* moe_mxfp4_ffn_noalloc: the sizes need more than its fixed scratch */

@@ -500,7 +500,7 @@ const char* k3moe_status_str(int status) {
     case K3MOE_ERR_NULL: return "a required pointer is NULL";
     case K3MOE_ERR_SHAPE: return "a size argument is out of range or inconsistent";
     case K3MOE_ERR_ALIGN: return "a device pointer is not 16-byte aligned";
-    case K3MOE_ERR_WORKSPACE: return "workspace is smaller than moe_mxfp4_ffn_workspace_size()";
+    case K3MOE_ERR_WORKSPACE: return "workspace is smaller than the call's own workspace_size() function says";
     case K3MOE_ERR_UNSUPPORTED: return "unsupported enum value";
     case K3MOE_ERR_DEVICE: return "the HIP runtime refused a launch";
     case K3MOE_ERR_TOO_LARGE:

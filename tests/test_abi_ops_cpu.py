@@ -113,3 +113,10 @@ def test_layer_checks_and_workspace(k3):
     for bad in (dict(T=17), dict(T=-1), dict(D=48), dict(I=0), dict(D=65536 + 32), dict(E=0), dict(k=9), dict(k=0), dict(E=8193)):
         assert call(ok, **bad) == ERR_SHAPE, bad
     assert call([None] * 6, T=0, out=None, ids=None, w=None, ws=None, n=0) == OK
+
+
+def test_short_workspace_message_names_no_other_call(k3):
+    """One status for every call that takes a workspace: its text sends the caller to that call's own size function."""
+    text = k3.status_str(ERR_WORKSPACE)
+    assert "workspace" in text and "moe_mxfp4_ffn_workspace_size" not in text
+    assert text in str(k3.K3MoeError("mxfp4_linear", ERR_WORKSPACE))
