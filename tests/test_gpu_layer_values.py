@@ -1,5 +1,6 @@
 """moe_mxfp4_layer on values that its number formats have to cope with (a few
-channels of x far above the rest) and over workspaces of NaN.
+channels of x far above the rest, infinities, sums beyond fp32) and over
+workspaces of NaN.
 
 Bound for such x, with u = 2^-24 (half a step of fp32).  A 32-block of x enters
 as five base-32 digits, the first of step 2^s with max |x| < 2^(s + 4), so the
@@ -93,3 +94,24 @@ def test_sums_read_finished_rows_alone(k3, T, E, k, D, I):
     for i in range(24):
         work.fill_(255)
         assert torch.equal(k3.moe_mxfp4_layer(x, z, None, *dev, k, workspace=work)[0], want), i
+
+
+@pytest.mark.parametrize("what", ["inf", "-inf", "nan", "h overflows", "x at the largest bf16"])
+def test_values_beyond_fp32_stay_in_their_token(k3, what):
+    """NaN in every output of the token, as moe_mxfp4_ffn gives; the others keep their bits."""
+    g = torch.Generator().manual_seed(11)
+    T, E, k, D, I = 6, 4, 2, 96, 64
+    dev, _ = experts(k3, g, E, D, I, [])
+    x, z = torch.randn((T, D), generator=g).bfloat16(), torch.randn((T, E), generator=g).cuda()
+    want, ids, w = k3.moe_mxfp4_layer(x.cuda(), z, None, *dev, k)
+    if what == "h overflows":
+        x[2] *= 2.0**80  # g and u near 2^80, h near 2^160
+    elif what == "x at the largest bf16":
+        x[2, 40:44] = torch.finfo(torch.bfloat16).max
+    else:
+        x[2, 40] = float(what)
+    out = k3.moe_mxfp4_layer(x.cuda(), z, None, *dev, k)[0]
+    ffn = k3.moe_mxfp4_ffn(x.cuda(), ids, w, *dev)
+    others = [0, 1, 3, 4, 5]
+    assert bool(torch.isnan(out[2]).all()) and torch.equal(out[others], want[others])
+    assert torch.equal(torch.isnan(ffn), torch.isnan(out))
