@@ -34,10 +34,11 @@
 // ring of three LDS stages that runs on across units.
 //
 // Measured (graph replay; 16 experts a token, D = 3584, I = 3072): one token 64
-// us, 281 MB of weights (plan 4.8, first weights in LDS 6 to 8 us into the second
-// launch, the stream at 5.6 TB/s, sums 4); eight tokens 286 us, 1.58 GB, 5.5
-// TB/s; the two calls moe_route_topk and moe_mxfp4_ffn take 64 and 291 us there.
-// 13 tokens, 5 of 61 experts, D = 1056, I = 736: 36 us against 186; one token,
+// to 65 us, 281 MB of weights (plan 4.8, first weights in LDS 6 to 8 us into the
+// second launch, the stream at 5.6 TB/s, sums 4); eight tokens 286 to 292 us, 1.58
+// GB, 5.4-5.5 TB/s; the two calls moe_route_topk and moe_mxfp4_ffn take 64 to 72
+// and 290 to 297 us there.
+// 13 tokens, 5 of 61 experts, D = 1056, I = 736: 37 us against 186; one token,
 // 2 of 8 experts, D = 128, I = 256: 17 us against 22.  What bounds it: the bytes
 // with many tokens, plan, first loads and sums with one.
 //

@@ -12,13 +12,14 @@
 //   few rows (M <= 16): the weights are read once, straight from memory into
 //     the operand registers, with the rows of A (quantised on the way from
 //     float rows by the linear layer) in LDS; bound by the weight bytes (8 x
-//     33792 x 7168: 23.3 us, 5.5 TB/s; 1 x 3584 x 7168: 5.2 us, of which 3 are
+//     33792 x 7168: 24 us, 5.4 TB/s; 1 x 3584 x 7168: 5.8 us, of which 3 are
 //     the launch and the way of A through LDS);
 //   tiles: square output tiles, both operands staged through a ring of LDS
-//     buffers by direct global -> LDS loads; bound by the matrix cores for
-//     large products (4096 x 4096 x 7168: 68 us, 3.5 PFLOP/s, the matrix cores
-//     busy 0.54 of a CU's time) and by load latency for small ones (128 x 7168 x
-//     3584: 7.8-8.3 us).
+//     buffers by direct global -> LDS loads.  Large products are bound by loads
+//     and matrix instructions that overlap in part only (4096 x 4096 x 7168: 69
+//     to 71 us, 3.4 PFLOP/s; 55 without the loads, 46 without the matrix
+//     instructions; 4096 x 7168 x 7168: 114 us, the matrix cores busy 0.51 of the
+//     CUs' time), small ones by load latency (128 x 7168 x 3584: 7.8-8.3 us).
 #include "mx_common.h"
 #include "mx_shape.h"
 
