@@ -109,14 +109,15 @@ int mxfp4_linear(const void* x, int32_t x_dtype, const uint8_t* w_packed, const 
  *   workspace  moe_mxfp4_layer_workspace_size() bytes; contents on entry do
  *            not matter and are clobbered
  *
- * Precision: exact weights, fp32 accumulation. x and h = SiLU(g) * u (fp32)
- * enter the products in fixed point per 32-element block, to 2^-24 of the
- * block's largest magnitude (elements of x down to 2^-17 of it exactly; blocks
- * below 2^-104 to 2^-128). The k expert outputs are summed in fp32 in slot order (deterministic,
- * no atomics on values). moe_mxfp4_ffn rounds h to about 16 bits, so the two
- * agree to that. A token with an infinite or NaN element of x, or with an h
- * beyond fp32, gets NaN outputs, as from moe_mxfp4_ffn, and no other token does.
- * The weights' E8M0 bytes must be <= 254. More than 1024 experts take a third launch (the router's own).
+ * Precision: exact weights, fp32 accumulation. x and h = SiLU(g) * u (fp32) enter
+ * the products in fixed point per 32-element block, to 2^-24 of the block's
+ * largest magnitude (elements of x down to 2^-17 of it exactly; blocks below
+ * 2^-104 to 2^-128). The k expert outputs are summed in fp32 in slot order
+ * (deterministic, no atomics on values). moe_mxfp4_ffn rounds h to about 16 bits,
+ * so the two agree to that. A token with an infinite or NaN element of x, or with
+ * an h beyond fp32, gets NaN outputs, as from moe_mxfp4_ffn, and no other token
+ * does. The weights' E8M0 bytes must be <= 254. More than 1024 experts take a
+ * third launch (the router's own).
  * An expert's weights are streamed once per two of its tokens, so tokens that
  * mostly choose different experts gain; where many share one, moe_route_topk and
  * moe_mxfp4_ffn stream less.
