@@ -29,6 +29,13 @@ __all__ = [
     "mxfp4_matmul",
     "mxfp4_linear",
     "mxfp4_linear_workspace_size",
+    "mxfp8_quantize",
+    "mxfp8_unpack",
+    "mxfp8_rms_norm",
+    "mxfp8_matmul",
+    "moe_route_groups",
+    "moe_verify_draft",
+    "moe_verify_draft_workspace_size",
     "moe_mxfp4_layer",
     "moe_mxfp4_layer_workspace_size",
     "moe_mxfp4_ffn_workspace_size",
@@ -131,6 +138,20 @@ lib.moe_mxfp4_layer.restype = ctypes.c_int
 lib.moe_mxfp4_layer.argtypes = [_vp] * 6 + [_i64] + [_i32] * 5 + [_f32, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
 lib.mxfp4_linear.restype = ctypes.c_int
 lib.mxfp4_linear.argtypes = [_vp, _i32, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _sz, _vp]
+lib.mxfp8_quantize.restype = ctypes.c_int
+lib.mxfp8_quantize.argtypes = lib.mxfp4_quantize.argtypes
+lib.mxfp8_unpack.restype = ctypes.c_int
+lib.mxfp8_unpack.argtypes = lib.mxfp4_unpack.argtypes
+lib.mxfp8_rms_norm.restype = ctypes.c_int
+lib.mxfp8_rms_norm.argtypes = [_vp] * 3 + [_i32] * 2 + [_i64] * 2 + [ctypes.c_double, _i32] + [_vp] * 5
+lib.mxfp8_matmul.restype = ctypes.c_int
+lib.mxfp8_matmul.argtypes = lib.mxfp4_matmul.argtypes
+lib.moe_route_groups.restype = ctypes.c_int
+lib.moe_route_groups.argtypes = [_vp, _vp, _i64] + [_i32] * 7 + [_f32, _vp, _vp, _vp]
+lib.moe_verify_draft_workspace_size.restype = _sz
+lib.moe_verify_draft_workspace_size.argtypes = [_i64, _i32, _i32]
+lib.moe_verify_draft.restype = ctypes.c_int
+lib.moe_verify_draft.argtypes = [_vp, _i32] + [_vp] * 6 + [_i64] + [_i32] * 2 + [_vp] * 4 + [_sz, _vp]
 BLOCK_STAGE_EVENTS = 7
 # launches between consecutive events of moe_latent_block_profiled
 BLOCK_STAGES = ("dense1", "mid", "route", "ffn", "dense2", "sum")
@@ -409,6 +430,224 @@ def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
     _launch("mxfp4_linear", x.device, x.data_ptr(), _FLOAT_CODES[x.dtype], w_packed.data_ptr(), w_scale.data_ptr(), M, N, K,
             int(bool(saturate)), code, out.data_ptr(), _ptr(workspace), 0 if workspace is None else workspace.numel())
     return out
+
+
+def _mx8_pair(codes: torch.Tensor, scale: torch.Tensor, name: str, dims: int | None = None) -> int:
+    """Checks a microscaled 8-bit pair; returns K."""
+    _dev(codes, name, torch.uint8)
+    _dev(scale, name, torch.uint8)
+    cs = codes.shape
+    if not cs or (dims is not None and len(cs) != dims):
+        raise ValueError(f"{name}: codes must have {dims or 'at least 1'} dimensions")
+    K = cs[-1]
+    if scale.shape != (*cs[:-1], K // 32) or K % 32:
+        raise ValueError(f"{name}: scale must be [..., R, K/32] for codes [..., R, K]")
+    if scale.get_device() != codes.get_device():
+        raise ValueError(f"{name}: codes and scale are on different devices")
+    return K
+
+
+def mxfp8_quantize(x: torch.Tensor, saturate: bool = True, codes: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None):
+    """Float rows [..., R, K] (f32, bf16 or f16; K a multiple of 32) to
+    microscaled 8 bits: (codes u8 [..., R, K] of E4M3, scale u8 [..., R, K/32]),
+    what mxfp8_matmul reads. saturate=False takes the next larger scale where a
+    block's largest element would be clamped."""
+    _dev(x, "x", tuple(_FLOAT_CODES))
+    if x.dim() < 1:
+        raise ValueError("x must be [..., K]")
+    K = x.shape[-1]
+    if K % 32:
+        raise ValueError("K must be a multiple of 32")
+    given = codes is not None or scale is not None
+    if codes is None:
+        codes = x.new_empty(x.shape, dtype=torch.uint8)
+    if scale is None:
+        scale = x.new_empty((*x.shape[:-1], K // 32), dtype=torch.uint8)
+    if given:
+        if _mx8_pair(codes, scale, "output") != K or codes.shape != x.shape:
+            raise ValueError("codes must have x's shape")
+        _same_device(x, codes=codes)
+    R = x.numel() // K if K else 0
+    _launch("mxfp8_quantize", x.device, x.data_ptr(), _FLOAT_CODES[x.dtype], R, K, int(bool(saturate)), codes.data_ptr(),
+            scale.data_ptr())
+    return codes, scale
+
+
+def mxfp8_unpack(codes: torch.Tensor, scale: torch.Tensor, out_dtype: torch.dtype = torch.float32,
+                 out: torch.Tensor | None = None) -> torch.Tensor:
+    """Values [..., R, K] (f32 or bf16) of a microscaled 8-bit pair (codes u8
+    [..., R, K], scale u8 [..., R, K/32]); NaN where the scale byte is 255."""
+    K = _mx8_pair(codes, scale, "input")
+    code = _out_code(out_dtype)
+    if out is None:
+        out = codes.new_empty(codes.shape, dtype=out_dtype)
+    else:
+        _dev(out, "out", out_dtype)
+        if out.numel() != codes.numel():
+            raise ValueError("out has the wrong size")
+        _same_device(codes, out=out)
+    R = codes.numel() // K if K else 0
+    _launch("mxfp8_unpack", codes.device, codes.data_ptr(), scale.data_ptr(), R, K, code, out.data_ptr())
+    return out
+
+
+def mxfp8_rms_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                   eps: float = 1e-5, saturate: bool = True, normed: bool = False, total: torch.Tensor | None = None,
+                   y: torch.Tensor | None = None, codes: torch.Tensor | None = None,
+                   scale: torch.Tensor | None = None):
+    """v = x + residual, y = v / sqrt(mean(v^2) + eps) * gamma over the last
+    dimension, and y in microscaled 8 bits as mxfp8_quantize rounds it, from the
+    unrounded v and y.
+
+    x, residual [..., R, K] (f32, bf16 or f16), gamma [K] (any of these types, or
+    None for ones). Returns (codes, scale, total, y): total is v in x's type (None
+    without a residual, unless a buffer for it is given; it may be `residual` or
+    `x` itself, which is then updated), y the normed rows in x's type (None unless
+    `normed` or a buffer is given)."""
+    _dev(x, "x", tuple(_FLOAT_CODES))
+    if x.dim() < 1:
+        raise ValueError("x must be [..., K]")
+    K = x.shape[-1]
+    if K % 32:
+        raise ValueError("K must be a multiple of 32")
+    for name, t in (("residual", residual), ("total", total), ("y", y)):
+        if t is not None:
+            _dev(t, name, x.dtype)
+            if t.shape != x.shape:
+                raise ValueError(f"{name} must have x's shape")
+    if gamma is not None:
+        _dev(gamma, "gamma", tuple(_FLOAT_CODES))
+        if gamma.shape != (K,):
+            raise ValueError("gamma must be [K]")
+    if total is None and residual is not None:
+        total = torch.empty_like(x)
+    if y is None and normed:
+        y = torch.empty_like(x)
+    given = codes is not None or scale is not None
+    if codes is None:
+        codes = x.new_empty(x.shape, dtype=torch.uint8)
+    if scale is None:
+        scale = x.new_empty((*x.shape[:-1], K // 32), dtype=torch.uint8)
+    if given and (_mx8_pair(codes, scale, "output") != K or codes.shape != x.shape):
+        raise ValueError("codes must have x's shape")
+    _same_device(x, residual=residual, gamma=gamma, total=total, y=y, codes=codes)
+    R = x.numel() // K if K else 0
+    _launch("mxfp8_rms_norm", x.device, x.data_ptr(), _ptr(residual), _ptr(gamma), _FLOAT_CODES[x.dtype],
+            DTYPE_F32 if gamma is None else _FLOAT_CODES[gamma.dtype], R, K, float(eps), int(bool(saturate)), _ptr(total),
+            _ptr(y), codes.data_ptr(), scale.data_ptr())
+    return codes, scale, total, y
+
+
+def mxfp8_matmul(a_codes: torch.Tensor, a_scale: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
+                 out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rows A [M, K] in microscaled 8 bits times a microscaled 4-bit matrix W
+    [N, K] transposed: out [M, N] f32 or bf16, exact products summed in fp32."""
+    K = _mx8_pair(a_codes, a_scale, "A", 2)
+    if _mx_pair(w_packed, w_scale, "W", 2) != K:
+        raise ValueError("A and W have different K")
+    M, N = a_codes.shape[0], w_packed.shape[0]
+    code = _out_code(out_dtype)
+    if out is None:
+        out = a_codes.new_empty((M, N), dtype=out_dtype)
+    else:
+        _dev(out, "out", out_dtype)
+        if out.shape != (M, N):
+            raise ValueError("out must be [M, N]")
+    _same_device(a_codes, W=w_packed, out=out)
+    _launch("mxfp8_matmul", a_codes.device, a_codes.data_ptr(), a_scale.data_ptr(), w_packed.data_ptr(), w_scale.data_ptr(),
+            M, N, K, code, out.data_ptr())
+    return out
+
+
+SCORES = {"sigmoid": 0, "softmax": 1}
+
+
+def moe_route_groups(logits: torch.Tensor, bias: torch.Tensor | None, k: int, groups: int, topk_groups: int,
+                     group_top: int = 2, score: str = "sigmoid", normalize: bool = True, route_scale: float = 1.0,
+                     ids: torch.Tensor | None = None, weights: torch.Tensor | None = None):
+    """Top-k routing within the topk_groups best of `groups` equal runs of
+    experts, by sigmoid or softmax gates plus a bias. logits f32 [T, E], bias f32
+    [E] or None. Returns (ids int32 [T, k], weights f32 [T, k])."""
+    _dev(logits, "logits", torch.float32)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    if score not in SCORES:
+        raise ValueError("score must be 'sigmoid' or 'softmax'")
+    if bias is not None:
+        _dev(bias, "bias", torch.float32)
+        if bias.shape != (E,):
+            raise ValueError("bias must be [E]")
+    if ids is None:
+        ids = logits.new_empty((T, max(k, 0)), dtype=torch.int32)
+    if weights is None:
+        weights = logits.new_empty((T, max(k, 0)))
+    _dev(ids, "ids", torch.int32)
+    _dev(weights, "weights", torch.float32)
+    if ids.shape != (T, k) or weights.shape != (T, k):
+        raise ValueError("ids / weights must be [T, k]")
+    _same_device(logits, bias=bias, ids=ids, weights=weights)
+    _launch("moe_route_groups", logits.device, logits.data_ptr(), _ptr(bias), T, E, groups, topk_groups, group_top, k,
+            SCORES[score], int(bool(normalize)), float(route_scale), ids.data_ptr(), weights.data_ptr())
+    return ids, weights
+
+
+def moe_verify_draft_workspace_size(S: int, W: int, V: int) -> int:
+    return int(lib.moe_verify_draft_workspace_size(S, W, V))
+
+
+def moe_verify_draft(logits: torch.Tensor, draft_ids: torch.Tensor | None, u_accept: torch.Tensor | None,
+                     u_sample: torch.Tensor, draft_probs: torch.Tensor | None = None,
+                     draft_len: torch.Tensor | None = None, temperature: torch.Tensor | None = None,
+                     n_accepted: torch.Tensor | None = None, tokens: torch.Tensor | None = None,
+                     accept_prob: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Speculative verification of W - 1 proposals per sequence against the
+    target's logits [S, W, V] (f32, bf16 or f16), from given uniforms.
+
+    draft_ids i32 [S, W-1], u_accept f32 [S, W-1] (both may be None with W == 1),
+    u_sample f32 [S]; draft_probs f32 [S, W-1, V] (None: proposals of probability
+    1), draft_len i32 [S] (None: W - 1), temperature f32 [S] (None: 1; 0: greedy).
+    Returns (n_accepted i32 [S], tokens i32 [S, W]: the accepted proposals, the
+    next token, then -1, accept_prob f32 [S, W-1]: each proposal's probability of
+    being accepted)."""
+    _dev(logits, "logits", tuple(_FLOAT_CODES))
+    if logits.dim() != 3:
+        raise ValueError("logits must be [S, W, V]")
+    S, W, V = logits.shape
+    if W < 1:
+        raise ValueError("logits must have a row per sequence")
+    given = (("draft_ids", draft_ids, torch.int32, (S, W - 1)), ("u_accept", u_accept, torch.float32, (S, W - 1)),
+             ("u_sample", u_sample, torch.float32, (S,)), ("draft_probs", draft_probs, torch.float32, (S, W - 1, V)),
+             ("draft_len", draft_len, torch.int32, (S,)), ("temperature", temperature, torch.float32, (S,)),
+             ("n_accepted", n_accepted, torch.int32, (S,)), ("tokens", tokens, torch.int32, (S, W)),
+             ("accept_prob", accept_prob, torch.float32, (S, W - 1)))
+    index = logits.get_device()
+    for name, t, dtype, shape in given:
+        if t is None:
+            if name == "u_sample" or (W > 1 and name in ("draft_ids", "u_accept")):
+                raise ValueError(f"{name} is required")
+            continue
+        _dev(t, name, dtype)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+        if t.get_device() != index:
+            raise ValueError(f"{name}: must be on {logits.device}")
+    if n_accepted is None:
+        n_accepted = logits.new_empty((S,), dtype=torch.int32)
+    if tokens is None:
+        tokens = logits.new_empty((S, W), dtype=torch.int32)
+    if accept_prob is None:
+        accept_prob = logits.new_empty((S, W - 1), dtype=torch.float32)
+    if workspace is None:
+        workspace = logits.new_empty(moe_verify_draft_workspace_size(S, W, V), dtype=torch.uint8)
+    else:
+        _dev(workspace, "workspace", torch.uint8)
+        _same_device(logits, workspace=workspace)
+    _launch("moe_verify_draft", logits.device, logits.data_ptr(), _FLOAT_CODES[logits.dtype], _ptr(draft_ids),
+            _ptr(draft_probs), _ptr(draft_len), _ptr(temperature), _ptr(u_accept), u_sample.data_ptr(), S, W, V,
+            n_accepted.data_ptr(), tokens.data_ptr(), _ptr(accept_prob), workspace.data_ptr(), workspace.numel())
+    return n_accepted, tokens, accept_prob
 
 
 def moe_mxfp4_layer_workspace_size(T: int, D: int, I: int, E: int, k: int) -> int:

@@ -26,7 +26,8 @@ LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 INCLUDE = os.path.join(os.path.dirname(PKG_DIR), "include")
 
 SOURCES = ["abi.hip", "route.hip", "codec.hip", "group.hip", "ffn.hip", "ffn_big.hip", "ffn_stream.hip", "ffn_q4k.hip", "verify.hip", "cache.hip", "dense.hip",
-           "quant.hip", "mxprod.hip", "layer.hip"]
+           "quant.hip", "mxprod.hip", "layer.hip",
+           "mx8.hip", "mx8prod.hip", "route_groups.hip", "verify_draft.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

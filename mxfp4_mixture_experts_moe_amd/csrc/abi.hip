@@ -3,6 +3,7 @@
 #include "k3moe.h"
 #include "k3moe_internal.h"
 #include "k3moe_ops.h"
+#include "k3moe_serve.h"
 
 #include <math.h>
 #include <sys/syscall.h>
@@ -1087,6 +1088,102 @@ int moe_group_by_expert(const int32_t* topk_ids, int64_t T, int32_t E, int32_t k
   g.chunk_mask = reinterpret_cast<unsigned long long*>(ws + L.chunk_mask);
   g.x_perm = nullptr;
   return device_status(launch_group(g, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp8_quantize(const void* x, int32_t x_dtype, int64_t R, int64_t K, int32_t saturate, uint8_t* codes,
+                   uint8_t* scale, void* stream) {
+  if (!mx_rows_ok(R, K)) return K3MOE_ERR_SHAPE;
+  if (!mx_float_type(x_dtype)) return K3MOE_ERR_UNSUPPORTED;
+  if (R == 0) return K3MOE_OK;
+  if (!x || !codes || !scale) return K3MOE_ERR_NULL;
+  if (misaligned(x) || misaligned(codes) || misaligned(scale)) return K3MOE_ERR_ALIGN;
+  return device_status(launch_quantize8(x, x_dtype, R * K, saturate, codes, scale, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp8_unpack(const uint8_t* codes, const uint8_t* scale, int64_t R, int64_t K, int32_t out_dtype, void* out,
+                 void* stream) {
+  if (!mx_rows_ok(R, K)) return K3MOE_ERR_SHAPE;
+  if (out_dtype != K3MOE_DTYPE_F32 && out_dtype != K3MOE_DTYPE_BF16) return K3MOE_ERR_UNSUPPORTED;
+  if (R == 0) return K3MOE_OK;
+  if (!codes || !scale || !out) return K3MOE_ERR_NULL;
+  if (misaligned(codes) || misaligned(scale) || misaligned(out)) return K3MOE_ERR_ALIGN;
+  return device_status(launch_unpack8(codes, scale, R * K, out_dtype == K3MOE_DTYPE_BF16, out,
+                                      static_cast<hipStream_t>(stream)));
+}
+
+int mxfp8_rms_norm(const void* x, const void* residual, const void* gamma, int32_t x_dtype, int32_t gamma_dtype,
+                   int64_t R, int64_t K, double eps, int32_t saturate, void* sum, void* y, uint8_t* codes,
+                   uint8_t* scale, void* stream) {
+  if (!mx_rows_ok(R, K) || !(eps >= 0.0)) return K3MOE_ERR_SHAPE;
+  if (!mx_float_type(x_dtype) || !mx_float_type(gamma_dtype)) return K3MOE_ERR_UNSUPPORTED;
+  if (R == 0) return K3MOE_OK;
+  if (!x || !codes != !scale || (!codes && !y)) return K3MOE_ERR_NULL;
+  if (misaligned(x) || misaligned(residual) || misaligned(gamma) || misaligned(sum) || misaligned(y) ||
+      misaligned(codes) || misaligned(scale))
+    return K3MOE_ERR_ALIGN;
+  const NormCall c{x, residual, gamma, x_dtype, gamma_dtype, R, K, eps, saturate, sum, y, codes, scale};
+  return device_status(launch_norm8(c, static_cast<hipStream_t>(stream)));
+}
+
+int mxfp8_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const uint8_t* w_packed, const uint8_t* w_scale,
+                 int64_t M, int64_t N, int64_t K, int32_t out_dtype, void* out, void* stream) {
+  if (!mx_product_ok(M, N, K)) return K3MOE_ERR_SHAPE;
+  if (out_dtype != K3MOE_DTYPE_F32 && out_dtype != K3MOE_DTYPE_BF16) return K3MOE_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return K3MOE_OK;
+  if (!a_codes || !a_scale || !w_packed || !w_scale || !out) return K3MOE_ERR_NULL;
+  if (misaligned(a_codes) || misaligned(a_scale) || misaligned(w_packed) || misaligned(w_scale) || misaligned(out))
+    return K3MOE_ERR_ALIGN;
+  return device_status(launch_mx8_product(a_codes, a_scale, w_packed, w_scale, M, (int)N, (int)K,
+                                          out_dtype == K3MOE_DTYPE_BF16, out, static_cast<hipStream_t>(stream)));
+}
+
+int moe_route_groups(const float* logits, const float* bias, int64_t T, int32_t E, int32_t groups, int32_t topk_groups,
+                     int32_t group_top, int32_t k, int32_t score, int32_t normalize, float route_scale,
+                     int32_t* topk_ids, float* topk_w, void* stream) {
+  if (T < 0 || T > ((int64_t)1 << 40) || E < 1 || E > K3MOE_MAX_EXPERTS_FFN || groups < 1 || groups > E ||
+      E % groups != 0 || topk_groups < 1 || topk_groups > groups || k < 1 || k > K3MOE_MAX_TOPK ||
+      k > topk_groups * (E / groups))
+    return K3MOE_ERR_SHAPE;
+  if ((score != K3MOE_SCORE_SIGMOID && score != K3MOE_SCORE_SOFTMAX) || group_top < 1 || group_top > 2)
+    return K3MOE_ERR_UNSUPPORTED;
+  if (T == 0) return K3MOE_OK;
+  if (!logits || !topk_ids || !topk_w) return K3MOE_ERR_NULL;
+  if (misaligned(logits) || misaligned(bias) || misaligned(topk_ids) || misaligned(topk_w)) return K3MOE_ERR_ALIGN;
+  const RouteGroupsCall c{logits, bias, T, E, groups, topk_groups, group_top, k, score == K3MOE_SCORE_SOFTMAX, normalize, route_scale, topk_ids, topk_w};
+  return device_status(launch_route_groups(c, static_cast<hipStream_t>(stream)));
+}
+
+static bool verify_draft_ok(int64_t S, int32_t W, int32_t V) {
+  if (S < 0 || W < 1 || W > K3MOE_MAX_VERIFY_WIDTH || V < 1 || V > K3MOE_MAX_VOCAB) return false;
+  // workgroups of a launch (a grid dimension has fewer than 2^32 threads)
+  return S < (1 << 24) && S * W * ((V + kVocabChunk - 1) / kVocabChunk) < (1 << 24);
+}
+
+size_t moe_verify_draft_workspace_size(int64_t S, int32_t W, int32_t V) {
+  return S > 0 && verify_draft_ok(S, W, V) ? verify_draft_layout(S, W, V).total : 0;
+}
+
+int moe_verify_draft(const void* logits, int32_t dtype, const int32_t* draft_ids, const float* draft_probs,
+                     const int32_t* draft_len, const float* temperature, const float* u_accept, const float* u_sample,
+                     int64_t S, int32_t W, int32_t V, int32_t* n_accepted, int32_t* tokens, float* accept_prob,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  if (!verify_draft_ok(S, W, V)) return K3MOE_ERR_SHAPE;
+  if (!mx_float_type(dtype)) return K3MOE_ERR_UNSUPPORTED;
+  if (S == 0) return K3MOE_OK;
+  if (!logits || !u_sample || !n_accepted || !tokens || !workspace || (W > 1 && (!draft_ids || !u_accept)))
+    return K3MOE_ERR_NULL;
+  if (W == 1) {
+    draft_ids = nullptr;
+    draft_probs = u_accept = nullptr;
+    accept_prob = nullptr;
+  }
+  if (misaligned(logits) || misaligned(draft_ids) || misaligned(draft_probs) || misaligned(draft_len) ||
+      misaligned(temperature) || misaligned(u_accept) || misaligned(u_sample) || misaligned(n_accepted) ||
+      misaligned(tokens) || misaligned(accept_prob) || misaligned(workspace))
+    return K3MOE_ERR_ALIGN;
+  if (workspace_bytes < verify_draft_layout(S, W, V).total) return K3MOE_ERR_WORKSPACE;
+  const VerifyDraftCall c{logits, dtype, draft_ids, draft_probs, draft_len, temperature, u_accept, u_sample, S, W, V, n_accepted, tokens, accept_prob, workspace};
+  return device_status(launch_verify_draft(c, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

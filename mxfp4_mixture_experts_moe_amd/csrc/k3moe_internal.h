@@ -5,6 +5,7 @@
 
 #include "k3moe.h"
 #include "k3moe_ops.h"
+#include "k3moe_serve.h"
 #include <stddef.h>
 #include <stdint.h>
 
@@ -79,6 +80,25 @@ hipError_t launch_mx_few(const void* x, int x_dtype, const uint8_t* xs, const ui
                          int N, int K, int saturate, bool out_bf16, void* out, hipStream_t s);
 hipError_t launch_mx_product(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t M, int N,
                              int K, bool out_bf16, void* out, hipStream_t s);
+
+// Microscaled 8-bit rows: rounding and decode of n elements (n a multiple of
+// 32), the norm, and products with microscaled 4-bit weights.
+hipError_t launch_quantize8(const void* x, int x_dtype, int64_t n, int saturate, uint8_t* codes, uint8_t* scale,
+                            hipStream_t s);
+hipError_t launch_unpack8(const uint8_t* codes, const uint8_t* scale, int64_t n, int out_bf16, void* out,
+                          hipStream_t s);
+struct NormCall {
+  const void *x, *residual, *gamma;  // residual, gamma: may be null
+  int x_dtype, gamma_dtype;
+  int64_t R, K;
+  double eps;
+  int saturate;
+  void *sum, *y;  // may be null
+  uint8_t *codes, *scale;  // both or neither
+};
+hipError_t launch_norm8(const NormCall& c, hipStream_t s);
+hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t M,
+                              int N, int K, bool out_bf16, void* out, hipStream_t s);
 
 // Stage-tiled order of an MXFP4 matrix of N rows x nb 17-byte blocks (the
 // order mxfp4_tile writes and the FFN kernels read): rows in groups of 16 and
@@ -206,6 +226,41 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t s);
 // position <= w of S sequences of W rows (W <= kMaxVerifyWidth, E <= 8192).
 constexpr int kMaxVerifyWidth = 64;
 hipError_t launch_verify_distinct(const int32_t* ids, int S, int W, int E, int k, int32_t* distinct, hipStream_t s);
+
+// Routing within the best groups of experts.
+struct RouteGroupsCall {
+  const float *z, *bias;  // bias: may be null
+  int64_t T;
+  int E, groups, keep, group_top, k;
+  int softmax, normalize;
+  float route_scale;
+  int32_t* ids;
+  float* w;
+};
+hipError_t launch_route_groups(const RouteGroupsCall& c, hipStream_t s);
+
+// Verification of drafted tokens (workspace: verify_draft_layout).
+constexpr int kVocabChunk = 4096;  // vocabulary entries of a workgroup
+struct VerifyDraftLayout {
+  size_t stats, mass, done, total;
+  int chunks;
+};
+VerifyDraftLayout verify_draft_layout(int64_t S, int W, int V);
+struct VerifyDraftCall {
+  const void* logits;
+  int dtype;
+  const int32_t* draft;
+  const float* q;            // null: every proposal had probability 1
+  const int32_t* len;        // null: W - 1
+  const float* temperature;  // null: 1
+  const float *u_accept, *u_sample;
+  int64_t S;
+  int W, V;
+  int32_t *accepted, *tokens;
+  float* accept_prob;  // may be null
+  void* workspace;
+};
+hipError_t launch_verify_draft(const VerifyDraftCall& c, hipStream_t s);
 
 // Device expert cache (state layout inside the caller's buffer; the header
 // type is public, k3moe_expert_cache_header).

@@ -1,0 +1,631 @@
+// Products of microscaled 8-bit rows and microscaled 4-bit weights: C[m][n] =
+// sum_k A[m][k] * W[n][k], A in E4M3 codes, W in E2M1 codes, both with an E8M0
+// scale per 32 elements, on CDNA4's block-scaled matrix instructions.
+//
+// Exact sums.  The instruction adds the products of a block in a fixed-point
+// window: what lies more than 2^14 below the largest product is cut off
+// (measured), and E4M3 spans 2^-9 .. 448.  So every fragment of A goes in twice,
+// as
+//   its elements of magnitude >= 2 (code bit 6 set) and zeros:  products are
+//     multiples of 2^-3 up to 2688, 15 bits;
+//   the others (< 2) and zeros:  multiples of 2^-10 up to 11.25, 14 bits;
+// each of which the window holds whole, and only fp32 additions round.  The split
+// is five register operations per four codes (a byte mask out of the sign bits of
+// a shifted copy).  It makes the rate that of bf16 products, of which the
+// library's reach 1.2 to 1.4 PFLOP/s at 8192^3.
+//
+// Operands.  For K slots of 32 (a block each), the 4-bit operand's lane group g
+// holds block g, 16 bytes as they are stored; the 8-bit operand's holds 16 bytes
+// of two blocks: with G lane groups, registers 0-3 bytes 16 (g % 2) .. of block g
+// / 2, registers 4-7 the same of block G / 2 + g / 2, that is bytes 16 g and 16 G
+// + 16 g of the G blocks.  The scale of a lane group is block g's for both.
+//
+// Two kernels, as for the 4-bit products (mxprod.hip): few rows, bound by the
+// weight bytes, and square tiles through a ring of LDS buffers.
+#include "mx_common.h"
+#include "mx_shape.h"
+
+#include <type_traits>
+
+namespace k3moe {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kFp8 = 0, kFp4 = 4;  // operand types of the scaled matrix instructions: E4M3, E2M1
+
+__device__ __forceinline__ i32x8 operand4(mx_u32x4 q) {
+  return i32x8{(int)q[0], (int)q[1], (int)q[2], (int)q[3], 0, 0, 0, 0};
+}
+
+// The elements of magnitude >= 2 of a lane's 32 codes, and the others.
+struct Split {
+  i32x8 hi, lo;
+};
+__device__ __forceinline__ Split split8(mx_u32x4 p, mx_u32x4 q) {
+  Split s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = i < 4 ? p[i] : q[i - 4];
+    // bit 6 of bytes 1 and 3 at bits 15 and 31 of x << 1, that of bytes 0 and 2 there of x << 9;
+    // selectors 8 to 11 fill a byte with bit 15 or 31 of the second or the first operand
+    const uint32_t mask = __builtin_amdgcn_perm(x << 1, x << 9, 0x0B090A08u);
+    s.hi[i] = (int)(x & mask);
+    s.lo[i] = (int)(x & ~mask);
+  }
+  return s;
+}
+
+// Scale bytes i .. i+3 of a row's nb, those past the end 127 (the value 1).
+__device__ __forceinline__ uint32_t load_tail(const uint8_t* row, int i, int nb) {
+  uint32_t v = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t b = row[min(i + j, nb - 1)];
+    v |= (i + j < nb ? b : 127u) << (8 * j);
+  }
+  return v;
+}
+__device__ __forceinline__ uint32_t load_u32(const uint8_t* p) {  // any alignment
+  uint32_t v;
+  __builtin_memcpy(&v, p, 4);
+  return v;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void store_out(void* out, int64_t i, float v) {
+  if constexpr (kBf16)
+    static_cast<__bf16*>(out)[i] = (__bf16)v;
+  else
+    static_cast<float*>(out)[i] = v;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: as mx_few_kernel of mxprod.hip (16 weight rows a group, the waves of
+// a group split K in pieces of 512, pieces asked for two turns ahead across
+// rounds, partial sums through LDS), with the rows of A, 8 bits an element, in
+// LDS.  Rows that do not fit together go in chunks, side by side in the grid.
+constexpr int kFewWaves = 8;  // at most, per workgroup
+constexpr int kFewRows = 16;
+constexpr int kFewLds = 80 * 1024;     // two workgroups share a CU
+constexpr int kFewLdsAll = 156 * 1024;  // one has it to itself
+constexpr int kFewAhead = 2;            // pieces a wave asks for ahead
+
+struct FewArgs {
+  const uint8_t *a, *as, *w, *ws;
+  int64_t M;
+  int N, nb;       // nb = K / 32
+  int rows;        // of A per chunk
+  int kw, rw;      // waves per group, groups side by side
+  int per;         // pieces per wave and group
+  int arow, srow;  // LDS bytes per row of codes and of scales
+  void* out;
+};
+
+// kTail: K is no multiple of 512, so a row's last piece is shorter (and
+// scale rows are not 16-byte aligned).
+template <bool kBf16, bool kTail, int kLds>
+__global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_few_kernel(FewArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+  const int64_t m0 = (int64_t)blockIdx.y * a.rows;
+  const int M = (int)(a.M - m0 < a.rows ? a.M - m0 : a.rows);
+  uint8_t* const codes = lds;                // [M][arow]
+  uint8_t* const scales = lds + M * a.arow;  // [M][srow]
+  float* const red = reinterpret_cast<float*>(lds + ((M * (a.arow + a.srow) + 15) & ~15));  // [2][8 waves][256]
+  const int tid = threadIdx.x, lane = tid & 63, threads = 64 * a.kw * a.rw;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int rho = lane & 15, g = lane >> 4;
+  const int nb = a.nb, nss = (nb + 15) >> 4;
+
+  // this wave's turns: pieces s0, s0 + kw, ... of groups g0, g0 + step, ...
+  const int gw = __builtin_amdgcn_readfirstlane(wave / a.kw), s0 = wave - gw * a.kw;
+  const int ngroups = mx_groups(a.N, 16);
+  struct Piece {
+    mx_u32x4 q[4], sc;  // sc: 16 scale bytes; kTail: four dwords of one byte, this lane's blocks'
+  };
+  // Piece ss of group grp, without a branch (a wait for one piece must not become
+  // one for all); what lies outside the matrix is outside the buffer: zeros.
+  const uint32_t rowb = (uint32_t)nb * 16;
+  auto load = [&](int g_, int s_, Piece& d) __attribute__((always_inline)) {
+    const int grp = __builtin_amdgcn_readfirstlane(g_), ss = __builtin_amdgcn_readfirstlane(s_);
+    const int rows = __builtin_amdgcn_readfirstlane(grp < ngroups && ss < nss ? min(a.N - 16 * grp, 16) : 0);
+    const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc((void*)(a.w + (int64_t)grp * 16 * rowb), 0, rows * rowb, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc((void*)(a.ws + (int64_t)grp * 16 * nb), 0, rows * nb, 0x00020000);
+    const uint32_t b = (uint32_t)(16 * ss + g), row = (uint32_t)rho * nb;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t at = !kTail || b + 4 * i < (uint32_t)nb ? row + b + 4 * i : 0x0FFFFFFFu;
+      d.q[i] = __builtin_amdgcn_raw_buffer_load_b128(rw, 16 * at, 0, 0);
+      if constexpr (kTail) d.sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, at, 0, 0);
+    }
+    if constexpr (!kTail) d.sc = __builtin_amdgcn_raw_buffer_load_b128(rs, row + 16 * ss, 0, 0);
+  };
+  const int gstep = (int)gridDim.x * a.rw;
+  const int rounds = __builtin_amdgcn_readfirstlane(mx_few_rounds(a.N, a.rw, (int)gridDim.x));  // the same for every wave: the barriers below
+  int grp = (int)blockIdx.x * a.rw + gw, done = 0;  // done: turns of this round behind us
+  int lgrp = grp, ldone = 0;                        // the same of the next piece to ask for
+  Piece ring[kFewAhead];
+  auto ask = [&](Piece& d) __attribute__((always_inline)) {
+    load(lgrp, s0 + ldone * a.kw, d);
+    if (++ldone == a.per) ldone = 0, lgrp += gstep;
+  };
+  // A, in units of half a block, all rows' in order, kBatch a thread at a time.
+  // The first batch is asked for ahead of the weights (loads return in order).
+  constexpr int kBatch = 8;
+  const int units = M * nb * 2;
+  mx_u32x4 raw[kBatch];
+  uint32_t rsc[kBatch];
+  int at0 = 0;  // first unit of the batch
+  auto fetch = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int64_t u = m0 * nb * 2 + min(at0 + b * threads + tid, units - 1);
+      raw[b] = reinterpret_cast<const mx_u32x4*>(a.a)[u];
+      rsc[b] = a.as[u >> 1];
+    }
+  };
+  auto stage = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int u = at0 + b * threads + tid;
+      const int m = u / (2 * nb), r = u - m * 2 * nb;
+      if (u < units) {
+        *reinterpret_cast<mx_u32x4*>(codes + m * a.arow + 16 * r) = raw[b];
+        if ((r & 1) == 0) scales[m * a.srow + (r >> 1)] = (uint8_t)rsc[b];
+      }
+    }
+    at0 += kBatch * threads;
+  };
+  fetch();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kFewAhead; ++i) ask(ring[i]);
+  asm volatile("" ::: "memory");
+  stage();
+  while (at0 < units) {
+    fetch();
+    stage();
+  }
+  if ((nb & 15) != 0)  // scales past K, up to the piece's end
+    for (int i = tid; i < M * 16; i += threads)
+      if (nb + (i & 15) < 16 * nss) scales[(i >> 4) * a.srow + nb + (i & 15)] = 127;
+  __syncthreads();
+
+  const int mrow = min(rho, M - 1);  // columns past M repeat the last row and are never stored
+  const uint8_t* const brow = codes + mrow * a.arow;
+  const uint8_t* const bsc = scales + mrow * a.srow;
+  const int last = 32 * nb - 16;  // last half block of a row
+  // byte g of four dwords, as one
+  const uint32_t pick = 0x0c0c0400u + 0x0101u * (uint32_t)g;
+  auto bytes = [&](mx_u32x4 v) __attribute__((always_inline)) -> uint32_t {
+    return __builtin_amdgcn_perm(v[1], v[0], pick) | __builtin_amdgcn_perm(v[3], v[2], pick) << 16;
+  };
+  f32x4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = acc0;
+  int par = 0, rd = 0;
+  auto turn = [&](Piece& cur) __attribute__((always_inline)) {
+    const int ss = s0 + done * a.kw, sl = min(ss, nss - 1);
+    mx_u32x4 bs4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bs4[i] = *reinterpret_cast<const uint32_t*>(bsc + 16 * sl + 4 * i);
+    const uint32_t bs = bytes(bs4);
+    uint32_t sc;
+    if constexpr (kTail)
+      sc = (cur.sc[0] | cur.sc[1] << 8) | (cur.sc[2] | cur.sc[3] << 8) << 16;
+    else
+      sc = bytes(cur.sc);
+    // (past K the weights are zeros, and the last half block stands in for A's)
+    auto step = [&](auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
+      const int at = 512 * sl + 128 * i + 16 * g;
+      const Split b = split8(*reinterpret_cast<const mx_u32x4*>(brow + min(at, last)),
+                             *reinterpret_cast<const mx_u32x4*>(brow + min(at + 64, last)));
+      acc0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand4(cur.q[i]), b.hi, acc0, kFp4, kFp8, i, (int)sc, i, (int)bs);
+      acc1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand4(cur.q[i]), b.lo, acc1, kFp4, kFp8, i, (int)sc, i, (int)bs);
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+    ask(cur);
+    if (++done < a.per) return;
+    done = 0;
+    f32x4 sum = acc0 + acc1;
+    acc0 = acc1 = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (a.kw > 1) {
+      float* const slot = red + (par * kFewWaves + wave) * 256;
+      *reinterpret_cast<f32x4*>(slot + 4 * lane) = sum;
+      __syncthreads();
+      if (s0 == 0)
+        for (int i = 1; i < a.kw; ++i) sum += *reinterpret_cast<const f32x4*>(slot + 256 * i + 4 * lane);
+      par ^= 1;
+    }
+    if (s0 == 0 && grp < ngroups && rho < M) {
+      const int n = 16 * grp + 4 * g;
+      const int64_t at = (m0 + rho) * a.N + n;
+      if (n <= a.N - 4 && (a.N & 3) == 0) {
+        if constexpr (kBf16) {
+          typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<b4*>(static_cast<__bf16*>(a.out) + at) = b4{(__bf16)sum[0], (__bf16)sum[1], (__bf16)sum[2], (__bf16)sum[3]};
+        } else {
+          *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at) = sum;
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (n < a.N - v) store_out<kBf16>(a.out, at + v, sum[v]);
+      }
+    }
+    grp += gstep;
+    ++rd;
+  };
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < kFewAhead; ++i) {
+      turn(ring[i]);
+      if (rd >= rounds) return;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tiles.  A workgroup of kWm x kWn waves owns a B x B tile of C; K goes in steps
+// of 128 (four blocks: 128 bytes of a row of A, 64 of W) through a ring of LDS
+// buffers filled by direct global -> LDS loads.  Instruction kk (0, 1) of a step
+// takes its blocks 2 kk and 2 kk + 1.  The 16-byte chunks of an LDS row are
+// permuted by the row so that the lanes of a read touch every bank once.
+//   kStaged (K a multiple of 512): scales, 16 bytes (four steps) of every row, go
+//     through LDS, too, one load per wave and four steps;
+//   else each lane loads the four scale bytes of its rows for every step, which
+//     are not aligned.
+constexpr int kXcds = 8;
+
+struct TileArgs {
+  const uint8_t *a, *as, *w, *ws;
+  int M, N, nb;
+  void* out;
+};
+
+template <int N_>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N_ >= 0 && N_ < 64, "vmcnt is 6 bits");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N_) : "memory");
+}
+// Barrier of the ring: this wave's LDS reads are done (the buffer they read is
+// refilled after it) and its loads of the next step's buffer have landed.
+__device__ __forceinline__ void ring_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <int B, int kWm, int kWn, bool kStaged, bool kBf16>
+__global__ __launch_bounds__(kWm * kWn * 64) void mx8_tile_kernel(TileArgs t) {
+  constexpr int kWaves = kWm * kWn;
+  constexpr int kTm = B / (32 * kWm), kTn = B / (32 * kWn);  // 32-row operand tiles per wave
+  constexpr int kRing = B >= 256 ? 2 : 4;
+  constexpr int kADw = B * 32, kStageDw = B * 48;  // dwords of a step's rows of A; and of W behind them
+  constexpr int kLoadsA = B / (8 * kWaves), kLoadsW = B / (16 * kWaves), kLoads = kLoadsA + kLoadsW;  // 1 KB each, per wave and step
+  // one array per buffer, so that the compiler sees that a read of one buffer
+  // does not depend on the loads in flight into the others
+  __shared__ __attribute__((aligned(256))) uint32_t l0[kStageDw], l1[kStageDw], l2[kRing > 2 ? kStageDw : 1],
+      l3[kRing > 2 ? kStageDw : 1];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / kWn, wn = wave % kWn;
+  const int r32 = lane & 31, h = lane >> 5;
+
+  // Tile order: the ids an XCD gets (id % 8) are a contiguous run of the
+  // logical order, which walks groups of four tile rows column by column.
+  const int mt = mx_groups(t.M, B), nt = mx_groups(t.N, B);
+  const int64_t total = (int64_t)mt * nt;
+  int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  if (id >= total) return;
+  {
+    const int64_t q = total / kXcds, r = total % kXcds, x = id % kXcds, j = id / kXcds;
+    id = x * q + (x < r ? x : r) + j;
+  }
+  constexpr int kGm = 4;
+  const int64_t grp = id / ((int64_t)kGm * nt), in = id - grp * kGm * nt;
+  const int gm = mt - (int)grp * kGm < kGm ? mt - (int)grp * kGm : kGm;
+  const int64_t m0 = (grp * kGm + in % gm) * B;
+  const int n0 = (int)(in / gm) * B;
+
+  const int nb = t.nb;
+  const uint32_t arowb = (uint32_t)nb * 32, wrowb = (uint32_t)nb * 16;
+  const int mrows = t.M - m0 < B ? (int)(t.M - m0) : B;
+  const int nrows = t.N - n0 < B ? t.N - n0 : B;
+  const int nsteps = (nb + 3) >> 2;
+
+  // position of 16-byte chunk c in LDS row r
+  auto place_a = [](int c, int r) { return c ^ ((r >> 1) & 7); };
+  auto place_w = [](int c, int r) { return c ^ ((r >> 2) & 3); };
+  // loads: wave w fills LDS rows w * B / kWaves .. of A and of W
+  const int lrow0 = wave * (B / kWaves);
+  uint32_t aoff[kLoadsA], woff[kLoadsW];
+#pragma unroll
+  for (int j = 0; j < kLoadsA; ++j) {
+    const int r = lrow0 + 8 * j + lane / 8;
+    aoff[j] = (uint32_t)min(r, mrows - 1) * arowb + 16 * place_a(lane % 8, r);
+  }
+#pragma unroll
+  for (int j = 0; j < kLoadsW; ++j) {
+    const int r = lrow0 + 16 * j + lane / 4;
+    woff[j] = (uint32_t)min(r, nrows - 1) * wrowb + 16 * place_w(lane % 4, r);
+  }
+  // (steps past K are outside the buffers: zeros that cost no traffic)
+  auto issue = [&](int step, uint32_t* buf) {
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(t.a + m0 * arowb), 0, step < nsteps ? (int)(mrows * arowb) : 0, 0x00020000);
+    const __amdgpu_buffer_rsrc_t rw =
+        __builtin_amdgcn_make_buffer_rsrc((void*)(t.w + (int64_t)n0 * wrowb), 0, step < nsteps ? (int)(nrows * wrowb) : 0, 0x00020000);
+    uint32_t* const da = buf + lrow0 * 32;
+    uint32_t* const dw = buf + kADw + lrow0 * 16;
+    const int sa = 128 * step, sw = 64 * step;
+#pragma unroll
+    for (int j = 0; j < kLoadsA; ++j) {
+      const uint32_t vo = aoff[j];  // (an array element passed straight makes the host pass drop the kernel's launch stub)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, da + 256 * j, 16, vo, sa, 0, 0);
+    }
+#pragma unroll
+    for (int j = 0; j < kLoadsW; ++j) {
+      const uint32_t vo = woff[j];
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, dw + 256 * j, 16, vo, sw, 0, 0);
+    }
+  };
+
+  // scales of this lane's rows
+  const uint8_t* ap[kTm];
+  const uint8_t* wp[kTn];
+#pragma unroll
+  for (int i = 0; i < kTm; ++i) ap[i] = t.as + (m0 + min(wm * (B / kWm) + 32 * i + r32, mrows - 1)) * nb;
+#pragma unroll
+  for (int i = 0; i < kTn; ++i) wp[i] = t.ws + (int64_t)(n0 + min(wn * (B / kWn) + 32 * i + r32, nrows - 1)) * nb;
+  uint32_t sa[kTm], sw[kTn];  // !kStaged: of the next step
+  auto load_scales = [&](int step) {
+#pragma unroll
+    for (int i = 0; i < kTm; ++i) sa[i] = load_u32(ap[i] + 4 * step);
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) sw[i] = load_u32(wp[i] + 4 * step);
+  };
+  // kStaged: 16 bytes (four steps) of each of the tile's rows through LDS
+  constexpr int kScaleLoads = 2 * B / 64;  // of 64 rows; one per wave (some twice where there are more waves)
+  static_assert(kScaleLoads <= kWaves, "every wave does one load of scales");
+  __shared__ __attribute__((aligned(256))) uint32_t lsc[kStaged ? 2 * 2 * B * 4 : 1];
+  const int sload = wave % kScaleLoads;
+  const bool s_a = sload < kScaleLoads / 2;
+  const int slrows = s_a ? mrows : nrows;
+  const __amdgpu_buffer_rsrc_t rsc = __builtin_amdgcn_make_buffer_rsrc((void*)(s_a ? t.as + m0 * nb : t.ws + (int64_t)n0 * nb), 0, slrows * nb, 0x00020000);
+  const int svoff = min(sload % (kScaleLoads / 2) * 64 + lane, slrows - 1) * nb;
+  auto issue_scales = [&](int group) {
+    uint32_t* dst = lsc + (group & 1) * 2 * B * 4 + sload * 256;
+    const int so = 16 * min(group, (nb >> 4) - 1), vo = svoff;  // (past the last: that again, not used)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsc, dst, 16, vo, so, 0, 0);
+  };
+  mx_u32x4 ga[kTm], gw[kTn];
+  uint32_t ca[kTm], cw[kTn];  // bytes 0 and 2: of this lane half's blocks of both instructions of the step
+  auto own_bytes = [&](uint32_t v) { return h ? v >> 8 : v; };
+
+  f32x16 acc[kTm][kTn];
+#pragma unroll
+  for (int i = 0; i < kTm; ++i)
+#pragma unroll
+    for (int j = 0; j < kTn; ++j) acc[i][j] = f32x16{};
+
+  const uint32_t arow = (uint32_t)(wm * (B / kWm) + r32) * 128, wrow = (uint32_t)kADw * 4 + (uint32_t)(wn * (B / kWn) + r32) * 64;
+  // Instruction kk of a step held in `buf`; keep0, keep1: false zeroes its first
+  // or second block of A (blocks past K).
+  auto part = [&](const uint32_t* buf, auto kc, bool keep0, bool keep1) {
+    constexpr int kk = decltype(kc)::value;
+    const uint8_t* const l = reinterpret_cast<const uint8_t*>(buf);
+    mx_u32x4 fw[kTn];
+    Split fa[kTm];
+    const uint32_t p0 = 16u * (uint32_t)place_a(4 * kk + h, r32), p1 = 16u * (uint32_t)place_a(4 * kk + 2 + h, r32);
+    const uint32_t pw = 16u * (uint32_t)place_w(2 * kk + h, r32);
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) fw[i] = *reinterpret_cast<const mx_u32x4*>(l + wrow + 32 * 64 * i + pw);
+#pragma unroll
+    for (int i = 0; i < kTm; ++i) {
+      mx_u32x4 x0 = *reinterpret_cast<const mx_u32x4*>(l + arow + 32 * 128 * i + p0);
+      mx_u32x4 x1 = *reinterpret_cast<const mx_u32x4*>(l + arow + 32 * 128 * i + p1);
+      if (!keep0) x0 = mx_u32x4{0u, 0u, 0u, 0u};
+      if (!keep1) x1 = mx_u32x4{0u, 0u, 0u, 0u};
+      fa[i] = split8(x0, x1);
+    }
+#pragma unroll
+    for (int i = 0; i < kTm; ++i)
+#pragma unroll
+      for (int j = 0; j < kTn; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i].hi, operand4(fw[j]), acc[i][j], kFp8, kFp4, 2 * kk, (int)ca[i], 2 * kk, (int)cw[j]);
+#pragma unroll
+    for (int i = 0; i < kTm; ++i)
+#pragma unroll
+      for (int j = 0; j < kTn; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i].lo, operand4(fw[j]), acc[i][j], kFp8, kFp4, 2 * kk, (int)ca[i], 2 * kk, (int)cw[j]);
+  };
+  using C0 = std::integral_constant<int, 0>;
+  using C1 = std::integral_constant<int, 1>;
+  using C2 = std::integral_constant<int, 2>;
+  using C3 = std::integral_constant<int, 3>;
+
+  // Whole groups of four steps.  Every step issues the loads of kRing - 1 steps
+  // on, the first of a group (kStaged; else every one) the scales of the next
+  // but those, without a branch, so the number of loads in flight is the same
+  // everywhere: when a step starts, the loads after its own are those of kRing -
+  // 2 steps and up to one set of scales.
+  const int full = nb >> 4;
+  auto stage = [&](auto uc, int q, uint32_t* cur, uint32_t* refill) {
+    constexpr int u = decltype(uc)::value;  // the step in its group
+    if constexpr (kStaged)
+      wait_vm<(kRing - 2) * kLoads + (kRing > 2 && (u == 1 || u == 2) ? 1 : 0)>();
+    else
+      wait_vm<kRing == 2 ? 0 : 2 * kLoads + kTm + kTn>();
+    ring_barrier();
+    if constexpr (kStaged && u == 0) {
+      const uint32_t* const l = lsc + ((q >> 2) & 1) * 2 * B * 4;
+#pragma unroll
+      for (int i = 0; i < kTm; ++i) ga[i] = *reinterpret_cast<const mx_u32x4*>(l + 4 * (wm * (B / kWm) + 32 * i + r32));
+#pragma unroll
+      for (int i = 0; i < kTn; ++i) gw[i] = *reinterpret_cast<const mx_u32x4*>(l + 4 * (B + wn * (B / kWn) + 32 * i + r32));
+      asm volatile("" ::: "memory");
+      issue_scales((q >> 2) + 1);
+      asm volatile("" ::: "memory");
+    }
+    if constexpr (kStaged) {
+#pragma unroll
+      for (int i = 0; i < kTm; ++i) ca[i] = own_bytes(ga[i][u]);
+#pragma unroll
+      for (int i = 0; i < kTn; ++i) cw[i] = own_bytes(gw[i][u]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTm; ++i) ca[i] = own_bytes(sa[i]);
+#pragma unroll
+      for (int i = 0; i < kTn; ++i) cw[i] = own_bytes(sw[i]);
+      load_scales(min(q + 1, 4 * full - 1));
+      asm volatile("" ::: "memory");
+    }
+    issue(q + kRing - 1, refill);
+    asm volatile("" ::: "memory");  // the loads go out before the reads below
+    part(cur, C0{}, true, true);
+    part(cur, C1{}, true, true);
+  };
+  if constexpr (kStaged) issue_scales(0);
+  asm volatile("" ::: "memory");
+  if constexpr (kRing == 2) {
+    if (!kStaged && full > 0) load_scales(0);
+    asm volatile("" ::: "memory");
+    issue(0, l0);
+    for (int q = 0; q < 4 * full; q += 4) {
+      stage(C0{}, q, l0, l1);
+      stage(C1{}, q + 1, l1, l0);
+      stage(C2{}, q + 2, l0, l1);
+      stage(C3{}, q + 3, l1, l0);
+    }
+  } else {
+    issue(0, l0);
+    issue(1, l1);
+    if (!kStaged && full > 0) load_scales(0);
+    asm volatile("" ::: "memory");
+    issue(2, l2);
+    for (int q = 0; q < 4 * full; q += 4) {
+      stage(C0{}, q, l0, l3);
+      stage(C1{}, q + 1, l1, l0);
+      stage(C2{}, q + 2, l2, l1);
+      stage(C3{}, q + 3, l3, l2);
+    }
+  }
+
+  // The rest of K, up to four steps.
+  const int rest = kStaged ? 0 : nsteps - 4 * full;
+  for (int u = 0; u < rest; ++u) {
+    const int q = 4 * full + u, b0 = 4 * q;
+    wait_vm<0>();
+    ring_barrier();
+    auto pick = [&](int i) { return kRing == 2 ? (i & 1 ? l1 : l0) : (i & 3) == 0 ? l0 : (i & 3) == 1 ? l1 : (i & 3) == 2 ? l2 : l3; };
+    issue(q + kRing - 1, pick(u + kRing - 1));
+#pragma unroll
+    for (int i = 0; i < kTm; ++i) ca[i] = own_bytes(load_tail(ap[i], b0, nb));
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) cw[i] = own_bytes(load_tail(wp[i], b0, nb));
+    part(pick(u), C0{}, true, b0 + 1 < nb);
+    part(pick(u), C1{}, b0 + 2 < nb, b0 + 3 < nb);
+  }
+  wait_vm<0>();  // no load into LDS outlives the workgroup
+
+  // lane holds column n = lane % 32, rows 8 * (v / 4) + 4 * h + v % 4
+#pragma unroll
+  for (int i = 0; i < kTm; ++i)
+#pragma unroll
+    for (int j = 0; j < kTn; ++j) {
+      const int n = wn * (B / kWn) + 32 * j + r32;
+      if (n >= nrows) continue;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int m = wm * (B / kWm) + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
+        if (m < mrows) store_out<kBf16>(t.out, (m0 + m) * (int64_t)t.N + n0 + n, acc[i][j][v]);
+      }
+    }
+}
+
+// LDS bytes of the few-row kernel: rows of codes (an odd number of 16-byte
+// units, so 16 rows start in different banks), rows of scales, partial sums.
+int few_arow(int nb) { return 32 * nb + 16; }
+int few_srow(int nb) { return (nb + 15) / 16 * 16 + 4; }
+constexpr int kFewRed = 12 + 2 * kFewWaves * 256 * (int)sizeof(float);
+// Rows of A that fit `lds` bytes together, at most 16.
+int few_rows(int nb, int lds) {
+  const int r = (lds - kFewRed) / (few_arow(nb) + few_srow(nb));
+  return r < kFewRows ? r : kFewRows;
+}
+
+template <int B, int kWm, int kWn>
+hipError_t launch_square(const TileArgs& t, bool bf16, hipStream_t s) {
+  const MxTileGrid g = mx_tile_grid(t.M, t.N, B);
+  const dim3 grid(g.x, g.y), block(kWm * kWn * 64);
+  auto go = [&](auto st, auto b) {
+    hipLaunchKernelGGL((mx8_tile_kernel<B, kWm, kWn, decltype(st)::value, decltype(b)::value>), grid, block, 0, s, t);
+  };
+  const bool staged = t.nb % 16 == 0;
+  if (staged && bf16) go(std::true_type{}, std::true_type{});
+  else if (staged) go(std::true_type{}, std::false_type{});
+  else if (bf16) go(std::false_type{}, std::true_type{});
+  else go(std::false_type{}, std::false_type{});
+  return hipGetLastError();
+}
+
+hipError_t launch_few(FewArgs a, bool bf16, hipStream_t s) {
+  const int need = a.M < kFewRows ? (int)a.M : kFewRows;
+  // two workgroups per CU where all rows (of a chunk of 16) fit half of its LDS, else one
+  const bool half = few_rows(a.nb, kFewLds) >= need;
+  const int most = half ? kFewRows : few_rows(a.nb, kFewLdsAll);
+  const int64_t chunks = (a.M + most - 1) / most;
+  a.rows = (int)((a.M + chunks - 1) / chunks);
+  a.arow = few_arow(a.nb);
+  a.srow = few_srow(a.nb);
+  const int cus = device_cu_count();
+  const dim3 grid((unsigned)mx_few_grid(a.N, a.rw, half ? cus : (cus + 1) / 2).wgs, (unsigned)chunks), block((unsigned)(64 * a.kw * a.rw));
+  auto go = [&](auto b, auto t, auto l) {
+    hipLaunchKernelGGL((mx8_few_kernel<decltype(b)::value, decltype(t)::value, decltype(l)::value>), grid, block, 0, s, a);
+  };
+  using Half = std::integral_constant<int, kFewLds>;
+  using All = std::integral_constant<int, kFewLdsAll>;
+  const bool tail = a.nb % 16 != 0;
+  auto type = [&](auto t, auto l) {
+    if (bf16) go(std::true_type{}, t, l);
+    else go(std::false_type{}, t, l);
+  };
+  if (half && tail) type(std::true_type{}, Half{});
+  else if (half) type(std::false_type{}, Half{});
+  else if (tail) type(std::true_type{}, All{});
+  else type(std::false_type{}, All{});
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t M,
+                              int N, int K, bool out_bf16, void* out, hipStream_t s) {
+  const int nb = K / 32;
+  if (M <= kFewRows && few_rows(nb, kFewLdsAll) >= 1) {
+    FewArgs f{};
+    f.a = a;
+    f.as = as;
+    f.w = w;
+    f.ws = ws;
+    f.M = M;
+    f.N = N;
+    f.nb = nb;
+    const int nss = (nb + 15) / 16;
+    f.per = (nss + kFewWaves - 1) / kFewWaves;
+    f.kw = (nss + f.per - 1) / f.per;
+    f.rw = kFewWaves / f.kw;
+    f.out = out;
+    return launch_few(f, out_bf16, s);
+  }
+  const TileArgs t{a, as, w, ws, (int)M, N, nb, out};
+  const int64_t cus = device_cu_count();
+  auto tiles = [&](int B) { return mx_tile_grid(t.M, N, B).total; };
+  // the largest tile that gives every CU one and that either side more than half fills
+  const int64_t side = M < N ? M : N;
+  if (side > 128 && tiles(256) >= cus) return launch_square<256, 4, 2>(t, out_bf16, s);
+  if (side > 64 && tiles(128) >= cus) return launch_square<128, 4, 2>(t, out_bf16, s);
+  return launch_square<64, 2, 2>(t, out_bf16, s);
+}
+
+}  // namespace k3moe

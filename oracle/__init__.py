@@ -22,6 +22,9 @@ Modules
             experts, latent up, shared expert
 ``q4k``     Q4_K expert blocks (ggml's 4-bit k-quant): decode, and the routed FFN
             over Q4_K experts
+``mx4``, ``mx8``  microscaled 4- and 8-bit rounding and products; the norm in front of the latter
+``groups``  top-k routing within the best groups of experts
+``draft``   verification of drafted tokens against the target's distribution
 
 Parity status
 -------------
