@@ -6,17 +6,20 @@
 // order.  A sum over the vocabulary decides between neighbours that hold 1e-6 of
 // it, so an fp32 sum's order would move the token; everything here is fp64
 // from the logits on, and two runs (or another order of summation) differ only
-// where a uniform lies within about 1e-15 of a border.
+// where a uniform lies within about 1e-14 of a border.
 //
-// Two launches, both over chunks of 4096 vocabulary entries:
+// Two launches, over chunks of 4096 vocabulary entries:
 //   stats   every row's chunks: largest logit, its lowest index (greedy), sum of
 //           exponentials relative to the chunk's own largest;
-//   choose  per sequence, the chunks of the one row that is sampled from: the
-//           rows' totals out of the chunks' (each workgroup for itself, a few KB
-//           from the L2), which proposals are accepted, the chunk's share of max(p
-//           - q, 0); the workgroup that finishes last adds the shares up in
-//           order, finds the chunk that holds the token, and the token in it.
-// "Last" is a counter per sequence that the first launch clears; nothing waits.
+//   choose  out of the chunks' sums the rows', which proposals are accepted, and
+//           the next token: the chunk that holds it by a scan of the chunks'
+//           shares, then the entry by a scan of the chunk.  The shares of p are the
+//           first launch's sums, so without draft distributions one workgroup per
+//           sequence does (the proposal's own chunk is summed again without it);
+//           with them a workgroup per chunk sums its share of max(p - q, 0), after
+//           deciding the acceptances for itself (a few KB from the L2), and the one
+//           that finishes last goes on to the token.  "Last" is a counter per
+//           sequence that the first launch clears; nothing waits.
 #include "k3moe_internal.h"
 
 #include <math.h>
@@ -50,7 +53,11 @@ struct VerifyArgs {
   float* accept_prob;
 };
 
-// Logit i of a row.
+template <int kType>
+constexpr int kSize = kType == K3MOE_DTYPE_F32 ? 4 : 2;
+template <int kType>
+constexpr int kVec = 16 / kSize<kType>;  // logits of a 16-byte load
+
 template <int kType>
 __device__ __forceinline__ float logit(const uint8_t* row, int64_t i) {
   if constexpr (kType == K3MOE_DTYPE_F32) {
@@ -61,14 +68,66 @@ __device__ __forceinline__ float logit(const uint8_t* row, int64_t i) {
     return (float)reinterpret_cast<const _Float16*>(row)[i];
   }
 }
+// Logits v .. v + kVec - 1 of a row of V (rows start at any multiple of the
+// type's size); -inf past its end.
 template <int kType>
-constexpr int kSize = kType == K3MOE_DTYPE_F32 ? 4 : 2;
+__device__ __forceinline__ void logits16(const uint8_t* row, int v, int V, float* l) {
+  constexpr int n = kVec<kType>;
+  if (v + n <= V) {
+    uint32_t d[4];
+    __builtin_memcpy(d, row + (int64_t)v * kSize<kType>, 16);
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      if constexpr (kType == K3MOE_DTYPE_F32) {
+        l[i] = __uint_as_float(d[i]);
+      } else if constexpr (kType == K3MOE_DTYPE_BF16) {
+        l[i] = __uint_as_float(i & 1 ? d[i / 2] & 0xFFFF0000u : d[i / 2] << 16);
+      } else {
+        const uint16_t h = (uint16_t)(i & 1 ? d[i / 2] >> 16 : d[i / 2]);
+        l[i] = (float)__builtin_bit_cast(_Float16, h);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) l[i] = v + i < V ? logit<kType>(row, v + i) : -INFINITY;
+  }
+}
 
-// exp((l - m) / T) for l <= m; 0 for NaN and -inf; an infinite m is shared by those that reach it.
-__device__ __forceinline__ double weight(float l, float m, double inv_t) {
-  if (!(l > -INFINITY)) return 0.0;
-  if (l == m) return 1.0;
-  return m == INFINITY ? 0.0 : exp(((double)l - (double)m) * inv_t);
+// exp(d) for d <= 0: 2^n e^r with n = rint(d / ln 2), |r| <=
+// ln(2) / 2, and the power series of e^r to r^11 (what is left of it is below
+// r^12 / 12! = 7e-15).  NaN and everything below -800 give 0.
+__device__ __forceinline__ double exp_down(double d) {
+  d = fmax(d, -800.0);
+  constexpr double kShift = 6755399441055744.0;  // 1.5 * 2^52: an integer's bits end up in the lowest of the sum
+  const double t = fma(d, 1.4426950408889634, kShift);
+  const double n = t - kShift;
+  double r = fma(n, -6.93147180369123816490e-01, d);  // ln 2 in two parts, the first of 32 bits
+  r = fma(n, -1.90821492927058770002e-10, r);
+  double p = 1.0 / 39916800.0;
+  p = fma(p, r, 1.0 / 3628800.0);
+  p = fma(p, r, 1.0 / 362880.0);
+  p = fma(p, r, 1.0 / 40320.0);
+  p = fma(p, r, 1.0 / 5040.0);
+  p = fma(p, r, 1.0 / 720.0);
+  p = fma(p, r, 1.0 / 120.0);
+  p = fma(p, r, 1.0 / 24.0);
+  p = fma(p, r, 1.0 / 6.0);
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return ldexp(p, (int)(uint32_t)(uint64_t)__double_as_longlong(t));
+}
+
+// exp((l - m) / T) for logits l <= m of a row or chunk whose largest is m: 0 for
+// NaN and -inf.
+struct Scale {
+  double inv_t, m;
+  bool infinite;  // m is +inf (shared by the logits that reach it) or -inf (no logit is above it)
+};
+__device__ __forceinline__ Scale scale_of(float m, double inv_t) { return Scale{inv_t, (double)m, fabsf(m) == INFINITY}; }
+__device__ __forceinline__ double weight(float l, const Scale& s) {
+  if (s.infinite) return l == INFINITY ? 1.0 : 0.0;
+  return exp_down(((double)fmaxf(l, -INFINITY) - s.m) * s.inv_t);  // (fmaxf: NaN as -inf; the difference first: a low temperature leaves nothing of 1 / T's last bits)
 }
 
 __device__ __forceinline__ float wave_max(float v) {
@@ -86,62 +145,65 @@ __device__ __forceinline__ int wave_min(int v) {
   for (int d = 1; d < 64; d <<= 1) v = min(v, __shfl_xor(v, d, 64));
   return v;
 }
+// Sum over the lanes up to this one.
+__device__ __forceinline__ double wave_scan(double v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const double o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
 
 __device__ __forceinline__ float temperature_of(const VerifyArgs& a, int64_t s) { return a.temperature ? a.temperature[s] : 1.0f; }
 
 template <int kType>
 __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a) {
-  __shared__ float wm[kWaves];
-  __shared__ double wz[kWaves];
-  __shared__ int wi[kWaves];
+  __shared__ ChunkStat part[kWaves];
   const int64_t r = blockIdx.x / (unsigned)a.chunks;
   const int c = (int)(blockIdx.x - r * a.chunks);
   const int64_t s = r / a.W;
   const int wave = threadIdx.x >> 6;
   if (c == 0 && r == s * a.W && threadIdx.x == 0) a.done[s] = 0u;
   const uint8_t* const row = a.logits + r * a.V * kSize<kType>;
-  const int v0 = c * kVocabChunk;
+  constexpr int n = kVec<kType>;
+  const int v0 = c * kVocabChunk + (int)threadIdx.x * n;
   float l[kEach];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int v = v0 + i * kThreads + (int)threadIdx.x;
-    l[i] = v < a.V ? logit<kType>(row, v) : -INFINITY;
-  }
+  for (int i = 0; i < kEach; i += n) logits16<kType>(row, v0 + i * kThreads, a.V, l + i);
+  const float t = temperature_of(a, s);
+  const bool greedy = !(t > 0.0f);
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) m = fmaxf(m, l[i]);  // (passes over NaN)
   m = wave_max(m);
-  if ((threadIdx.x & 63) == 0) wm[wave] = m;
-  __syncthreads();
-  m = wm[0];
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i) m = fmaxf(m, wm[i]);
-  const float t = temperature_of(a, s);
-  const bool greedy = !(t > 0.0f);
   double z = 0.0;
   int at = INT_MAX;
   if (greedy) {
 #pragma unroll
     for (int i = kEach - 1; i >= 0; --i)
-      if (l[i] == m && m > -INFINITY) at = v0 + i * kThreads + (int)threadIdx.x;
+      if (l[i] == m && m > -INFINITY) at = v0 + i / n * n * kThreads + i % n;
     at = wave_min(at);
   } else {
-    const double inv_t = 1.0 / (double)t;
+    const Scale sc = scale_of(m, 1.0 / (double)t);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) z += weight(l[i], m, inv_t);
+    for (int i = 0; i < kEach; ++i) z += weight(l[i], sc);
     z = wave_sum(z);
   }
-  if ((threadIdx.x & 63) == 0) {
-    wz[wave] = z;
-    wi[wave] = at;
-  }
+  if ((threadIdx.x & 63) == 0) part[wave] = ChunkStat{m, at, z};
   __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kWaves; ++i) {
-      z += wz[i];
-      at = min(at, wi[i]);
+  if (threadIdx.x < 64) {  // the waves' together, each at its own largest so far
+    const int lane = threadIdx.x;
+    const ChunkStat x = part[lane < kWaves ? lane : 0];
+    m = wave_max(x.m);
+    z = lane < kWaves && !greedy ? x.z * weight(x.m, scale_of(m, 1.0 / (double)t)) : 0.0;
+    at = greedy && x.m == m ? x.at : INT_MAX;
+#pragma unroll
+    for (int d = 1; d < kWaves; d <<= 1) {
+      z += __shfl_xor(z, d, 64);
+      at = min(at, __shfl_xor(at, d, 64));
     }
-    a.stats[r * a.chunks + c] = ChunkStat{m, at, z};
+    if (lane == 0) a.stats[r * a.chunks + c] = ChunkStat{m, at, z};
   }
 }
 
@@ -152,171 +214,230 @@ struct RowStat {
   double z;
 };
 __device__ __forceinline__ RowStat row_stat(const ChunkStat* st, int chunks, int lane, double inv_t, bool greedy) {
-  float m = -INFINITY;
-  for (int c = lane; c < chunks; c += 64) m = fmaxf(m, st[c].m);
+  const ChunkStat own = lane < chunks ? st[lane] : ChunkStat{-INFINITY, INT_MAX, 0.0};
+  float m = own.m;
+  for (int c = lane + 64; c < chunks; c += 64) m = fmaxf(m, st[c].m);
   m = wave_max(m);
-  double z = 0.0;
-  int at = INT_MAX;
-  for (int c = lane; c < chunks; c += 64) {
+  const Scale sc = scale_of(m, inv_t);
+  auto take = [&](const ChunkStat& x) { return greedy ? 0.0 : x.z * weight(x.m, sc); };
+  double z = take(own);
+  int at = greedy && own.m == m ? own.at : INT_MAX;
+  for (int c = lane + 64; c < chunks; c += 64) {
     const ChunkStat x = st[c];
-    if (greedy) {
-      if (x.m == m) at = min(at, x.at);
-    } else {
-      z += x.z * weight(x.m, m, inv_t);
-    }
+    z += take(x);
+    if (greedy && x.m == m) at = min(at, x.at);
   }
-  return RowStat{m, wave_min(at), wave_sum(z)};
+  return RowStat{m, greedy ? wave_min(at) : INT_MAX, greedy ? 0.0 : wave_sum(z)};
 }
 
 // What is sampled from, entry v of a row: max(p - q, 0) or p.
 struct Source {
-  float m;
-  double inv_t, inv_z;
+  Scale sc;
+  double inv_z;
   const float* q;  // null: q is 1 at x
-  int x;           // -1: p itself
+  int x;           // the proposal, -1: none
   bool residual;
 };
-__device__ __forceinline__ double entry(const Source& d, float l, int v) {
-  const double p = weight(l, d.m, d.inv_t) * d.inv_z;
+__device__ __forceinline__ double entry(const Source& d, float l, int v, float q) {
+  const double p = weight(l, d.sc) * d.inv_z;
   if (!d.residual) return p;
-  return fmax(p - (d.q ? (double)d.q[v] : v == d.x ? 1.0 : 0.0), 0.0);
+  return fmax(p - (d.q ? (double)q : v == d.x ? 1.0 : 0.0), 0.0);
+}
+// Entries v .. v + kVec - 1 (0 past the row's end).
+template <int kType>
+__device__ __forceinline__ void entries16(const Source& d, const uint8_t* row, int v, int V, double* e) {
+  constexpr int n = kVec<kType>;
+  float l[n], q[n];
+  logits16<kType>(row, v, V, l);
+  if (d.residual && d.q) {
+#pragma unroll
+    for (int i = 0; i < n; i += 4) logits16<K3MOE_DTYPE_F32>(reinterpret_cast<const uint8_t*>(d.q), v + i, V, q + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < n; ++i) q[i] = 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < n; ++i) e[i] = v + i < V ? entry(d, l[i], v + i, q[i]) : 0.0;
+}
+// This thread's part of a chunk's share.
+template <int kType>
+__device__ __forceinline__ double chunk_part(const Source& d, const uint8_t* row, int c, int V) {
+  constexpr int n = kVec<kType>;
+  double sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < kEach; i += n) {
+    double e[n];
+    entries16<kType>(d, row, c * kVocabChunk + (i * kThreads + (int)threadIdx.x * n), V, e);
+#pragma unroll
+    for (int j = 0; j < n; ++j) sum += e[j];
+  }
+  return sum;
+}
+// The sum over the workgroup, in thread 0.
+__device__ __forceinline__ double block_sum(double v, double (&part)[kWaves]) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+  __syncthreads();
+  if (threadIdx.x == 0)
+    for (int i = 1; i < kWaves; ++i) v += part[i];
+  return v;
 }
 
-template <int kType>
+template <int kType, bool kProbs>
 __global__ __launch_bounds__(kThreads) void choose_kernel(VerifyArgs a) {
   __shared__ RowStat rows[kMaxVerifyWidth];
-  __shared__ double wz[kWaves];
-  __shared__ double scan[kThreads];
-  __shared__ int sh_count, sh_last, sh_found;
-  __shared__ double sh_before;
-  const int64_t s = blockIdx.x / (unsigned)a.chunks;
-  const int c = (int)(blockIdx.x - s * a.chunks);
+  __shared__ double part[kWaves], own_mass, sh_target, sh_before;
+  __shared__ int sh_count, sh_last, sh_found, sh_residual, wat[kWaves], wlast[kWaves];
+  const int64_t s = kProbs ? blockIdx.x / (unsigned)a.chunks : blockIdx.x;
+  const int c = kProbs ? (int)(blockIdx.x - s * a.chunks) : 0;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int W = a.W, V = a.V, D = W - 1;
   const float t = temperature_of(a, s);
   const bool greedy = !(t > 0.0f);
   const double inv_t = greedy ? 1.0 : 1.0 / (double)t;
+  // the proposals, one lane each: what their test reads, asked for ahead of the sums
+  int x = -1;
+  float xl = -INFINITY, xq = 1.0f, xu = 0.0f;
+  if (wave == 0 && lane < D) {
+    x = a.draft[s * D + lane];
+    xu = a.u_accept[s * D + lane];
+    if (x >= 0 && x < V) {
+      xl = logit<kType>(a.logits + (s * W + lane) * V * kSize<kType>, x);
+      if constexpr (kProbs) xq = a.q[(s * D + lane) * V + x];
+    }
+  }
   int n = a.len ? a.len[s] : D;
   n = n < 0 ? 0 : n > D ? D : n;
-  for (int w = wave; w <= n; w += kWaves) {
+  for (int w = wave; w < W; w += kWaves) {
     const RowStat st = row_stat(a.stats + (s * W + w) * a.chunks, a.chunks, lane, inv_t, greedy);
     if (lane == 0) rows[w] = st;
   }
   __syncthreads();
-  // the proposals, one lane each
   if (wave == 0) {
     bool take = false;
-    if (lane < D) {
-      const int x = a.draft[s * D + lane];
-      double chance = 0.0;
-      if (lane < n && x >= 0 && x < V) {
-        const RowStat st = rows[lane];
-        if (greedy) {
-          take = x == st.at;
-          chance = take ? 1.0 : 0.0;
-        } else if (st.z > 0.0) {
-          const double p = weight(logit<kType>(a.logits + (s * W + lane) * V * kSize<kType>, x), st.m, inv_t) / st.z;
-          const double q = a.q ? (double)a.q[(s * D + lane) * V + x] : 1.0;
-          take = (double)a.u_accept[s * D + lane] * q < p;
-          chance = q < p ? 1.0 : q > 0.0 ? p / q : 0.0;
-        }
+    double chance = 0.0;
+    if (lane < n && x >= 0 && x < V) {
+      const RowStat st = rows[lane];
+      if (greedy) {
+        take = x == st.at;
+        chance = take ? 1.0 : 0.0;
+      } else if (st.z > 0.0) {
+        const double p = weight(xl, scale_of(st.m, inv_t)) / st.z, q = (double)xq;
+        take = (double)xu * q < p;
+        chance = q < p ? 1.0 : q > 0.0 ? p / q : 0.0;
       }
-      if (c == 0 && a.accept_prob) a.accept_prob[s * D + lane] = (float)chance;
     }
     const uint64_t no = ~__builtin_amdgcn_ballot_w64(take);
     const int count = no ? __builtin_ctzll(no) : 64;  // (D <= 63)
     if (lane == 0) sh_count = count;
     if (c == 0) {
+      if (lane < D && a.accept_prob) a.accept_prob[s * D + lane] = (float)chance;
       if (lane == 0) a.accepted[s] = count;
-      if (lane < W && lane != count) a.tokens[s * W + lane] = lane < count ? a.draft[s * D + lane] : -1;
+      if (lane < W && lane != count) a.tokens[s * W + lane] = lane < count ? x : -1;
     }
   }
   __syncthreads();
   const int count = sh_count;
   const RowStat st = rows[count];
+  int32_t* const token = a.tokens + s * W + count;
   if (greedy) {
-    if (c == 0 && threadIdx.x == 0) a.tokens[s * W + count] = st.at == INT_MAX ? -1 : st.at;
+    if (c == 0 && threadIdx.x == 0) *token = st.at == INT_MAX ? -1 : st.at;
     return;
   }
 
   const uint8_t* const row = a.logits + (s * W + count) * V * kSize<kType>;
-  Source d{st.m, inv_t, st.z > 0.0 ? 1.0 / st.z : 0.0, nullptr, -1, count < n};
+  Source d{scale_of(st.m, inv_t), st.z > 0.0 ? 1.0 / st.z : 0.0, nullptr, -1, count < n};
   if (d.residual) {
     d.x = a.draft[s * D + count];
-    d.q = a.q ? a.q + (s * D + count) * V : nullptr;
+    if constexpr (kProbs) d.q = a.q + (s * D + count) * V;
   }
-  const int v0 = c * kVocabChunk;
-  double mass = 0.0;
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int v = v0 + i * kThreads + (int)threadIdx.x;
-    if (v < V) mass += entry(d, logit<kType>(row, v), v);
-  }
-  mass = wave_sum(mass);
-  if (lane == 0) wz[wave] = mass;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kWaves; ++i) mass += wz[i];
-    __hip_atomic_store(a.mass + s * a.chunks + c, mass, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    sh_last = __hip_atomic_fetch_add(a.done + s, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)a.chunks - 1u;
-  }
-  __syncthreads();
-  if (!sh_last) return;
-
-  // The last workgroup of the sequence: the chunk, then the entry.
-  const double u = (double)a.u_sample[s];
-  const ChunkStat* const cs = a.stats + (s * W + count) * a.chunks;
-  if (threadIdx.x == 0) {
-    auto load = [&](int i) { return __hip_atomic_load(a.mass + s * a.chunks + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-    auto share = [&](int i) { return d.residual ? load(i) : cs[i].z * weight(cs[i].m, d.m, inv_t) * d.inv_z; };
-    double total = 0.0;
-    for (int i = 0; i < a.chunks; ++i) total += share(i);
-    if (d.residual && !(total > 0.0)) {  // p nowhere above q: p itself
-      d.residual = false;
-      total = 0.0;
-      for (int i = 0; i < a.chunks; ++i) total += share(i);
-    }
-    sh_count = d.residual;
-    // the first chunk whose cumulative sum exceeds the target; past the end (a uniform of 1), the last that holds anything
-    double sum = 0.0, before = 0.0;
-    int found = -1;
-    for (int i = 0; i < a.chunks; ++i) {
-      const double x = share(i);
-      if (x > 0.0) {
-        found = i;
-        before = sum;
-        if (sum + x > u * total) break;
+  const bool inside = d.x >= 0 && d.x < V;
+  const int own = !kProbs && d.residual && inside ? d.x / kVocabChunk : -1;  // the chunk whose share of max(p - q, 0) is not that of p
+  if constexpr (kProbs) {
+    if (d.residual) {  // (else p's shares are there)
+      const double mass = block_sum(chunk_part<kType>(d, row, c, V), part);
+      if (threadIdx.x == 0) {
+        __hip_atomic_store(a.mass + s * a.chunks + c, mass, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        sh_last = __hip_atomic_fetch_add(a.done + s, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)a.chunks - 1u;
       }
-      sum += x;
+      __syncthreads();
+      if (!sh_last) return;
+    } else if (c != 0) {
+      return;
     }
-    sh_found = found;
-    sh_before = before;
-    wz[0] = u * total;
+  } else if (own >= 0) {
+    const double mass = block_sum(chunk_part<kType>(d, row, own, V), part);
+    if (threadIdx.x == 0) own_mass = mass;
   }
   __syncthreads();
-  d.residual = sh_count != 0;
+
+  // The chunk: the first whose cumulative sum exceeds the target; past the end (a
+  // uniform of 1), the last that holds anything.
+  if (wave == 0) {
+    const double u = (double)a.u_sample[s];
+    const ChunkStat* const cs = a.stats + (s * W + count) * a.chunks;
+    bool residual = d.residual;
+    auto share = [&](int i) -> double {
+      if (i >= a.chunks) return 0.0;
+      if (kProbs && residual) return __hip_atomic_load(a.mass + s * a.chunks + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (residual && i == own) return own_mass;
+      return cs[i].z * weight(cs[i].m, d.sc) * d.inv_z;
+    };
+    auto total_of = [&]() {
+      double v = 0.0;
+      for (int i = lane; i < a.chunks; i += 64) v += share(i);
+      return wave_sum(v);
+    };
+    double total = total_of();
+    if (residual && !(total > 0.0)) {  // p nowhere above q: p itself
+      residual = false;
+      total = total_of();
+    }
+    const double target = u * total;
+    int found = -1;
+    double base = 0.0, before = 0.0;
+    for (int i0 = 0; i0 < a.chunks; i0 += 64) {
+      const double v = share(i0 + lane);
+      const double incl = base + wave_scan(v, lane);
+      const double prev = __shfl_up(incl, 1, 64), excl = lane ? prev : base;
+      const uint64_t any = __builtin_amdgcn_ballot_w64(v > 0.0), over = __builtin_amdgcn_ballot_w64(v > 0.0 && incl > target);
+      if (any) {
+        const int at = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(any);
+        found = i0 + at;
+        before = __shfl(excl, at, 64);
+      }
+      if (over) break;
+      base = __shfl(incl, 63, 64);
+    }
+    if (lane == 0) {
+      sh_found = found;
+      sh_before = before;
+      sh_target = target;
+      sh_residual = residual;
+    }
+  }
+  __syncthreads();
   const int f = sh_found;
   if (f < 0) {
-    if (threadIdx.x == 0) a.tokens[s * W + count] = -1;
+    if (threadIdx.x == 0) *token = -1;
     return;
   }
-  const double target = wz[0];
+  // The entry: sixteen in a row per thread.
+  d.residual = sh_residual != 0;
+  const double target = sh_target;
   const int b0 = f * kVocabChunk + (int)threadIdx.x * kEach;
-  double e[kEach], own = 0.0;
+  double e[kEach], mine = 0.0;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    e[i] = b0 + i < V ? entry(d, logit<kType>(row, b0 + i), b0 + i) : 0.0;
-    own += e[i];
-  }
-  scan[threadIdx.x] = own;
+  for (int i = 0; i < kEach; i += kVec<kType>) entries16<kType>(d, row, b0 + i, V, e + i);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) mine += e[i];
+  const double incl = wave_scan(mine, lane);
+  if (lane == 63) part[wave] = incl;
   __syncthreads();
-  for (int step = 1; step < kThreads; step <<= 1) {
-    const double o = (int)threadIdx.x >= step ? scan[threadIdx.x - step] : 0.0;
-    __syncthreads();
-    scan[threadIdx.x] += o;
-    __syncthreads();
-  }
-  double sum = sh_before + (threadIdx.x ? scan[threadIdx.x - 1] : 0.0);
+  double sum = sh_before;
+  for (int i = 0; i < wave; ++i) sum += part[i];
+  const double prev = __shfl_up(incl, 1, 64);
+  sum += lane ? prev : 0.0;
   int at = INT_MAX, last = -1;  // first entry over the target; last one that holds anything
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
@@ -328,7 +449,6 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(VerifyArgs a) {
   }
   at = wave_min(at);
   last = -wave_min(-last);
-  __shared__ int wat[kWaves], wlast[kWaves];
   if (lane == 0) {
     wat[wave] = at;
     wlast[wave] = last;
@@ -339,7 +459,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(VerifyArgs a) {
       at = min(at, wat[i]);
       last = max(last, wlast[i]);
     }
-    a.tokens[s * W + count] = at != INT_MAX ? at : last;
+    *token = at != INT_MAX ? at : last;
   }
 }
 
@@ -378,7 +498,7 @@ hipError_t launch_verify_draft(const VerifyDraftCall& c, hipStream_t s) {
   a.accepted = c.accepted;
   a.tokens = c.tokens;
   a.accept_prob = c.accept_prob;
-  const dim3 g1((unsigned)(c.S * c.W * l.chunks)), g2((unsigned)(c.S * l.chunks)), block(kThreads);
+  const dim3 g1((unsigned)(c.S * c.W * l.chunks)), g2((unsigned)(c.q ? c.S * l.chunks : c.S)), block(kThreads);
   auto go = [&](auto k1, auto k2) -> hipError_t {
     hipLaunchKernelGGL(k1, g1, block, 0, s, a);
     const hipError_t e = hipGetLastError();
@@ -386,9 +506,12 @@ hipError_t launch_verify_draft(const VerifyDraftCall& c, hipStream_t s) {
     hipLaunchKernelGGL(k2, g2, block, 0, s, a);
     return hipGetLastError();
   };
-  if (c.dtype == K3MOE_DTYPE_F32) return go(stats_kernel<K3MOE_DTYPE_F32>, choose_kernel<K3MOE_DTYPE_F32>);
-  if (c.dtype == K3MOE_DTYPE_BF16) return go(stats_kernel<K3MOE_DTYPE_BF16>, choose_kernel<K3MOE_DTYPE_BF16>);
-  return go(stats_kernel<K3MOE_DTYPE_F16>, choose_kernel<K3MOE_DTYPE_F16>);
+  auto of_type = [&](auto k1, auto with, auto without) { return c.q ? go(k1, with) : go(k1, without); };
+  if (c.dtype == K3MOE_DTYPE_F32)
+    return of_type(stats_kernel<K3MOE_DTYPE_F32>, choose_kernel<K3MOE_DTYPE_F32, true>, choose_kernel<K3MOE_DTYPE_F32, false>);
+  if (c.dtype == K3MOE_DTYPE_BF16)
+    return of_type(stats_kernel<K3MOE_DTYPE_BF16>, choose_kernel<K3MOE_DTYPE_BF16, true>, choose_kernel<K3MOE_DTYPE_BF16, false>);
+  return of_type(stats_kernel<K3MOE_DTYPE_F16>, choose_kernel<K3MOE_DTYPE_F16, true>, choose_kernel<K3MOE_DTYPE_F16, false>);
 }
 
 }  // namespace k3moe
