@@ -24,12 +24,14 @@
 
 #include <math.h>
 
+#include <type_traits>
+
 namespace k3moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
-constexpr int kEach = kVocabChunk / kThreads;  // entries per thread
+// Threads of a workgroup: of the first launch, and of the second, whose waves
+// take a row's sums each.
+constexpr int kThreads = 256, kChooseThreads = 512;
 
 struct ChunkStat {
   float m;     // largest logit, -inf: none
@@ -69,11 +71,11 @@ __device__ __forceinline__ float logit(const uint8_t* row, int64_t i) {
   }
 }
 // Logits v .. v + kVec - 1 of a row of V (rows start at any multiple of the
-// type's size); -inf past its end.
+// type's size); -inf past its end.  whole: none of the caller's lie past it.
 template <int kType>
-__device__ __forceinline__ void logits16(const uint8_t* row, int v, int V, float* l) {
+__device__ __forceinline__ void logits16(const uint8_t* row, int v, int V, bool whole, float* l) {
   constexpr int n = kVec<kType>;
-  if (v + n <= V) {
+  if (whole) {
     uint32_t d[4];
     __builtin_memcpy(d, row + (int64_t)v * kSize<kType>, 16);
 #pragma unroll
@@ -93,56 +95,109 @@ __device__ __forceinline__ void logits16(const uint8_t* row, int v, int V, float
   }
 }
 
-// exp(d) for d <= 0: 2^n e^r with n = rint(d / ln 2), |r| <=
-// ln(2) / 2, and the power series of e^r to r^11 (what is left of it is below
-// r^12 / 12! = 7e-15).  NaN and everything below -800 give 0.
-__device__ __forceinline__ double exp_down(double d) {
-  d = fmax(d, -800.0);
-  constexpr double kShift = 6755399441055744.0;  // 1.5 * 2^52: an integer's bits end up in the lowest of the sum
-  const double t = fma(d, 1.4426950408889634, kShift);
-  const double n = t - kShift;
-  double r = fma(n, -6.93147180369123816490e-01, d);  // ln 2 in two parts, the first of 32 bits
-  r = fma(n, -1.90821492927058770002e-10, r);
-  double p = 1.0 / 39916800.0;
-  p = fma(p, r, 1.0 / 3628800.0);
-  p = fma(p, r, 1.0 / 362880.0);
-  p = fma(p, r, 1.0 / 40320.0);
-  p = fma(p, r, 1.0 / 5040.0);
-  p = fma(p, r, 1.0 / 720.0);
-  p = fma(p, r, 1.0 / 120.0);
-  p = fma(p, r, 1.0 / 24.0);
-  p = fma(p, r, 1.0 / 6.0);
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
-  return ldexp(p, (int)(uint32_t)(uint64_t)__double_as_longlong(t));
+// a * b + c with c from scalar registers.  (The compiler would copy every
+// coefficient of a series to vector registers first, for the two-operand form:
+// as many moves again.)
+__device__ __forceinline__ double fma_scalar(double a, double b, double c) {
+  double r;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "s"(c));
+  return r;
 }
 
 // exp((l - m) / T) for logits l <= m of a row or chunk whose largest is m: 0 for
-// NaN and -inf.
+// NaN and -inf.  As 2^y with y = (l - m) log2(e) / T = n + f, n = rint(y): 2^f on
+// |f| <= 1/2 by a polynomial fitted to it (1 at f = 0; largest relative error
+// 1.5e-14, near-minimax, by reweighted least squares on Chebyshev nodes).
 struct Scale {
-  double inv_t, m;
-  bool infinite;  // m is +inf (shared by the logits that reach it) or -inf (no logit is above it)
+  double m, c, least;  // c: log2(e) / T; least: l - m is taken no lower (its weight is 0 there)
+  bool infinite;       // m is +inf (shared by the logits that reach it) or -inf (no logit is above it)
 };
-__device__ __forceinline__ Scale scale_of(float m, double inv_t) { return Scale{inv_t, (double)m, fabsf(m) == INFINITY}; }
+__device__ __forceinline__ Scale scale_of(float m, double inv_t) {
+  const double c = fmax(inv_t * 1.4426950408889634, 1e-300);  // (T = inf: all finite logits weigh 1, and -inf still nothing)
+  return Scale{(double)m, c, fmax(-1100.0 / c, -1.7e308), fabsf(m) == INFINITY};
+}
+// ... for an m that is the same in the whole wave.
+__device__ __forceinline__ Scale scale_of_wave(float m, double inv_t) {
+  return scale_of(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(m))), inv_t);
+}
+// The weights of n logits; one coefficient after the other for all of them, which
+// keeps it in its registers.
+template <int n>
+__device__ __forceinline__ void weights(const float* l, const Scale& s, double* w) {
+  if (s.infinite) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) w[i] = l[i] == INFINITY ? 1.0 : 0.0;
+    return;
+  }
+  constexpr double kShift = 6755399441055744.0;  // 1.5 * 2^52: an integer's bits end up in the lowest of the sum
+  constexpr double kP[10] = {1.0, 0.6931471805598851, 0.2402265069572282, 0.055504108668415666, 0.009618129181164007,
+                             0.0013333557625477394, 0.00015403440884395527, 1.5252990012952022e-05, 1.3258335417356016e-06,
+                             1.0148340949089715e-07};
+  double f[n];
+  int e[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const double d = fmax((double)l[i] - s.m, s.least);  // (the difference first: a low temperature makes much of its last bits; NaN: least)
+    const double t = fma(d, s.c, kShift);
+    e[i] = (int)(uint32_t)(uint64_t)__double_as_longlong(t);
+    f[i] = fma(d, s.c, kShift - t);
+    w[i] = kP[9];
+  }
+#pragma unroll
+  for (int k = 8; k >= 0; --k)
+#pragma unroll
+    for (int i = 0; i < n; ++i) w[i] = fma_scalar(w[i], f[i], kP[k]);
+#pragma unroll
+  for (int i = 0; i < n; ++i) w[i] = ldexp(w[i], e[i]);
+}
 __device__ __forceinline__ double weight(float l, const Scale& s) {
-  if (s.infinite) return l == INFINITY ? 1.0 : 0.0;
-  return exp_down(((double)fmaxf(l, -INFINITY) - s.m) * s.inv_t);  // (fmaxf: NaN as -inf; the difference first: a low temperature leaves nothing of 1 / T's last bits)
+  double w;
+  weights<1>(&l, s, &w);
+  return w;
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = fmaxf(v, __shfl_xor(v, d, 64));
+// Reductions over a wave, the result in every lane: exchanges inside rows of 16
+// lanes by DPP, then with the other rows (the gfx950 row swaps), no LDS trips.
+template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xF, 0xF, false);
+}
+__device__ __forceinline__ uint32_t other_row(uint32_t v, int lane, bool far) {
+  const auto r = far ? __builtin_amdgcn_permlane32_swap(v, v, false, false) : __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  return (lane & (far ? 32 : 16)) ? r[0] : r[1];
+}
+template <int kStep>
+__device__ __forceinline__ uint32_t partner(uint32_t v, int lane) {
+  if constexpr (kStep == 0) return dpp<0xB1>(v);        // lane ^ 1
+  else if constexpr (kStep == 1) return dpp<0x4E>(v);   // lane ^ 2
+  else if constexpr (kStep == 2) return dpp<0x141>(v);  // mirrored in its half row
+  else if constexpr (kStep == 3) return dpp<0x140>(v);  // mirrored in its row
+  else return other_row(v, lane, kStep == 5);
+}
+template <int kStep>
+__device__ __forceinline__ double partner(double v, int lane) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)partner<kStep>((uint32_t)(b >> 32), lane) << 32 | partner<kStep>((uint32_t)b, lane)));
+}
+template <typename F>
+__device__ __forceinline__ void six_steps(F&& f) {
+  f(std::integral_constant<int, 0>{});
+  f(std::integral_constant<int, 1>{});
+  f(std::integral_constant<int, 2>{});
+  f(std::integral_constant<int, 3>{});
+  f(std::integral_constant<int, 4>{});
+  f(std::integral_constant<int, 5>{});
+}
+__device__ __forceinline__ float wave_max(float v, int lane) {
+  six_steps([&](auto k) { v = fmaxf(v, __uint_as_float(partner<decltype(k)::value>(__float_as_uint(v), lane))); });
   return v;
 }
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d, 64);
+__device__ __forceinline__ double wave_sum(double v, int lane) {
+  six_steps([&](auto k) { v += partner<decltype(k)::value>(v, lane); });
   return v;
 }
-__device__ __forceinline__ int wave_min(int v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v = min(v, __shfl_xor(v, d, 64));
+__device__ __forceinline__ int wave_min(int v, int lane) {
+  six_steps([&](auto k) { v = min(v, (int)partner<decltype(k)::value>((uint32_t)v, lane)); });
   return v;
 }
 // Sum over the lanes up to this one.
@@ -159,50 +214,55 @@ __device__ __forceinline__ float temperature_of(const VerifyArgs& a, int64_t s) 
 
 template <int kType>
 __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a) {
+  constexpr int kWaves = kThreads / 64, kEach = kVocabChunk / kThreads;
   __shared__ ChunkStat part[kWaves];
   const int64_t r = blockIdx.x / (unsigned)a.chunks;
   const int c = (int)(blockIdx.x - r * a.chunks);
   const int64_t s = r / a.W;
-  const int wave = threadIdx.x >> 6;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   if (c == 0 && r == s * a.W && threadIdx.x == 0) a.done[s] = 0u;
   const uint8_t* const row = a.logits + r * a.V * kSize<kType>;
   constexpr int n = kVec<kType>;
   const int v0 = c * kVocabChunk + (int)threadIdx.x * n;
+  const bool whole = (c + 1) * kVocabChunk <= a.V;
   float l[kEach];
 #pragma unroll
-  for (int i = 0; i < kEach; i += n) logits16<kType>(row, v0 + i * kThreads, a.V, l + i);
+  for (int i = 0; i < kEach; i += n) logits16<kType>(row, v0 + i * kThreads, a.V, whole, l + i);
   const float t = temperature_of(a, s);
   const bool greedy = !(t > 0.0f);
+  const double inv_t = 1.0 / (double)t;
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) m = fmaxf(m, l[i]);  // (passes over NaN)
-  m = wave_max(m);
+  m = wave_max(m, lane);
   double z = 0.0;
   int at = INT_MAX;
   if (greedy) {
 #pragma unroll
     for (int i = kEach - 1; i >= 0; --i)
       if (l[i] == m && m > -INFINITY) at = v0 + i / n * n * kThreads + i % n;
-    at = wave_min(at);
+    at = wave_min(at, lane);
   } else {
-    const Scale sc = scale_of(m, 1.0 / (double)t);
+    const Scale sc = scale_of_wave(m, inv_t);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) z += weight(l[i], sc);
-    z = wave_sum(z);
+    for (int i = 0; i < kEach; i += 8) {
+      double w[8];
+      weights<8>(l + i, sc, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z += w[j];
+    }
+    z = wave_sum(z, lane);
   }
-  if ((threadIdx.x & 63) == 0) part[wave] = ChunkStat{m, at, z};
+  if (lane == 0) part[wave] = ChunkStat{m, at, z};
   __syncthreads();
   if (threadIdx.x < 64) {  // the waves' together, each at its own largest so far
-    const int lane = threadIdx.x;
     const ChunkStat x = part[lane < kWaves ? lane : 0];
-    m = wave_max(x.m);
-    z = lane < kWaves && !greedy ? x.z * weight(x.m, scale_of(m, 1.0 / (double)t)) : 0.0;
+    m = wave_max(x.m, lane);
+    z = lane < kWaves && !greedy ? x.z * weight(x.m, scale_of_wave(m, inv_t)) : 0.0;
     at = greedy && x.m == m ? x.at : INT_MAX;
-#pragma unroll
-    for (int d = 1; d < kWaves; d <<= 1) {
-      z += __shfl_xor(z, d, 64);
-      at = min(at, __shfl_xor(at, d, 64));
-    }
+    z += partner<0>(z, lane);
+    z += partner<1>(z, lane);  // (the four waves')
+    at = wave_min(at, lane);
     if (lane == 0) a.stats[r * a.chunks + c] = ChunkStat{m, at, z};
   }
 }
@@ -217,8 +277,8 @@ __device__ __forceinline__ RowStat row_stat(const ChunkStat* st, int chunks, int
   const ChunkStat own = lane < chunks ? st[lane] : ChunkStat{-INFINITY, INT_MAX, 0.0};
   float m = own.m;
   for (int c = lane + 64; c < chunks; c += 64) m = fmaxf(m, st[c].m);
-  m = wave_max(m);
-  const Scale sc = scale_of(m, inv_t);
+  m = wave_max(m, lane);
+  const Scale sc = scale_of_wave(m, inv_t);
   auto take = [&](const ChunkStat& x) { return greedy ? 0.0 : x.z * weight(x.m, sc); };
   double z = take(own);
   int at = greedy && own.m == m ? own.at : INT_MAX;
@@ -227,7 +287,7 @@ __device__ __forceinline__ RowStat row_stat(const ChunkStat* st, int chunks, int
     z += take(x);
     if (greedy && x.m == m) at = min(at, x.at);
   }
-  return RowStat{m, greedy ? wave_min(at) : INT_MAX, greedy ? 0.0 : wave_sum(z)};
+  return RowStat{m, greedy ? wave_min(at, lane) : INT_MAX, greedy ? 0.0 : wave_sum(z, lane)};
 }
 
 // What is sampled from, entry v of a row: max(p - q, 0) or p.
@@ -238,53 +298,55 @@ struct Source {
   int x;           // the proposal, -1: none
   bool residual;
 };
-__device__ __forceinline__ double entry(const Source& d, float l, int v, float q) {
-  const double p = weight(l, d.sc) * d.inv_z;
-  if (!d.residual) return p;
-  return fmax(p - (d.q ? (double)q : v == d.x ? 1.0 : 0.0), 0.0);
-}
 // Entries v .. v + kVec - 1 (0 past the row's end).
 template <int kType>
-__device__ __forceinline__ void entries16(const Source& d, const uint8_t* row, int v, int V, double* e) {
+__device__ __forceinline__ void entries16(const Source& d, const uint8_t* row, int v, int V, bool whole, double* e) {
   constexpr int n = kVec<kType>;
   float l[n], q[n];
-  logits16<kType>(row, v, V, l);
+  logits16<kType>(row, v, V, whole, l);
   if (d.residual && d.q) {
 #pragma unroll
-    for (int i = 0; i < n; i += 4) logits16<K3MOE_DTYPE_F32>(reinterpret_cast<const uint8_t*>(d.q), v + i, V, q + i);
+    for (int i = 0; i < n; i += 4) logits16<K3MOE_DTYPE_F32>(reinterpret_cast<const uint8_t*>(d.q), v + i, V, whole, q + i);
   } else {
 #pragma unroll
-    for (int i = 0; i < n; ++i) q[i] = 0.0f;
+    for (int i = 0; i < n; ++i) q[i] = d.residual && v + i == d.x ? 1.0f : 0.0f;
   }
+  weights<n>(l, d.sc, e);
 #pragma unroll
-  for (int i = 0; i < n; ++i) e[i] = v + i < V ? entry(d, l[i], v + i, q[i]) : 0.0;
+  for (int i = 0; i < n; ++i) {
+    e[i] *= d.inv_z;
+    if (d.residual) e[i] = fmax(e[i] - (double)q[i], 0.0);
+    if (!whole && v + i >= V) e[i] = 0.0;
+  }
 }
 // This thread's part of a chunk's share.
 template <int kType>
 __device__ __forceinline__ double chunk_part(const Source& d, const uint8_t* row, int c, int V) {
-  constexpr int n = kVec<kType>;
+  constexpr int n = kVec<kType>, kEach = kVocabChunk / kChooseThreads;
   double sum = 0.0;
 #pragma unroll
   for (int i = 0; i < kEach; i += n) {
     double e[n];
-    entries16<kType>(d, row, c * kVocabChunk + (i * kThreads + (int)threadIdx.x * n), V, e);
+    entries16<kType>(d, row, c * kVocabChunk + (i * kChooseThreads + (int)threadIdx.x * n), V, (c + 1) * kVocabChunk <= V, e);
 #pragma unroll
     for (int j = 0; j < n; ++j) sum += e[j];
   }
   return sum;
 }
 // The sum over the workgroup, in thread 0.
-__device__ __forceinline__ double block_sum(double v, double (&part)[kWaves]) {
-  v = wave_sum(v);
+constexpr int kChooseWaves = kChooseThreads / 64;
+__device__ __forceinline__ double block_sum(double v, double (&part)[kChooseWaves]) {
+  v = wave_sum(v, threadIdx.x & 63);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
   __syncthreads();
   if (threadIdx.x == 0)
-    for (int i = 1; i < kWaves; ++i) v += part[i];
+    for (int i = 1; i < kChooseWaves; ++i) v += part[i];
   return v;
 }
 
 template <int kType, bool kProbs>
-__global__ __launch_bounds__(kThreads) void choose_kernel(VerifyArgs a) {
+__global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
+  constexpr int kWaves = kChooseWaves, kEach = kVocabChunk / kChooseThreads;
   __shared__ RowStat rows[kMaxVerifyWidth];
   __shared__ double part[kWaves], own_mass, sh_target, sh_before;
   __shared__ int sh_count, sh_last, sh_found, sh_residual, wat[kWaves], wlast[kWaves];
@@ -346,7 +408,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(VerifyArgs a) {
   }
 
   const uint8_t* const row = a.logits + (s * W + count) * V * kSize<kType>;
-  Source d{scale_of(st.m, inv_t), st.z > 0.0 ? 1.0 / st.z : 0.0, nullptr, -1, count < n};
+  Source d{scale_of_wave(st.m, inv_t), st.z > 0.0 ? 1.0 / st.z : 0.0, nullptr, -1, count < n};
   if (d.residual) {
     d.x = a.draft[s * D + count];
     if constexpr (kProbs) d.q = a.q + (s * D + count) * V;
@@ -386,7 +448,7 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(VerifyArgs a) {
     auto total_of = [&]() {
       double v = 0.0;
       for (int i = lane; i < a.chunks; i += 64) v += share(i);
-      return wave_sum(v);
+      return wave_sum(v, lane);
     };
     double total = total_of();
     if (residual && !(total > 0.0)) {  // p nowhere above q: p itself
@@ -422,13 +484,13 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(VerifyArgs a) {
     if (threadIdx.x == 0) *token = -1;
     return;
   }
-  // The entry: sixteen in a row per thread.
+  // The entry: eight in a row per thread.
   d.residual = sh_residual != 0;
   const double target = sh_target;
   const int b0 = f * kVocabChunk + (int)threadIdx.x * kEach;
   double e[kEach], mine = 0.0;
 #pragma unroll
-  for (int i = 0; i < kEach; i += kVec<kType>) entries16<kType>(d, row, b0 + i, V, e + i);
+  for (int i = 0; i < kEach; i += kVec<kType>) entries16<kType>(d, row, b0 + i, V, (f + 1) * kVocabChunk <= V, e + i);
 #pragma unroll
   for (int i = 0; i < kEach; ++i) mine += e[i];
   const double incl = wave_scan(mine, lane);
@@ -447,8 +509,8 @@ __global__ __launch_bounds__(kThreads) void choose_kernel(VerifyArgs a) {
       if (sum > target) at = min(at, b0 + i);
     }
   }
-  at = wave_min(at);
-  last = -wave_min(-last);
+  at = wave_min(at, lane);
+  last = -wave_min(-last, lane);
   if (lane == 0) {
     wat[wave] = at;
     wlast[wave] = last;
@@ -498,12 +560,12 @@ hipError_t launch_verify_draft(const VerifyDraftCall& c, hipStream_t s) {
   a.accepted = c.accepted;
   a.tokens = c.tokens;
   a.accept_prob = c.accept_prob;
-  const dim3 g1((unsigned)(c.S * c.W * l.chunks)), g2((unsigned)(c.q ? c.S * l.chunks : c.S)), block(kThreads);
+  const dim3 g1((unsigned)(c.S * c.W * l.chunks)), g2((unsigned)(c.q ? c.S * l.chunks : c.S));
   auto go = [&](auto k1, auto k2) -> hipError_t {
-    hipLaunchKernelGGL(k1, g1, block, 0, s, a);
+    hipLaunchKernelGGL(k1, g1, dim3(kThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k2, g2, block, 0, s, a);
+    hipLaunchKernelGGL(k2, g2, dim3(kChooseThreads), 0, s, a);
     return hipGetLastError();
   };
   auto of_type = [&](auto k1, auto with, auto without) { return c.q ? go(k1, with) : go(k1, without); };
