@@ -344,14 +344,17 @@ __device__ __forceinline__ double block_sum(double v, double (&part)[kChooseWave
   return v;
 }
 
-template <int kType, bool kProbs>
+// kPer: chunks of a workgroup (0: without draft distributions, one workgroup per sequence).
+template <int kType, int kPer>
 __global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
+  constexpr bool kProbs = kPer > 0;
   constexpr int kWaves = kChooseWaves, kEach = kVocabChunk / kChooseThreads;
   __shared__ RowStat rows[kMaxVerifyWidth];
   __shared__ double part[kWaves], own_mass, sh_target, sh_before;
   __shared__ int sh_count, sh_last, sh_found, sh_residual, wat[kWaves], wlast[kWaves];
-  const int64_t s = kProbs ? blockIdx.x / (unsigned)a.chunks : blockIdx.x;
-  const int c = kProbs ? (int)(blockIdx.x - s * a.chunks) : 0;
+  const unsigned wgs = kProbs ? (unsigned)(a.chunks + kPer - 1) / (unsigned)(kProbs ? kPer : 1) : 1u;  // of a sequence
+  const int64_t s = blockIdx.x / wgs;
+  const int c = (int)(blockIdx.x - s * wgs);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int W = a.W, V = a.V, D = W - 1;
   const float t = temperature_of(a, s);
@@ -417,10 +420,29 @@ __global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
   const int own = !kProbs && d.residual && inside ? d.x / kVocabChunk : -1;  // the chunk whose share of max(p - q, 0) is not that of p
   if constexpr (kProbs) {
     if (d.residual) {  // (else p's shares are there)
-      const double mass = block_sum(chunk_part<kType>(d, row, c, V), part);
+      __shared__ double sums[kProbs ? kPer : 1][kWaves];
+      double own_sum[kProbs ? kPer : 1];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) own_sum[i] = c * kPer + i < a.chunks ? chunk_part<kType>(d, row, c * kPer + i, V) : 0.0;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        own_sum[i] = wave_sum(own_sum[i], lane);
+        if (lane == 0) sums[i][wave] = own_sum[i];
+      }
+      __syncthreads();
       if (threadIdx.x == 0) {
-        __hip_atomic_store(a.mass + s * a.chunks + c, mass, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        sh_last = __hip_atomic_fetch_add(a.done + s, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)a.chunks - 1u;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          double mass = 0.0;
+          for (int w = 0; w < kWaves; ++w) mass += sums[i][w];
+          if (c * kPer + i < a.chunks) __hip_atomic_store(a.mass + s * a.chunks + c * kPer + i, mass, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
+        // The shares are written through to where the last workgroup's device-scope
+        // loads find them before the count says so.  (Release and acquire would write
+        // back and invalidate a whole L2 for every workgroup: 42 us instead of 20 for
+        // 32 rows of 163840.)
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        sh_last = __hip_atomic_fetch_add(a.done + s, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == wgs - 1u;
       }
       __syncthreads();
       if (!sh_last) return;
@@ -560,20 +582,23 @@ hipError_t launch_verify_draft(const VerifyDraftCall& c, hipStream_t s) {
   a.accepted = c.accepted;
   a.tokens = c.tokens;
   a.accept_prob = c.accept_prob;
-  const dim3 g1((unsigned)(c.S * c.W * l.chunks)), g2((unsigned)(c.q ? c.S * l.chunks : c.S));
-  auto go = [&](auto k1, auto k2) -> hipError_t {
-    hipLaunchKernelGGL(k1, g1, dim3(kThreads), 0, s, a);
+  // Chunks of a workgroup of the second launch: each takes the proposals' test
+  // first, so four where that still leaves a workgroup for every CU.
+  const int per = !c.q ? 0 : c.S * ((l.chunks + 3) / 4) >= device_cu_count() ? 4 : 1;
+  const dim3 g1((unsigned)(c.S * c.W * l.chunks)), g2((unsigned)(c.S * (per ? (l.chunks + per - 1) / per : 1)));
+  auto go = [&](auto type) -> hipError_t {
+    constexpr int kType = decltype(type)::value;
+    hipLaunchKernelGGL(stats_kernel<kType>, g1, dim3(kThreads), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k2, g2, dim3(kChooseThreads), 0, s, a);
+    if (per == 0) hipLaunchKernelGGL((choose_kernel<kType, 0>), g2, dim3(kChooseThreads), 0, s, a);
+    else if (per == 1) hipLaunchKernelGGL((choose_kernel<kType, 1>), g2, dim3(kChooseThreads), 0, s, a);
+    else hipLaunchKernelGGL((choose_kernel<kType, 4>), g2, dim3(kChooseThreads), 0, s, a);
     return hipGetLastError();
   };
-  auto of_type = [&](auto k1, auto with, auto without) { return c.q ? go(k1, with) : go(k1, without); };
-  if (c.dtype == K3MOE_DTYPE_F32)
-    return of_type(stats_kernel<K3MOE_DTYPE_F32>, choose_kernel<K3MOE_DTYPE_F32, true>, choose_kernel<K3MOE_DTYPE_F32, false>);
-  if (c.dtype == K3MOE_DTYPE_BF16)
-    return of_type(stats_kernel<K3MOE_DTYPE_BF16>, choose_kernel<K3MOE_DTYPE_BF16, true>, choose_kernel<K3MOE_DTYPE_BF16, false>);
-  return of_type(stats_kernel<K3MOE_DTYPE_F16>, choose_kernel<K3MOE_DTYPE_F16, true>, choose_kernel<K3MOE_DTYPE_F16, false>);
+  if (c.dtype == K3MOE_DTYPE_F32) return go(std::integral_constant<int, K3MOE_DTYPE_F32>{});
+  if (c.dtype == K3MOE_DTYPE_BF16) return go(std::integral_constant<int, K3MOE_DTYPE_BF16>{});
+  return go(std::integral_constant<int, K3MOE_DTYPE_F16>{});
 }
 
 }  // namespace k3moe
