@@ -112,13 +112,21 @@ struct Scale {
   double m, c, least;  // c: log2(e) / T; least: l - m is taken no lower (its weight is 0 there)
   bool infinite;       // m is +inf (shared by the logits that reach it) or -inf (no logit is above it)
 };
-__device__ __forceinline__ Scale scale_of(float m, double inv_t) {
-  const double c = fmax(inv_t * 1.4426950408889634, 1e-300);  // (T = inf: all finite logits weigh 1, and -inf still nothing)
-  return Scale{(double)m, c, fmax(-1100.0 / c, -1.7e308), fabsf(m) == INFINITY};
+// What a temperature gives: log2(e) / T and the lowest difference of logits.
+struct Heat {
+  double c, least;
+};
+__device__ __forceinline__ Heat heat_of(const float* temperature, int64_t s) {
+  constexpr double kLog2E = 1.4426950408889634;
+  if (!temperature) return Heat{kLog2E, -1100.0 / kLog2E};
+  const double t = (double)temperature[s];
+  // (T = inf: all finite logits weigh 1, and -inf still nothing)
+  return Heat{fmax(kLog2E / t, 1e-300), fmax(-1100.0 / kLog2E * t, -1.7e308)};
 }
+__device__ __forceinline__ Scale scale_of(float m, const Heat& h) { return Scale{(double)m, h.c, h.least, fabsf(m) == INFINITY}; }
 // ... for an m that is the same in the whole wave.
-__device__ __forceinline__ Scale scale_of_wave(float m, double inv_t) {
-  return scale_of(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(m))), inv_t);
+__device__ __forceinline__ Scale scale_of_wave(float m, const Heat& h) {
+  return scale_of(__uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(m))), h);
 }
 // The weights of n logits; one coefficient after the other for all of them, which
 // keeps it in its registers.
@@ -210,7 +218,7 @@ __device__ __forceinline__ double wave_scan(double v, int lane) {
   return v;
 }
 
-__device__ __forceinline__ float temperature_of(const VerifyArgs& a, int64_t s) { return a.temperature ? a.temperature[s] : 1.0f; }
+__device__ __forceinline__ bool greedy_of(const VerifyArgs& a, int64_t s) { return a.temperature && !(a.temperature[s] > 0.0f); }
 
 template <int kType>
 __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a) {
@@ -228,9 +236,8 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a) {
   float l[kEach];
 #pragma unroll
   for (int i = 0; i < kEach; i += n) logits16<kType>(row, v0 + i * kThreads, a.V, whole, l + i);
-  const float t = temperature_of(a, s);
-  const bool greedy = !(t > 0.0f);
-  const double inv_t = 1.0 / (double)t;
+  const bool greedy = greedy_of(a, s);
+  const Heat heat = heat_of(a.temperature, s);
   float m = -INFINITY;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) m = fmaxf(m, l[i]);  // (passes over NaN)
@@ -243,13 +250,12 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a) {
       if (l[i] == m && m > -INFINITY) at = v0 + i / n * n * kThreads + i % n;
     at = wave_min(at, lane);
   } else {
-    const Scale sc = scale_of_wave(m, inv_t);
+    const Scale sc = scale_of_wave(m, heat);
 #pragma unroll
-    for (int i = 0; i < kEach; i += 8) {
-      double w[8];
-      weights<8>(l + i, sc, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) z += w[j];
+    for (int i = 0; i < kEach; i += 4) {
+      double w[4];
+      weights<4>(l + i, sc, w);
+      z += (w[0] + w[1]) + (w[2] + w[3]);
     }
     z = wave_sum(z, lane);
   }
@@ -258,7 +264,7 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyArgs a) {
   if (threadIdx.x < 64) {  // the waves' together, each at its own largest so far
     const ChunkStat x = part[lane < kWaves ? lane : 0];
     m = wave_max(x.m, lane);
-    z = lane < kWaves && !greedy ? x.z * weight(x.m, scale_of_wave(m, inv_t)) : 0.0;
+    z = lane < kWaves && !greedy ? x.z * weight(x.m, scale_of_wave(m, heat)) : 0.0;
     at = greedy && x.m == m ? x.at : INT_MAX;
     z += partner<0>(z, lane);
     z += partner<1>(z, lane);  // (the four waves')
@@ -273,12 +279,12 @@ struct RowStat {
   int at;
   double z;
 };
-__device__ __forceinline__ RowStat row_stat(const ChunkStat* st, int chunks, int lane, double inv_t, bool greedy) {
+__device__ __forceinline__ RowStat row_stat(const ChunkStat* st, int chunks, int lane, const Heat& heat, bool greedy) {
   const ChunkStat own = lane < chunks ? st[lane] : ChunkStat{-INFINITY, INT_MAX, 0.0};
   float m = own.m;
   for (int c = lane + 64; c < chunks; c += 64) m = fmaxf(m, st[c].m);
   m = wave_max(m, lane);
-  const Scale sc = scale_of_wave(m, inv_t);
+  const Scale sc = scale_of_wave(m, heat);
   auto take = [&](const ChunkStat& x) { return greedy ? 0.0 : x.z * weight(x.m, sc); };
   double z = take(own);
   int at = greedy && own.m == m ? own.at : INT_MAX;
@@ -357,9 +363,8 @@ __global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
   const int c = (int)(blockIdx.x - s * wgs);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int W = a.W, V = a.V, D = W - 1;
-  const float t = temperature_of(a, s);
-  const bool greedy = !(t > 0.0f);
-  const double inv_t = greedy ? 1.0 : 1.0 / (double)t;
+  const bool greedy = greedy_of(a, s);
+  const Heat heat = heat_of(a.temperature, s);
   // the proposals, one lane each: what their test reads, asked for ahead of the sums
   int x = -1;
   float xl = -INFINITY, xq = 1.0f, xu = 0.0f;
@@ -374,7 +379,7 @@ __global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
   int n = a.len ? a.len[s] : D;
   n = n < 0 ? 0 : n > D ? D : n;
   for (int w = wave; w < W; w += kWaves) {
-    const RowStat st = row_stat(a.stats + (s * W + w) * a.chunks, a.chunks, lane, inv_t, greedy);
+    const RowStat st = row_stat(a.stats + (s * W + w) * a.chunks, a.chunks, lane, heat, greedy);
     if (lane == 0) rows[w] = st;
   }
   __syncthreads();
@@ -387,7 +392,7 @@ __global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
         take = x == st.at;
         chance = take ? 1.0 : 0.0;
       } else if (st.z > 0.0) {
-        const double p = weight(xl, scale_of(st.m, inv_t)) / st.z, q = (double)xq;
+        const double p = weight(xl, scale_of(st.m, heat)) / st.z, q = (double)xq;
         take = (double)xu * q < p;
         chance = q < p ? 1.0 : q > 0.0 ? p / q : 0.0;
       }
@@ -411,7 +416,7 @@ __global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
   }
 
   const uint8_t* const row = a.logits + (s * W + count) * V * kSize<kType>;
-  Source d{scale_of_wave(st.m, inv_t), st.z > 0.0 ? 1.0 / st.z : 0.0, nullptr, -1, count < n};
+  Source d{scale_of_wave(st.m, heat), st.z > 0.0 ? 1.0 / st.z : 0.0, nullptr, -1, count < n};
   if (d.residual) {
     d.x = a.draft[s * D + count];
     if constexpr (kProbs) d.q = a.q + (s * D + count) * V;
