@@ -5,13 +5,23 @@
 // is taken on fp64 scores with ties to the lower index, as in route.hip, so that
 // the selected ids are reproducible bit for bit.
 //
-// The scores of a token lie in LDS ([E] fp64) beside those of its groups
-// ([groups]).  The lanes take the groups in turn; the last of the kept groups is
-// found by `keep` rounds of the best group that ranks strictly after the one
-// before, which needs no flags; experts of the other groups are marked with NaN
-// (NaN scores themselves have become -inf by then), and k such rounds take the
-// experts.
+// Up to 1024 experts and 64 groups a token's logits stay in registers (lane l:
+// experts l, l + 64, ...).  fp32 scores, whose error has a bound (err below), take
+// the decisions that they are sure of: a few lanes per group find its best two
+// through LDS; the groups are kept by the threshold that their keep-th largest
+// score is, unless another lies within the error of it; the experts of the kept
+// groups that come within the error of the k-th best lane's best, at most 64,
+// are scored in fp64 and ranked by counting.  Without a bias a softmax's experts
+// are compared by their logits, which fp32 holds exactly.
+// What fp32 is not sure of (heavy ties, values that are no numbers, masked rows)
+// and larger sizes go the plain way: the fp64 scores of a token lie in LDS ([E])
+// beside those of its groups ([groups]); the last of the kept groups is found by
+// `keep` rounds of the best group that ranks strictly after the one before,
+// which needs no flags; experts of the other groups are marked with NaN (NaN
+// scores themselves have become -inf by then), and k such rounds take the experts.
 #include "route_device.h"
+
+#include <type_traits>
 
 namespace k3moe {
 namespace {
@@ -146,6 +156,287 @@ __device__ __forceinline__ void route_token(const GroupsArgs& a, int64_t t, int 
   }
 }
 
+// ---------------------------------------------------------------------------
+// The register path.
+
+// exp(d) for d <= 0 to 1.5e-14 of it, 0 below -762: 2^y, y = d log2(e) = n + f,
+// n = rint(y), 2^f by a fitted polynomial (verify_draft.hip).  Coefficients come
+// from scalar registers (fma_scalar there).
+__device__ __forceinline__ double fma_scalar(double a, double b, double c) {
+  double r;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "s"(c));
+  return r;
+}
+template <int n>
+__device__ __forceinline__ void exp_down(const double (&d)[n], double (&w)[n]) {
+  constexpr double kShift = 6755399441055744.0, kLog2E = 1.4426950408889634;
+  constexpr double kP[10] = {1.0, 0.6931471805598851, 0.2402265069572282, 0.055504108668415666, 0.009618129181164007,
+                             0.0013333557625477394, 0.00015403440884395527, 1.5252990012952022e-05, 1.3258335417356016e-06,
+                             1.0148340949089715e-07};
+  double f[n];
+  int e[n];
+#pragma unroll
+  for (int i = 0; i < n; ++i) {
+    const double x = fmax(d[i], -1100.0 / kLog2E), t = fma(x, kLog2E, kShift);
+    e[i] = (int)(uint32_t)(uint64_t)__double_as_longlong(t);
+    f[i] = fma(x, kLog2E, kShift - t);
+    w[i] = kP[9];
+  }
+#pragma unroll
+  for (int k = 8; k >= 0; --k)
+#pragma unroll
+    for (int i = 0; i < n; ++i) w[i] = fma_scalar(w[i], f[i], kP[k]);
+#pragma unroll
+  for (int i = 0; i < n; ++i) w[i] = ldexp(w[i], e[i]);
+}
+
+// Value of the lane that step k (0 .. 5) of a reduction exchanges with.
+template <int k>
+__device__ __forceinline__ uint32_t partner(uint32_t v, int lane) {
+  if constexpr (k == 0) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);        // lane ^ 1
+  else if constexpr (k == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false);   // lane ^ 2
+  else if constexpr (k == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false);  // mirrored in its half row
+  else if constexpr (k == 3) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false);  // mirrored in its row
+  else return swap_rows<k == 4 ? 16 : 32>(v, lane);
+}
+template <int k>
+__device__ __forceinline__ float partner(float v, int lane) { return __uint_as_float(partner<k>(__float_as_uint(v), lane)); }
+template <int k>
+__device__ __forceinline__ double partner(double v, int lane) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)partner<k>((uint32_t)(b >> 32), lane) << 32 | partner<k>((uint32_t)b, lane)));
+}
+// f(k) for the first log2(count) steps: lanes l / count apart stay apart (steps 2
+// and 3 mirror, after which the lanes of 8 and of 16 agree all the same).
+template <typename F>
+__device__ __forceinline__ void steps(int count, F&& f) {
+  if (count > 1) f(std::integral_constant<int, 0>{});
+  if (count > 2) f(std::integral_constant<int, 1>{});
+  if (count > 4) f(std::integral_constant<int, 2>{});
+  if (count > 8) f(std::integral_constant<int, 3>{});
+  if (count > 16) f(std::integral_constant<int, 4>{});
+  if (count > 32) f(std::integral_constant<int, 5>{});
+}
+
+// LDS of a wave: candidates' fp64 score, gate and expert, their logits and
+// biases; the top k by rank; behind it the fp32 scores [E].
+struct FastScratch {
+  double fs[kWaveSize], tg[kWaveSize];
+  int fe[kWaveSize], te[kWaveSize];
+  float cz[kWaveSize], cb[kWaveSize];
+};
+
+// Routes token t from registers; false where fp32 is not sure.  lanes: of a group
+// (a power of two, lanes * groups <= 64); inv_size: ceil(2^20 / size), which
+// divides every index below 1024 by size exactly.
+template <int NPER>
+__device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t, int lane, int lanes, uint32_t inv_size, FastScratch& x, float* score) {
+  const float* const zt = a.z + t * (int64_t)a.E;
+  float z[NPER], b[NPER];
+#pragma unroll
+  for (int j = 0; j < NPER; ++j) z[j] = zt[min(lane + kWaveSize * j, a.E - 1)];
+#pragma unroll
+  for (int j = 0; j < NPER; ++j) b[j] = a.bias ? a.bias[min(lane + kWaveSize * j, a.E - 1)] : 0.0f;
+
+  // fp32 scores s, of experts past E -inf, and what groups add up (gs).  u = 2^-24:
+  //   sigmoid: off by at most 2^-21 (1 + |s|) (route_device.h).
+  //   softmax: e^(z - m) from the rounded difference and the hardware exp2 is off by
+  //   (2 |z - m| + 3) u of itself, so by 3 u absolutely; their sum, of at least 1, by
+  //   (2 (ln E + 1) + 3 + NPER + 6) u < 2^-18 of itself (terms weigh |z - m| by at
+  //   most ln E + 1 on the whole): a gate by less than 2^-17 of the largest gate,
+  //   and the bias' addition by u |s|.
+  float s[NPER], m = 0.0f, top = 1.0f;
+  const bool by_logit = a.softmax && !a.bias;
+  if (a.softmax) {
+    m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NPER; ++j) m = fmaxf(m, z[j]);  // (passes over NaN; an expert seen twice does no harm)
+    steps(kWaveSize, [&](auto k) { m = fmaxf(m, partner<decltype(k)::value>(m, lane)); });
+    if (!(fabsf(m) < INFINITY)) return false;
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NPER; ++j) {
+      s[j] = __builtin_amdgcn_exp2f((z[j] - m) * 1.44269504088896341f);
+      sum += lane + kWaveSize * j < a.E ? s[j] : 0.0f;
+    }
+    steps(kWaveSize, [&](auto k) { sum += partner<decltype(k)::value>(sum, lane); });
+    if (!(sum < INFINITY)) return false;  // (NaN)
+    if (!by_logit) {
+      top = __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+      for (int j = 0; j < NPER; ++j) s[j] = s[j] * top + b[j];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < NPER; ++j) s[j] = route_score32(z[j], b[j]);
+  }
+  const float rel = a.softmax ? 0x1p-22f : 0x1p-21f, base = (a.softmax ? 0x1p-16f : 0x1p-21f) * top;  // |error of s| <= base + rel |s|
+
+  // The kept groups, a bit per group's first lane.
+  uint64_t kept = 0;
+  const int n_kept = a.keep * a.size;
+  if (a.keep < a.groups) {
+#pragma unroll
+    for (int j = 0; j < NPER; ++j)
+      if (lane + kWaveSize * j < a.E) score[lane + kWaveSize * j] = s[j];
+    wave_fence();
+    const int g = lane / lanes, sub = lane & (lanes - 1);
+    float b1 = -INFINITY, b2 = -INFINITY;
+    if (g < a.groups)
+      for (int i = sub; i < a.size; i += lanes) {
+        const float v = score[g * a.size + i];
+        b2 = __builtin_amdgcn_fmed3f(b1, b2, v);  // (b2 <= b1: the middle one is the second best)
+        b1 = fmaxf(b1, v);
+      }
+    steps(lanes, [&](auto k) {
+      const float o1 = partner<decltype(k)::value>(b1, lane), o2 = partner<decltype(k)::value>(b2, lane);
+      b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+      b1 = fmaxf(b1, o1);
+    });
+    const float gs = a.group_top == 2 && a.size > 1 ? b1 + b2 : b1;
+    const bool first = sub == 0 && g < a.groups;
+    const float thr = wave_kth_largest(first && gs == gs ? gs : -INFINITY, a.keep);
+    if (!(fabsf(thr) < INFINITY)) return false;
+    // Twice the error of a sum of two scores, each as large as any of the groups'
+    // best two; by logit, of e^(z - m), whose error is below 2^-16 of it down to
+    // e^-70 (and anything below that counts as near).
+    float err = 0x1p-14f * thr + 1e-30f;
+    if (!by_logit) {
+      float largest = first ? fmaxf(fabsf(b1), a.size > 1 ? fabsf(b2) : 0.0f) : 0.0f;
+      steps(kWaveSize, [&](auto k) { largest = fmaxf(largest, partner<decltype(k)::value>(largest, lane)); });
+      err = 4.0f * (2.0f * base + 3.0f * rel * largest);
+    }
+    kept = __builtin_amdgcn_ballot_w64(first && gs >= thr);
+    const uint64_t near = __builtin_amdgcn_ballot_w64(first && !(gs < thr - err));  // (NaN: near)
+    if (__builtin_popcountll(kept) != a.keep || near != kept) return false;
+  }
+  auto in_kept = [&](int e) { return a.keep == a.groups || ((kept >> (((uint32_t)e * inv_size >> 20) * lanes)) & 1ull) != 0; };
+
+  // Candidates.
+  uint64_t mask[NPER];
+  int total = 0;
+  if (n_kept <= kWaveSize) {
+#pragma unroll
+    for (int j = 0; j < NPER; ++j) {
+      const int e = lane + kWaveSize * j;
+      mask[j] = __builtin_amdgcn_ballot_w64(e < a.E && in_kept(e));
+    }
+    total = n_kept;
+  } else {
+    float best = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < NPER; ++j) {
+      const int e = lane + kWaveSize * j;
+      if (by_logit) s[j] = fmaxf(z[j] - m, -700.0f);
+      if (e >= a.E || !in_kept(e)) s[j] = -INFINITY;
+      best = fmaxf(best, s[j]);
+    }
+    const float thr = wave_kth_largest(best, a.k);
+    if (!(fabsf(thr) < INFINITY)) return false;
+    const float theta = thr - (by_logit ? 0x1p-21f * (1.0f + fabsf(thr)) : 4.0f * (base + rel * (1.0f + fabsf(thr))));
+#pragma unroll
+    for (int j = 0; j < NPER; ++j) {
+      mask[j] = __builtin_amdgcn_ballot_w64(s[j] >= theta);
+      total += __builtin_popcountll(mask[j]);
+    }
+    if (total > kWaveSize) return false;
+  }
+  int slot = 0;
+#pragma unroll
+  for (int j = 0; j < NPER; ++j) {
+    const int below = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask[j], 0u));
+    if ((mask[j] >> lane) & 1ull) {
+      x.fe[slot + below] = lane + kWaveSize * j;
+      x.cz[slot + below] = z[j];
+      x.cb[slot + below] = b[j];
+    }
+    slot += __builtin_popcountll(mask[j]);
+  }
+  wave_fence();
+
+  // The sum of a softmax in fp64, where a gate itself enters a score or a weight.
+  double sum = 1.0;
+  if (a.softmax && (a.bias || !a.normalize)) {
+    sum = 0.0;
+    constexpr int kBatch = NPER < 4 ? NPER : 4;
+#pragma unroll
+    for (int j = 0; j < NPER; j += kBatch) {
+      double d[kBatch], w[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) d[i] = (double)z[j + i] - (double)m;
+      exp_down<kBatch>(d, w);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) sum += lane + kWaveSize * (j + i) < a.E ? w[i] : 0.0;
+    }
+    steps(kWaveSize, [&](auto k) { sum += partner<decltype(k)::value>(sum, lane); });
+  }
+  double cs = -INFINITY, cg = 0.0;
+  int ce = INT_MAX;
+  if (lane < total) {
+    ce = x.fe[lane];
+    cg = a.softmax ? softmax_weight(x.cz[lane], m) / sum : sigmoid64(x.cz[lane]);
+    cs = cg + (double)x.cb[lane];
+    cs = cs == cs ? cs : -INFINITY;
+  }
+  x.fs[lane] = cs;
+  x.fe[lane] = ce;
+  x.tg[lane] = 0.0;
+  wave_fence();
+  // distinct experts, so distinct ranks: the top k are ranks 0 .. k-1 (all eight
+  // entries read first, and the test without branches, so that the reads overlap)
+  int rank = 0;
+  for (int j0 = 0; j0 < total; j0 += 8) {
+    double os[8];
+    int oe[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      os[i] = x.fs[j0 + i];
+      oe[i] = x.fe[j0 + i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rank += (int)((os[i] > cs) | ((os[i] == cs) & (oe[i] < ce)));
+  }
+  if (lane < total && rank < a.k) {
+    x.tg[rank] = cg;
+    x.te[rank] = ce;
+  }
+  wave_fence();
+  double weight_sum = 1.0;
+  if (a.normalize) {  // in rank order (past the k-th the entries are 0, which leaves the sum as it is)
+    weight_sum = 0.0;
+    for (int r0 = 0; r0 < a.k; r0 += 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) weight_sum += x.tg[r0 + i];
+    }
+  }
+  if (lane < a.k) {
+    const double g = x.tg[lane];
+    const double v = a.normalize ? (weight_sum == 0.0 ? 0.0 : g / weight_sum) : g;
+    a.ids[t * a.k + lane] = x.te[lane];
+    a.w[t * a.k + lane] = (float)(v * (double)a.route_scale);
+  }
+  wave_fence();  // all is read before the next token's is written
+  return true;
+}
+
+template <int NPER>
+__global__ __launch_bounds__(256) void route_groups_fast_kernel(GroupsArgs a, int lanes, uint32_t inv_size, int lds_wave) {
+  extern __shared__ double lds_scores[];
+  const int lane = threadIdx.x & (kWaveSize - 1);
+  const int wave = threadIdx.x / kWaveSize;
+  double* const own = lds_scores + (size_t)wave * lds_wave;
+  FastScratch& x = *reinterpret_cast<FastScratch*>(own);
+  float* const score = reinterpret_cast<float*>(own + sizeof(FastScratch) / sizeof(double));
+  const int waves = blockDim.x / kWaveSize;
+  for (int64_t t = (int64_t)blockIdx.x * waves + wave; t < a.T; t += (int64_t)gridDim.x * waves)
+    if (!route_token_fast<NPER>(a, t, lane, lanes, inv_size, x, score)) {
+      wave_fence();
+      route_token(a, t, lane, own, own + a.E);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Any size.
 __global__ __launch_bounds__(256) void route_groups_kernel(GroupsArgs a) {
   extern __shared__ double lds_scores[];
   const int lane = threadIdx.x & (kWaveSize - 1);
@@ -163,6 +454,22 @@ __global__ __launch_bounds__(256) void route_groups_kernel(GroupsArgs a) {
 hipError_t launch_route_groups(const RouteGroupsCall& c, hipStream_t s) {
   GroupsArgs a{c.z, c.bias, c.T, c.E, c.groups, c.E / c.groups, c.keep, c.group_top, c.k, c.softmax, c.normalize, c.route_scale, c.ids, c.w};
   const size_t per_wave = (size_t)(c.E + c.groups) * sizeof(double);
+  if (c.E <= 16 * kWaveSize && c.groups <= kWaveSize) {
+    int lanes = kWaveSize;
+    while (lanes * c.groups > kWaveSize) lanes /= 2;
+    const uint32_t inv_size = ((1u << 20) + a.size - 1) / a.size;
+    size_t fast = sizeof(FastScratch) + (size_t)(c.E + 1) / 2 * sizeof(double);
+    fast = fast > per_wave ? fast : per_wave;
+    const int64_t wgs = (c.T + 3) / 4;
+    const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : 1 << 20));
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(4 * kWaveSize), 4 * fast, s, a, lanes, inv_size, (int)(fast / sizeof(double))); };
+    if (c.E <= kWaveSize) go(route_groups_fast_kernel<1>);
+    else if (c.E <= 2 * kWaveSize) go(route_groups_fast_kernel<2>);
+    else if (c.E <= 4 * kWaveSize) go(route_groups_fast_kernel<4>);
+    else if (c.E <= 8 * kWaveSize) go(route_groups_fast_kernel<8>);
+    else go(route_groups_fast_kernel<16>);
+    return hipGetLastError();
+  }
   constexpr size_t kLdsBudget = 64 * 1024;
   int waves = (int)(kLdsBudget / per_wave);
   waves = waves > 4 ? 4 : waves < 1 ? 1 : waves;
