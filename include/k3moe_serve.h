@@ -125,7 +125,7 @@ int mxfp8_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const uint8_t* 
  * sum is 0), times `route_scale`, rounded once to f32. NaN logits leave the
  * softmax of the others as it is without them; where logits are +inf, they share it
  * equally; where all are -inf, every gate is 0.
- * Sizes: T >= 0 (T == 0 is a no-op), 1 <= E <= K3MOE_MAX_EXPERTS_FFN, groups
+ * Sizes: 0 <= T <= 2^36 (T == 0 is a no-op), 1 <= E <= K3MOE_MAX_EXPERTS_FFN, groups
  * >= 1 divides E, 1 <= topk_groups <= groups, 1 <= k <= min(K3MOE_MAX_TOPK,
  * topk_groups * E / groups); K3MOE_ERR_SHAPE otherwise. Unknown score, or a
  * group_top other than 1 and 2: K3MOE_ERR_UNSUPPORTED.

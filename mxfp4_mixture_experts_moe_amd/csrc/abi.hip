@@ -1140,7 +1140,7 @@ int mxfp8_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const uint8_t* 
 int moe_route_groups(const float* logits, const float* bias, int64_t T, int32_t E, int32_t groups, int32_t topk_groups,
                      int32_t group_top, int32_t k, int32_t score, int32_t normalize, float route_scale,
                      int32_t* topk_ids, float* topk_w, void* stream) {
-  if (T < 0 || T > ((int64_t)1 << 40) || E < 1 || E > K3MOE_MAX_EXPERTS_FFN || groups < 1 || groups > E ||
+  if (T < 0 || T > ((int64_t)1 << 36) || E < 1 || E > K3MOE_MAX_EXPERTS_FFN || groups < 1 || groups > E ||
       E % groups != 0 || topk_groups < 1 || topk_groups > groups || k < 1 || k > K3MOE_MAX_TOPK ||
       k > topk_groups * (E / groups))
     return K3MOE_ERR_SHAPE;

@@ -273,7 +273,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
   const float rel = a.softmax ? 0x1p-22f : 0x1p-21f, base = (a.softmax ? 0x1p-16f : 0x1p-21f) * top;  // |error of s| <= base + rel |s|
 
   // The kept groups, a bit per group's first lane.
-  uint64_t kept = 0;
+  uint64_t kept = ~0ull;
   const int n_kept = a.keep * a.size;
   if (a.keep < a.groups) {
 #pragma unroll
@@ -310,7 +310,11 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
     const uint64_t near = __builtin_amdgcn_ballot_w64(first && !(gs < thr - err));  // (NaN: near)
     if (__builtin_popcountll(kept) != a.keep || near != kept) return false;
   }
-  auto in_kept = [&](int e) { return a.keep == a.groups || ((kept >> (((uint32_t)e * inv_size >> 20) * lanes)) & 1ull) != 0; };
+  // An expert of a kept group, without a branch.
+  auto in_kept = [&](int e) -> bool {
+    const uint32_t bit = ((uint32_t)e * inv_size >> 20) * (uint32_t)lanes;
+    return (uint32_t)((e < a.E) & (int)(kept >> (bit & 63u))) != 0;
+  };
 
   // Candidates.
   uint64_t mask[NPER];
@@ -319,7 +323,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
 #pragma unroll
     for (int j = 0; j < NPER; ++j) {
       const int e = lane + kWaveSize * j;
-      mask[j] = __builtin_amdgcn_ballot_w64(e < a.E && in_kept(e));
+      mask[j] = __builtin_amdgcn_ballot_w64(in_kept(e));
     }
     total = n_kept;
   } else {
@@ -327,8 +331,8 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
 #pragma unroll
     for (int j = 0; j < NPER; ++j) {
       const int e = lane + kWaveSize * j;
-      if (by_logit) s[j] = fmaxf(z[j] - m, -700.0f);
-      if (e >= a.E || !in_kept(e)) s[j] = -INFINITY;
+      const float v = by_logit ? fmaxf(z[j] - m, -700.0f) : s[j];
+      s[j] = in_kept(e) ? v : -INFINITY;
       best = fmaxf(best, s[j]);
     }
     const float thr = wave_kth_largest(best, a.k);
@@ -415,7 +419,6 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
     a.ids[t * a.k + lane] = x.te[lane];
     a.w[t * a.k + lane] = (float)(v * (double)a.route_scale);
   }
-  wave_fence();  // all is read before the next token's is written
   return true;
 }
 
@@ -427,12 +430,12 @@ __global__ __launch_bounds__(256) void route_groups_fast_kernel(GroupsArgs a, in
   double* const own = lds_scores + (size_t)wave * lds_wave;
   FastScratch& x = *reinterpret_cast<FastScratch*>(own);
   float* const score = reinterpret_cast<float*>(own + sizeof(FastScratch) / sizeof(double));
-  const int waves = blockDim.x / kWaveSize;
-  for (int64_t t = (int64_t)blockIdx.x * waves + wave; t < a.T; t += (int64_t)gridDim.x * waves)
-    if (!route_token_fast<NPER>(a, t, lane, lanes, inv_size, x, score)) {
-      wave_fence();
-      route_token(a, t, lane, own, own + a.E);
-    }
+  const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + wave;
+  if (t >= a.T) return;  // (a wave's token; the kernel has no block-level barrier)
+  if (!route_token_fast<NPER>(a, t, lane, lanes, inv_size, x, score)) {
+    wave_fence();
+    route_token(a, t, lane, own, own + a.E);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -460,8 +463,8 @@ hipError_t launch_route_groups(const RouteGroupsCall& c, hipStream_t s) {
     const uint32_t inv_size = ((1u << 20) + a.size - 1) / a.size;
     size_t fast = sizeof(FastScratch) + (size_t)(c.E + 1) / 2 * sizeof(double);
     fast = fast > per_wave ? fast : per_wave;
-    const int64_t wgs = (c.T + 3) / 4;
-    const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : 1 << 20));
+    const int64_t wgs = (c.T + 3) / 4, wide = wgs < (1 << 20) ? wgs : 1 << 20;  // (a grid dimension has fewer than 2^32 threads)
+    const dim3 grid((unsigned)wide, (unsigned)((wgs + wide - 1) / wide));
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(4 * kWaveSize), 4 * fast, s, a, lanes, inv_size, (int)(fast / sizeof(double))); };
     if (c.E <= kWaveSize) go(route_groups_fast_kernel<1>);
     else if (c.E <= 2 * kWaveSize) go(route_groups_fast_kernel<2>);
