@@ -226,17 +226,28 @@ struct FastScratch {
   float cz[kWaveSize], cb[kWaveSize];
 };
 
-// Routes token t from registers; false where fp32 is not sure.  lanes: of a group
-// (a power of two, lanes * groups <= 64); inv_size: ceil(2^20 / size), which
+// Routes token t from registers; false where fp32 is not sure.  A group has 2^shift
+// lanes, 2^shift * groups <= 64; inv_size: ceil(2^20 / size), which
 // divides every index below 1024 by size exactly.
 template <int NPER>
-__device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t, int lane, int lanes, uint32_t inv_size, FastScratch& x, float* score) {
-  const float* const zt = a.z + t * (int64_t)a.E;
+__device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t, int lane, int shift, uint32_t inv_size, FastScratch& x, float* score) {
+  const int lanes = 1 << shift;
+  // (a buffer ends with the token's row: what lies past it costs no address arithmetic and reads as zeros)
+  const uint32_t at = 4u * (uint32_t)lane, bytes = 4u * (uint32_t)a.E;
+  const __amdgpu_buffer_rsrc_t zr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.z + t * (int64_t)a.E), 0, (int)bytes, 0x00020000);
   float z[NPER], b[NPER];
 #pragma unroll
-  for (int j = 0; j < NPER; ++j) z[j] = zt[min(lane + kWaveSize * j, a.E - 1)];
+  for (int j = 0; j < NPER; ++j) z[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(zr, at + 256u * j, 0, 0));
+  if (a.bias) {
+    const __amdgpu_buffer_rsrc_t br = __builtin_amdgcn_make_buffer_rsrc((void*)a.bias, 0, (int)bytes, 0x00020000);
 #pragma unroll
-  for (int j = 0; j < NPER; ++j) b[j] = a.bias ? a.bias[min(lane + kWaveSize * j, a.E - 1)] : 0.0f;
+    for (int j = 0; j < NPER; ++j) b[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(br, at + 256u * j, 0, 0));
+  } else {
+#pragma unroll
+    for (int j = 0; j < NPER; ++j) b[j] = 0.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < NPER; ++j) z[j] = lane + kWaveSize * j < a.E ? z[j] : -INFINITY;
 
   // fp32 scores s, of experts past E -inf, and what groups add up (gs).  u = 2^-24:
   //   sigmoid: off by at most 2^-21 (1 + |s|) (route_device.h).
@@ -250,14 +261,14 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
   if (a.softmax) {
     m = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NPER; ++j) m = fmaxf(m, z[j]);  // (passes over NaN; an expert seen twice does no harm)
+    for (int j = 0; j < NPER; ++j) m = fmaxf(m, z[j]);  // (passes over NaN)
     steps(kWaveSize, [&](auto k) { m = fmaxf(m, partner<decltype(k)::value>(m, lane)); });
     if (!(fabsf(m) < INFINITY)) return false;
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NPER; ++j) {
       s[j] = __builtin_amdgcn_exp2f((z[j] - m) * 1.44269504088896341f);
-      sum += lane + kWaveSize * j < a.E ? s[j] : 0.0f;
+      sum += s[j];  // (past E: 0)
     }
     steps(kWaveSize, [&](auto k) { sum += partner<decltype(k)::value>(sum, lane); });
     if (!(sum < INFINITY)) return false;  // (NaN)
@@ -312,20 +323,20 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
   }
   // An expert of a kept group, without a branch.
   auto in_kept = [&](int e) -> bool {
-    const uint32_t bit = ((uint32_t)e * inv_size >> 20) * (uint32_t)lanes;
-    return (uint32_t)((e < a.E) & (int)(kept >> (bit & 63u))) != 0;
+    const uint32_t g = __umul24((uint32_t)e, inv_size) >> 20;
+    return ((e < a.E) & (int)(kept >> ((g << shift) & 63u))) != 0;
   };
 
-  // Candidates.
+  // Candidates: s[j] >= theta.
+  float theta = 0.0f;
   uint64_t mask[NPER];
   int total = 0;
   if (n_kept <= kWaveSize) {
 #pragma unroll
     for (int j = 0; j < NPER; ++j) {
       const int e = lane + kWaveSize * j;
-      mask[j] = __builtin_amdgcn_ballot_w64(in_kept(e));
+      s[j] = in_kept(e) ? 1.0f : -1.0f;
     }
-    total = n_kept;
   } else {
     float best = -INFINITY;
 #pragma unroll
@@ -337,19 +348,19 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
     }
     const float thr = wave_kth_largest(best, a.k);
     if (!(fabsf(thr) < INFINITY)) return false;
-    const float theta = thr - (by_logit ? 0x1p-21f * (1.0f + fabsf(thr)) : 4.0f * (base + rel * (1.0f + fabsf(thr))));
-#pragma unroll
-    for (int j = 0; j < NPER; ++j) {
-      mask[j] = __builtin_amdgcn_ballot_w64(s[j] >= theta);
-      total += __builtin_popcountll(mask[j]);
-    }
-    if (total > kWaveSize) return false;
+    theta = thr - (by_logit ? 0x1p-21f * (1.0f + fabsf(thr)) : 4.0f * (base + rel * (1.0f + fabsf(thr))));
   }
+#pragma unroll
+  for (int j = 0; j < NPER; ++j) {
+    mask[j] = __builtin_amdgcn_ballot_w64(s[j] >= theta);
+    total += __builtin_popcountll(mask[j]);
+  }
+  if (total > kWaveSize) return false;
   int slot = 0;
 #pragma unroll
   for (int j = 0; j < NPER; ++j) {
     const int below = __builtin_amdgcn_mbcnt_hi((uint32_t)(mask[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask[j], 0u));
-    if ((mask[j] >> lane) & 1ull) {
+    if (s[j] >= theta) {
       x.fe[slot + below] = lane + kWaveSize * j;
       x.cz[slot + below] = z[j];
       x.cb[slot + below] = b[j];
@@ -370,7 +381,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
       for (int i = 0; i < kBatch; ++i) d[i] = (double)z[j + i] - (double)m;
       exp_down<kBatch>(d, w);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) sum += lane + kWaveSize * (j + i) < a.E ? w[i] : 0.0;
+      for (int i = 0; i < kBatch; ++i) sum += w[i];  // (past E: 0)
     }
     steps(kWaveSize, [&](auto k) { sum += partner<decltype(k)::value>(sum, lane); });
   }
@@ -423,7 +434,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
 }
 
 template <int NPER>
-__global__ __launch_bounds__(256) void route_groups_fast_kernel(GroupsArgs a, int lanes, uint32_t inv_size, int lds_wave) {
+__global__ __launch_bounds__(256) void route_groups_fast_kernel(GroupsArgs a, int shift, uint32_t inv_size, int lds_wave) {
   extern __shared__ double lds_scores[];
   const int lane = threadIdx.x & (kWaveSize - 1);
   const int wave = threadIdx.x / kWaveSize;
@@ -432,7 +443,7 @@ __global__ __launch_bounds__(256) void route_groups_fast_kernel(GroupsArgs a, in
   float* const score = reinterpret_cast<float*>(own + sizeof(FastScratch) / sizeof(double));
   const int64_t t = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 4 + wave;
   if (t >= a.T) return;  // (a wave's token; the kernel has no block-level barrier)
-  if (!route_token_fast<NPER>(a, t, lane, lanes, inv_size, x, score)) {
+  if (!route_token_fast<NPER>(a, t, lane, shift, inv_size, x, score)) {
     wave_fence();
     route_token(a, t, lane, own, own + a.E);
   }
@@ -458,14 +469,14 @@ hipError_t launch_route_groups(const RouteGroupsCall& c, hipStream_t s) {
   GroupsArgs a{c.z, c.bias, c.T, c.E, c.groups, c.E / c.groups, c.keep, c.group_top, c.k, c.softmax, c.normalize, c.route_scale, c.ids, c.w};
   const size_t per_wave = (size_t)(c.E + c.groups) * sizeof(double);
   if (c.E <= 16 * kWaveSize && c.groups <= kWaveSize) {
-    int lanes = kWaveSize;
-    while (lanes * c.groups > kWaveSize) lanes /= 2;
+    int shift = 6;
+    while (c.groups << shift > kWaveSize) --shift;
     const uint32_t inv_size = ((1u << 20) + a.size - 1) / a.size;
     size_t fast = sizeof(FastScratch) + (size_t)(c.E + 1) / 2 * sizeof(double);
     fast = fast > per_wave ? fast : per_wave;
     const int64_t wgs = (c.T + 3) / 4, wide = wgs < (1 << 20) ? wgs : 1 << 20;  // (a grid dimension has fewer than 2^32 threads)
     const dim3 grid((unsigned)wide, (unsigned)((wgs + wide - 1) / wide));
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(4 * kWaveSize), 4 * fast, s, a, lanes, inv_size, (int)(fast / sizeof(double))); };
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(4 * kWaveSize), 4 * fast, s, a, shift, inv_size, (int)(fast / sizeof(double))); };
     if (c.E <= kWaveSize) go(route_groups_fast_kernel<1>);
     else if (c.E <= 2 * kWaveSize) go(route_groups_fast_kernel<2>);
     else if (c.E <= 4 * kWaveSize) go(route_groups_fast_kernel<4>);
