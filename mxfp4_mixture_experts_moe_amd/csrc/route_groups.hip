@@ -59,17 +59,37 @@ __device__ __forceinline__ double gate64(float z, int softmax, const SoftmaxStat
   return softmax ? softmax_weight(z, st.m) / st.sum : sigmoid64(z);
 }
 
-// Best (s, e) of the wave, in every lane.
-__device__ __forceinline__ void best_of_wave(double& s, int& e) {
-#pragma unroll
-  for (int m = 1; m < kWaveSize; m <<= 1) {
-    const double os = __shfl_xor(s, m, kWaveSize);
-    const int oe = __shfl_xor(e, m, kWaveSize);
-    if (ranks_before(os, oe, s, e)) {
-      s = os;
-      e = oe;
-    }
-  }
+// Value of the lane that step k (0 .. 5) of a reduction exchanges with.
+template <int k>
+__device__ __forceinline__ uint32_t partner(uint32_t v, int lane) {
+  if constexpr (k == 0) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);        // lane ^ 1
+  else if constexpr (k == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false);   // lane ^ 2
+  else if constexpr (k == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false);  // mirrored in its half row
+  else if constexpr (k == 3) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false);  // mirrored in its row
+  else return swap_rows<k == 4 ? 16 : 32>(v, lane);
+}
+template <int k>
+__device__ __forceinline__ float partner(float v, int lane) { return __uint_as_float(partner<k>(__float_as_uint(v), lane)); }
+template <int k>
+__device__ __forceinline__ double partner(double v, int lane) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)partner<k>((uint32_t)(b >> 32), lane) << 32 | partner<k>((uint32_t)b, lane)));
+}
+// f(k) for the first log2(count) steps: lanes l / count apart stay apart (steps 2
+// and 3 mirror, after which the lanes of 8 and of 16 agree all the same).
+template <typename F>
+__device__ __forceinline__ void steps(int count, F&& f) {
+  if (count > 1) f(std::integral_constant<int, 0>{});
+  if (count > 2) f(std::integral_constant<int, 1>{});
+  if (count > 4) f(std::integral_constant<int, 2>{});
+  if (count > 8) f(std::integral_constant<int, 3>{});
+  if (count > 16) f(std::integral_constant<int, 4>{});
+  if (count > 32) f(std::integral_constant<int, 5>{});
+}
+
+// ranks_before without a branch.
+__device__ __forceinline__ bool before(double sa, int ea, double sb, int eb) {
+  return ((int)(sa > sb) | ((int)(sa == sb) & (int)(ea < eb))) != 0;
 }
 
 // The entry of a[0 .. n-1] that ranks best among those strictly after (ps, pe);
@@ -77,59 +97,93 @@ __device__ __forceinline__ void best_of_wave(double& s, int& e) {
 __device__ __forceinline__ void best_after(const double* a, int n, int lane, double& ps, int& pe) {
   double bs = -INFINITY;
   int be = INT_MAX;  // sentinel: ranks after every real entry
-  for (int i = lane; i < n; i += kWaveSize) {
-    const double v = a[i];
-    if (ranks_before(ps, pe, v, i) && ranks_before(v, i, bs, be)) {
-      bs = v;
-      be = i;
+  for (int i0 = lane; i0 < n; i0 += 4 * kWaveSize) {
+    double v[4];  // (read together; past the end the last entry again)
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = a[min(i0 + u * kWaveSize, n - 1)];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = min(i0 + u * kWaveSize, n - 1);
+      const bool take = ((int)before(ps, pe, v[u], i) & (int)before(v[u], i, bs, be)) != 0;
+      bs = take ? v[u] : bs;
+      be = take ? i : be;
     }
   }
-  best_of_wave(bs, be);
+  steps(kWaveSize, [&](auto k) {
+    const double os = partner<decltype(k)::value>(bs, lane);
+    const int oe = (int)partner<decltype(k)::value>((uint32_t)be, lane);
+    const bool take = before(os, oe, bs, be);
+    bs = take ? os : bs;
+    be = take ? oe : be;
+  });
   ps = bs;
   pe = be;
 }
 
+// Best two of the two best (b1 >= b2) seen here and (o1 >= o2) elsewhere.
+__device__ __forceinline__ void best_two(double& b1, double& b2, double o1, double o2) {
+  b2 = fmax(fmin(b1, o1), fmax(b2, o2));
+  b1 = fmax(b1, o1);
+}
+
 __device__ __forceinline__ void route_token(const GroupsArgs& a, int64_t t, int lane, double* s, double* gs) {
   const float* const zt = a.z + t * (int64_t)a.E;
+  // Experts e, e + 64, .. of the lane two at a time (their loads and exponentials
+  // overlap); past the end the last one again, not counted.
+  auto experts = [&](auto&& f) {
+    for (int e0 = lane; e0 < a.E; e0 += 2 * kWaveSize) {
+      float z[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) z[u] = zt[min(e0 + u * kWaveSize, a.E - 1)];
+      f(e0, z);
+    }
+  };
   SoftmaxStats st{0.0f, 1.0};
   if (a.softmax) {
     float m = -INFINITY;
-    for (int e = lane; e < a.E; e += kWaveSize) m = fmaxf(m, zt[e]);  // (passes over NaN)
-#pragma unroll
-    for (int d = 1; d < kWaveSize; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, kWaveSize));
+    experts([&](int, const float (&z)[2]) { m = fmaxf(m, fmaxf(z[0], z[1])); });  // (passes over NaN)
+    steps(kWaveSize, [&](auto k) { m = fmaxf(m, partner<decltype(k)::value>(m, lane)); });
     double sum = 0.0;
-    for (int e = lane; e < a.E; e += kWaveSize) {
-      const double v = softmax_weight(zt[e], m);
-      sum += v == v ? v : 0.0;
-    }
+    experts([&](int e0, const float (&z)[2]) {
+      double v[2];
 #pragma unroll
-    for (int d = 1; d < kWaveSize; d <<= 1) sum += __shfl_xor(sum, d, kWaveSize);
+      for (int u = 0; u < 2; ++u) v[u] = softmax_weight(z[u], m);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) sum += v[u] == v[u] && e0 + u * kWaveSize < a.E ? v[u] : 0.0;
+    });
+    steps(kWaveSize, [&](auto k) { sum += partner<decltype(k)::value>(sum, lane); });
     st = SoftmaxStats{m, sum > 0.0 ? sum : 1.0};
   }
-  for (int e = lane; e < a.E; e += kWaveSize) {
-    const double v = gate64(zt[e], a.softmax, st) + (a.bias ? (double)a.bias[e] : 0.0);
-    s[e] = v == v ? v : -INFINITY;
-  }
+  experts([&](int e0, const float (&z)[2]) {
+    double v[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) v[u] = gate64(z[u], a.softmax, st) + (a.bias ? (double)a.bias[min(e0 + u * kWaveSize, a.E - 1)] : 0.0);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      if (e0 + u * kWaveSize < a.E) s[e0 + u * kWaveSize] = v[u] == v[u] ? v[u] : -INFINITY;
+  });
   wave_fence();
 
   if (a.keep < a.groups) {
-    for (int g = lane; g < a.groups; g += kWaveSize) {
+    int shift = 0;  // 2^shift lanes per group, as many groups at a time as that leaves
+    while (shift < 6 && (int64_t)a.groups << (shift + 1) <= kWaveSize) ++shift;
+    for (int g0 = 0; g0 < a.groups; g0 += kWaveSize >> shift) {
+      const int g = g0 + (lane >> shift);
       double b1 = -INFINITY, b2 = -INFINITY;
-      for (int i = 0; i < a.size; ++i) {
-        const double v = s[g * a.size + i];
-        b2 = v > b1 ? b1 : fmax(b2, v);
-        b1 = fmax(b1, v);
-      }
+      if (g < a.groups)
+        for (int i = lane & ((1 << shift) - 1); i < a.size; i += 1 << shift) best_two(b1, b2, s[g * a.size + i], -INFINITY);
+      for (int d = 1; d < 1 << shift; d <<= 1) best_two(b1, b2, __shfl_xor(b1, d, kWaveSize), __shfl_xor(b2, d, kWaveSize));
       const double sum = a.group_top == 2 && a.size > 1 ? b1 + b2 : b1;
-      gs[g] = sum == sum ? sum : -INFINITY;  // (infinities of both signs)
+      if (g < a.groups && (lane & ((1 << shift) - 1)) == 0) gs[g] = sum == sum ? sum : -INFINITY;  // (infinities of both signs)
     }
     wave_fence();
     double ls = INFINITY;
     int le = -1;  // nothing ranks before (+inf, -1)
     for (int r = 0; r < a.keep; ++r) best_after(gs, a.groups, lane, ls, le);
-    for (int g = lane; g < a.groups; g += kWaveSize)
-      if (ranks_before(ls, le, gs[g], g))  // after the last one kept
-        for (int i = 0; i < a.size; ++i) s[g * a.size + i] = NAN;
+    for (int e = lane; e < a.E; e += kWaveSize) {
+      const int g = e / a.size;
+      if (ranks_before(ls, le, gs[g], g)) s[e] = NAN;  // after the last one kept
+    }
     wave_fence();
   }
 
@@ -188,34 +242,6 @@ __device__ __forceinline__ void exp_down(const double (&d)[n], double (&w)[n]) {
     for (int i = 0; i < n; ++i) w[i] = fma_scalar(w[i], f[i], kP[k]);
 #pragma unroll
   for (int i = 0; i < n; ++i) w[i] = ldexp(w[i], e[i]);
-}
-
-// Value of the lane that step k (0 .. 5) of a reduction exchanges with.
-template <int k>
-__device__ __forceinline__ uint32_t partner(uint32_t v, int lane) {
-  if constexpr (k == 0) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, false);        // lane ^ 1
-  else if constexpr (k == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, false);   // lane ^ 2
-  else if constexpr (k == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, false);  // mirrored in its half row
-  else if constexpr (k == 3) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, false);  // mirrored in its row
-  else return swap_rows<k == 4 ? 16 : 32>(v, lane);
-}
-template <int k>
-__device__ __forceinline__ float partner(float v, int lane) { return __uint_as_float(partner<k>(__float_as_uint(v), lane)); }
-template <int k>
-__device__ __forceinline__ double partner(double v, int lane) {
-  const uint64_t b = (uint64_t)__double_as_longlong(v);
-  return __longlong_as_double((long long)((uint64_t)partner<k>((uint32_t)(b >> 32), lane) << 32 | partner<k>((uint32_t)b, lane)));
-}
-// f(k) for the first log2(count) steps: lanes l / count apart stay apart (steps 2
-// and 3 mirror, after which the lanes of 8 and of 16 agree all the same).
-template <typename F>
-__device__ __forceinline__ void steps(int count, F&& f) {
-  if (count > 1) f(std::integral_constant<int, 0>{});
-  if (count > 2) f(std::integral_constant<int, 1>{});
-  if (count > 4) f(std::integral_constant<int, 2>{});
-  if (count > 8) f(std::integral_constant<int, 3>{});
-  if (count > 16) f(std::integral_constant<int, 4>{});
-  if (count > 32) f(std::integral_constant<int, 5>{});
 }
 
 // LDS of a wave: candidates' fp64 score, gate and expert, their logits and
@@ -309,17 +335,67 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
     const float thr = wave_kth_largest(first && gs == gs ? gs : -INFINITY, a.keep);
     if (!(fabsf(thr) < INFINITY)) return false;
     // Twice the error of a sum of two scores, each as large as any of the groups'
-    // best two; by logit, of e^(z - m), whose error is below 2^-16 of it down to
-    // e^-70 (and anything below that counts as near).
-    float err = 0x1p-14f * thr + 1e-30f;
-    if (!by_logit) {
+    // best two; by logit, of e^(z - m), off by less than (2 |z - m| + 4) u of itself
+    // where it is not below 2^-100 (and anything below 1e-30 counts as near).
+    float err, one;  // .. and of one score
+    if (by_logit) {
+      err = one = thr * 0x1p-21f * (2.0f + fabsf(__builtin_amdgcn_logf(thr))) + 1e-30f;
+    } else {
       float largest = first ? fmaxf(fabsf(b1), a.size > 1 ? fabsf(b2) : 0.0f) : 0.0f;
       steps(kWaveSize, [&](auto k) { largest = fmaxf(largest, partner<decltype(k)::value>(largest, lane)); });
+      one = 4.0f * (base + rel * largest);
       err = 4.0f * (2.0f * base + 3.0f * rel * largest);
     }
     kept = __builtin_amdgcn_ballot_w64(first && gs >= thr);
     const uint64_t near = __builtin_amdgcn_ballot_w64(first && !(gs < thr - err));  // (NaN: near)
-    if (__builtin_popcountll(kept) != a.keep || near != kept) return false;
+    if (__builtin_popcountll(kept) != a.keep || near != kept) {
+      // Groups too near to the threshold for fp32: their scores in fp64, from their
+      // best two experts, if it is sure which these are.
+      const uint64_t above = __builtin_amdgcn_ballot_w64(first && gs > thr + err);
+      if (by_logit && !(thr > 1e-20f)) return false;
+      float t1 = -INFINITY, t2 = -INFINITY, t3 = -INFINITY;
+      int i1 = 0, i2 = 0;
+      if (first)
+        for (int i = g * a.size; i < (g + 1) * a.size; ++i) {
+          const float v = score[i];
+          if (v > t1) {
+            t3 = t2;
+            t2 = t1;
+            i2 = i1;
+            t1 = v;
+            i1 = i;
+          } else if (v > t2) {
+            t3 = t2;
+            t2 = v;
+            i2 = i;
+          } else {
+            t3 = fmaxf(t3, v);
+          }
+        }
+      const bool two = a.group_top == 2 && a.size > 1;
+      const bool mine = ((near & ~above) >> lane) & 1ull;
+      const float last = two ? t2 : t1, next = two ? t3 : t2;
+      if (__builtin_amdgcn_ballot_w64(mine && !(next < last - one)) != 0) return false;
+      double all = 1.0;
+      if (a.softmax && a.bias) {
+        all = 0.0;
+        for (int e = lane; e < a.E; e += kWaveSize) all += softmax_weight(a.z[t * (int64_t)a.E + e], m);
+        steps(kWaveSize, [&](auto k) { all += partner<decltype(k)::value>(all, lane); });
+      }
+      auto exact = [&](int e) {
+        const float ze = a.z[t * (int64_t)a.E + e];
+        return (a.softmax ? softmax_weight(ze, m) / all : sigmoid64(ze)) + (a.bias ? (double)a.bias[e] : 0.0);
+      };
+      double gd = exact(i1);
+      if (two) gd += exact(i2);
+      int rank = __builtin_popcountll(above);  // among the near ones, behind those above
+      for (uint64_t rest = near & ~above; rest != 0; rest &= rest - 1) {
+        const int l = __builtin_ctzll(rest);
+        rank += ranks_before(readlane_f64(gd, l), l, gd, lane) ? 1 : 0;
+      }
+      kept = above | __builtin_amdgcn_ballot_w64(mine && rank < a.keep);
+      if (__builtin_popcountll(kept) != a.keep) return false;
+    }
   }
   // An expert of a kept group, without a branch.
   auto in_kept = [&](int e) -> bool {
