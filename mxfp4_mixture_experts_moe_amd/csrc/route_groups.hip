@@ -13,12 +13,12 @@
 // groups that come within the error of the k-th best lane's best, at most 64,
 // are scored in fp64 and ranked by counting.  Without a bias a softmax's experts
 // are compared by their logits, which fp32 holds exactly.
-// What fp32 is not sure of (heavy ties, values that are no numbers, masked rows)
-// and larger sizes go the plain way: the fp64 scores of a token lie in LDS ([E])
-// beside those of its groups ([groups]); the last of the kept groups is found by
-// `keep` rounds of the best group that ranks strictly after the one before,
-// which needs no flags; experts of the other groups are marked with NaN (NaN
-// scores themselves have become -inf by then), and k such rounds take the experts.
+// What fp32 is not sure of (heavy ties, values that are no numbers, masked rows:
+// about 25 us for such a token of 896) and larger sizes go the plain way: the
+// fp64 scores of a token lie in LDS ([E]) beside those of its groups
+// ([groups]); experts of the groups that are not kept are marked with NaN (NaN
+// scores themselves have become -inf by then), and top_of() takes the best, of
+// groups as of experts.
 #include "route_device.h"
 
 #include <type_traits>
@@ -120,13 +120,66 @@ __device__ __forceinline__ void best_after(const double* a, int n, int lane, dou
   pe = be;
 }
 
+// The k entries of a[0 .. n-1] that rank best, NaN entries apart, the r-th in lane
+// r (k <= 64, and at least k entries are numbers).  Of the 64 lanes' best entries the
+// k-th ranks at or after every one of the top k, so these are among the entries
+// that rank at or before it: mostly few more than k, which are compacted into `few`
+// and sorted; with more than 64, k rounds of best_after.
+struct Few {
+  double s[kWaveSize];
+  int e[kWaveSize];
+};
+__device__ __forceinline__ int top_of(const double* a, int n, int k, int lane, Few& few) {
+  double bs = -INFINITY;
+  int be = INT_MAX;  // sentinel: ranks after every real entry
+  for (int i = lane; i < n; i += kWaveSize) {
+    const double v = a[i];
+    const bool take = before(v, i, bs, be);
+    bs = take ? v : bs;
+    be = take ? i : be;
+  }
+  if (n > kWaveSize) {
+    wave_sort64(bs, be, lane);
+    const double ts = readlane_f64(bs, k - 1);
+    const int te = __builtin_amdgcn_readlane(be, k - 1);
+    int total = 0;
+    for (int i0 = 0; i0 < n; i0 += kWaveSize) {
+      const int i = i0 + lane;
+      const double v = i < n ? a[i] : NAN;
+      const bool in = ((int)before(v, i, ts, te) | ((int)(v == ts) & (int)(i == te))) != 0;
+      const uint64_t mask = __builtin_amdgcn_ballot_w64(in);
+      const int slot = total + (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+      if (in && slot < kWaveSize) {
+        few.s[slot] = v;
+        few.e[slot] = i;
+      }
+      total += __builtin_popcountll(mask);
+    }
+    wave_fence();
+    if (total > kWaveSize) {
+      double ps = INFINITY;
+      int pe = -1, id = 0;
+      for (int r = 0; r < k; ++r) {
+        best_after(a, n, lane, ps, pe);
+        if (lane == r) id = pe;
+      }
+      return id;
+    }
+    bs = lane < total ? few.s[lane] : -INFINITY;
+    be = lane < total ? few.e[lane] : INT_MAX;
+  }
+  wave_sort64(bs, be, lane);
+  return be;
+}
+
 // Best two of the two best (b1 >= b2) seen here and (o1 >= o2) elsewhere.
 __device__ __forceinline__ void best_two(double& b1, double& b2, double o1, double o2) {
   b2 = fmax(fmin(b1, o1), fmax(b2, o2));
   b1 = fmax(b1, o1);
 }
 
-__device__ __forceinline__ void route_token(const GroupsArgs& a, int64_t t, int lane, double* s, double* gs) {
+__device__ __forceinline__ void route_token(const GroupsArgs& a, int64_t t, int lane, Few& few, double* s) {
+  double* const gs = s + a.E;
   const float* const zt = a.z + t * (int64_t)a.E;
   // Experts e, e + 64, .. of the lane two at a time (their loads and exponentials
   // overlap); past the end the last one again, not counted.
@@ -177,9 +230,14 @@ __device__ __forceinline__ void route_token(const GroupsArgs& a, int64_t t, int 
       if (g < a.groups && (lane & ((1 << shift) - 1)) == 0) gs[g] = sum == sum ? sum : -INFINITY;  // (infinities of both signs)
     }
     wave_fence();
-    double ls = INFINITY;
-    int le = -1;  // nothing ranks before (+inf, -1)
-    for (int r = 0; r < a.keep; ++r) best_after(gs, a.groups, lane, ls, le);
+    double ls = INFINITY;  // the last group kept
+    int le = -1;           // (nothing ranks before (+inf, -1))
+    if (a.keep <= kWaveSize) {
+      le = __builtin_amdgcn_readlane(top_of(gs, a.groups, a.keep, lane, few), a.keep - 1);
+      ls = gs[le];
+    } else {
+      for (int r = 0; r < a.keep; ++r) best_after(gs, a.groups, lane, ls, le);
+    }
     for (int e = lane; e < a.E; e += kWaveSize) {
       const int g = e / a.size;
       if (ranks_before(ls, le, gs[g], g)) s[e] = NAN;  // after the last one kept
@@ -187,12 +245,7 @@ __device__ __forceinline__ void route_token(const GroupsArgs& a, int64_t t, int 
     wave_fence();
   }
 
-  double ps = INFINITY;
-  int pe = -1, id = 0;
-  for (int r = 0; r < a.k; ++r) {
-    best_after(s, a.E, lane, ps, pe);
-    if (lane == r) id = pe;
-  }
+  const int id = top_of(s, a.E, a.k, lane, few);
   double g = 0.0;
   if (lane < a.k) g = gate64(zt[id], a.softmax, st);
   double sum = 1.0;
@@ -521,7 +574,7 @@ __global__ __launch_bounds__(256) void route_groups_fast_kernel(GroupsArgs a, in
   if (t >= a.T) return;  // (a wave's token; the kernel has no block-level barrier)
   if (!route_token_fast<NPER>(a, t, lane, shift, inv_size, x, score)) {
     wave_fence();
-    route_token(a, t, lane, own, own + a.E);
+    route_token(a, t, lane, *reinterpret_cast<Few*>(own), own + sizeof(Few) / sizeof(double));
   }
 }
 
@@ -531,19 +584,18 @@ __global__ __launch_bounds__(256) void route_groups_kernel(GroupsArgs a) {
   extern __shared__ double lds_scores[];
   const int lane = threadIdx.x & (kWaveSize - 1);
   const int wave = threadIdx.x / kWaveSize;
-  double* const s = lds_scores + (size_t)wave * (a.E + a.groups);
-  double* const gs = s + a.E;
+  double* const own = lds_scores + (size_t)wave * (sizeof(Few) / sizeof(double) + a.E + a.groups);
   const int waves = blockDim.x / kWaveSize;
   // (a wave's tokens; the kernel has no block-level barrier)
   for (int64_t t = (int64_t)blockIdx.x * waves + wave; t < a.T; t += (int64_t)gridDim.x * waves)
-    route_token(a, t, lane, s, gs);
+    route_token(a, t, lane, *reinterpret_cast<Few*>(own), own + sizeof(Few) / sizeof(double));
 }
 
 }  // namespace
 
 hipError_t launch_route_groups(const RouteGroupsCall& c, hipStream_t s) {
   GroupsArgs a{c.z, c.bias, c.T, c.E, c.groups, c.E / c.groups, c.keep, c.group_top, c.k, c.softmax, c.normalize, c.route_scale, c.ids, c.w};
-  const size_t per_wave = (size_t)(c.E + c.groups) * sizeof(double);
+  const size_t per_wave = sizeof(Few) + (size_t)(c.E + c.groups) * sizeof(double);
   if (c.E <= 16 * kWaveSize && c.groups <= kWaveSize) {
     int shift = 6;
     while (c.groups << shift > kWaveSize) --shift;
