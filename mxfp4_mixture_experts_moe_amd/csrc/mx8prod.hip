@@ -569,11 +569,8 @@ hipError_t launch_square(const TileArgs& t, bool bf16, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_few(FewArgs a, bool bf16, hipStream_t s) {
-  const int need = a.M < kFewRows ? (int)a.M : kFewRows;
-  // two workgroups per CU where all rows (of a chunk of 16) fit half of its LDS, else one
-  const bool half = few_rows(a.nb, kFewLds) >= need;
-  const int most = half ? kFewRows : few_rows(a.nb, kFewLdsAll);
+// most: rows of a chunk; half: two workgroups share a CU.
+hipError_t launch_few(FewArgs a, int most, bool half, bool bf16, hipStream_t s) {
   const int64_t chunks = (a.M + most - 1) / most;
   a.rows = (int)((a.M + chunks - 1) / chunks);
   a.arow = few_arow(a.nb);
@@ -601,25 +598,28 @@ hipError_t launch_few(FewArgs a, bool bf16, hipStream_t s) {
 
 hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t* w, const uint8_t* ws, int64_t M,
                               int N, int K, bool out_bf16, void* out, hipStream_t s) {
-  const int nb = K / 32;
-  if (M <= kFewRows && few_rows(nb, kFewLdsAll) >= 1) {
-    FewArgs f{};
-    f.a = a;
-    f.as = as;
-    f.w = w;
-    f.ws = ws;
-    f.M = M;
-    f.N = N;
-    f.nb = nb;
-    const int nss = (nb + 15) / 16;
-    f.per = (nss + kFewWaves - 1) / kFewWaves;
-    f.kw = (nss + f.per - 1) / f.per;
-    f.rw = kFewWaves / f.kw;
-    f.out = out;
-    return launch_few(f, out_bf16, s);
-  }
+  const int nb = K / 32, nss = (nb + 15) / 16;
+  FewArgs f{};
+  f.a = a;
+  f.as = as;
+  f.w = w;
+  f.ws = ws;
+  f.M = M;
+  f.N = N;
+  f.nb = nb;
+  f.per = (nss + kFewWaves - 1) / kFewWaves;
+  f.kw = (nss + f.per - 1) / f.per;
+  f.rw = kFewWaves / f.kw;
+  f.out = out;
+  const int fit = few_rows(nb, kFewLds), fit_all = few_rows(nb, kFewLdsAll);
+  const int64_t cus = device_cu_count(), wgs = (mx_groups(N, 16) + f.rw - 1) / f.rw;
+  // Few rows: two workgroups a CU where all rows fit half of its LDS, else one, in
+  // chunks of what fits.  More, with a long K: where the workgroups of every chunk
+  // are resident at once.
+  if (M <= kFewRows && fit >= M) return launch_few(f, kFewRows, true, out_bf16, s);
+  if (M <= kFewRows && fit_all >= 1) return launch_few(f, fit_all, false, out_bf16, s);
+  if (K >= 4096 && fit >= 8 && (M + fit - 1) / fit * wgs <= 2 * cus) return launch_few(f, fit, true, out_bf16, s);
   const TileArgs t{a, as, w, ws, (int)M, N, nb, out};
-  const int64_t cus = device_cu_count();
   auto tiles = [&](int B) { return mx_tile_grid(t.M, N, B).total; };
   // the largest tile that gives every CU one and that either side more than half fills
   const int64_t side = M < N ? M : N;
