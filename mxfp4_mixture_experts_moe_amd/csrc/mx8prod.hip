@@ -25,6 +25,8 @@
 #include "mx_common.h"
 #include "mx_shape.h"
 
+#include <math.h>
+
 #include <type_traits>
 
 namespace k3moe {
@@ -270,15 +272,22 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
 }
 
 // ---------------------------------------------------------------------------
-// Tiles.  A workgroup of kWm x kWn waves owns a B x B tile of C; K goes in steps
-// of 128 (four blocks: 128 bytes of a row of A, 64 of W) through a ring of LDS
-// buffers filled by direct global -> LDS loads.  Instruction kk (0, 1) of a step
-// takes its blocks 2 kk and 2 kk + 1.  The 16-byte chunks of an LDS row are
-// permuted by the row so that the lanes of a read touch every bank once.
+// Tiles.  A workgroup owns a B x B tile of C; kWm x kWn waves share it, and kSplit
+// such sets of waves take the steps of K (128: four blocks, 128 bytes of a row of
+// A, 64 of W) in turn, each with sums of its own that are added at the end.  A
+// stage is kSplit steps; stages go through a ring of kRing LDS buffers filled by
+// direct global -> LDS loads.  Instruction kk (0, 1) of a step takes its blocks 2
+// kk and 2 kk + 1.  The 16-byte chunks of an LDS row are permuted by the row so
+// that the lanes of a read touch every bank once.
+//
+// A wave's matrix instructions of one half step run while the operands of the
+// next are read and split; the barrier of a stage stands between its two halves,
+// when all of it has been read into registers: its buffer is free from there on,
+// and the next stage, whose loads the wave has waited for, is there.
 //   kStaged (K a multiple of 512): scales, 16 bytes (four steps) of every row, go
 //     through LDS, too, one load per wave and four steps;
 //   else each lane loads the four scale bytes of its rows for every step, which
-//     are not aligned.
+//     are not aligned, half a stage ahead.
 constexpr int kXcds = 8;
 
 struct TileArgs {
@@ -293,23 +302,25 @@ __device__ __forceinline__ void wait_vm() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N_) : "memory");
 }
 // Barrier of the ring: this wave's LDS reads are done (the buffer they read is
-// refilled after it) and its loads of the next step's buffer have landed.
+// refilled after it) and its loads of the next stage's buffer have landed.
 __device__ __forceinline__ void ring_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int B, int kWm, int kWn, bool kStaged, bool kBf16>
-__global__ __launch_bounds__(kWm * kWn * 64) void mx8_tile_kernel(TileArgs t) {
-  constexpr int kWaves = kWm * kWn;
+template <int B, int kWm, int kWn, int kSplit, int kRing, bool kStaged, bool kBf16>
+__global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileArgs t) {
+  constexpr int kSet = kWm * kWn, kWaves = kSet * kSplit;
   constexpr int kTm = B / (32 * kWm), kTn = B / (32 * kWn);  // 32-row operand tiles per wave
-  constexpr int kRing = B >= 256 ? 2 : 4;
-  constexpr int kADw = B * 32, kStageDw = B * 48;  // dwords of a step's rows of A; and of W behind them
-  constexpr int kLoadsA = B / (8 * kWaves), kLoadsW = B / (16 * kWaves), kLoads = kLoadsA + kLoadsW;  // 1 KB each, per wave and step
+  constexpr int kADw = B * 32, kStepDw = B * 48;  // dwords of a step's rows of A; and of W behind them
+  constexpr int kStageDw = kSplit * kStepDw;
+  constexpr int kLoadsA = kSplit * B / (8 * kWaves), kLoadsW = kSplit * B / (16 * kWaves), kLoads = kLoadsA + kLoadsW;  // 1 KB each, per wave and stage
+  constexpr int kGroup = 4 / kSplit;  // stages that a load of scales lasts
+  static_assert((kRing == 2 || kRing == 4) && kGroup >= kRing - 2, "scales land with the stage that they are for");
   // one array per buffer, so that the compiler sees that a read of one buffer
   // does not depend on the loads in flight into the others
   __shared__ __attribute__((aligned(256))) uint32_t l0[kStageDw], l1[kStageDw], l2[kRing > 2 ? kStageDw : 1],
-      l3[kRing > 2 ? kStageDw : 1];
+      l3[kRing > 3 ? kStageDw : 1];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / kWn, wn = wave % kWn;
+  const int ks = wave / kSet, wm = wave % kSet / kWn, wn = wave % kWn;
   const int r32 = lane & 31, h = lane >> 5;
 
   // Tile order: the ids an XCD gets (id % 8) are a contiguous run of the
@@ -332,13 +343,14 @@ __global__ __launch_bounds__(kWm * kWn * 64) void mx8_tile_kernel(TileArgs t) {
   const uint32_t arowb = (uint32_t)nb * 32, wrowb = (uint32_t)nb * 16;
   const int mrows = t.M - m0 < B ? (int)(t.M - m0) : B;
   const int nrows = t.N - n0 < B ? t.N - n0 : B;
-  const int nsteps = (nb + 3) >> 2;
+  const int nsteps = (nb + 3) >> 2, nstages = (nsteps + kSplit - 1) / kSplit;
 
   // position of 16-byte chunk c in LDS row r
   auto place_a = [](int c, int r) { return c ^ ((r >> 1) & 7); };
   auto place_w = [](int c, int r) { return c ^ ((r >> 2) & 3); };
-  // loads: wave w fills LDS rows w * B / kWaves .. of A and of W
-  const int lrow0 = wave * (B / kWaves);
+  // loads: wave w fills rows (w % kSet) * B / kSet .. of step w / kSet of a stage
+  constexpr int kRows = B / kSet;
+  const int lrow0 = wave % kSet * kRows;
   uint32_t aoff[kLoadsA], woff[kLoadsW];
 #pragma unroll
   for (int j = 0; j < kLoadsA; ++j) {
@@ -351,13 +363,14 @@ __global__ __launch_bounds__(kWm * kWn * 64) void mx8_tile_kernel(TileArgs t) {
     woff[j] = (uint32_t)min(r, nrows - 1) * wrowb + 16 * place_w(lane % 4, r);
   }
   // (steps past K are outside the buffers: zeros that cost no traffic)
-  auto issue = [&](int step, uint32_t* buf) {
+  auto issue = [&](int stage, uint32_t* buf) {
+    const int step = stage * kSplit + ks;
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(t.a + m0 * arowb), 0, step < nsteps ? (int)(mrows * arowb) : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rw =
         __builtin_amdgcn_make_buffer_rsrc((void*)(t.w + (int64_t)n0 * wrowb), 0, step < nsteps ? (int)(nrows * wrowb) : 0, 0x00020000);
-    uint32_t* const da = buf + lrow0 * 32;
-    uint32_t* const dw = buf + kADw + lrow0 * 16;
-    const int sa = 128 * step, sw = 64 * step;
+    uint32_t* const da = buf + ks * kStepDw + lrow0 * 32;
+    uint32_t* const dw = buf + ks * kStepDw + kADw + lrow0 * 16;
+    const int sa = __builtin_amdgcn_readfirstlane(128 * step), sw = __builtin_amdgcn_readfirstlane(64 * step);
 #pragma unroll
     for (int j = 0; j < kLoadsA; ++j) {
       const uint32_t vo = aoff[j];  // (an array element passed straight makes the host pass drop the kernel's launch stub)
@@ -370,37 +383,67 @@ __global__ __launch_bounds__(kWm * kWn * 64) void mx8_tile_kernel(TileArgs t) {
     }
   };
 
-  // scales of this lane's rows
-  const uint8_t* ap[kTm];
-  const uint8_t* wp[kTn];
-#pragma unroll
-  for (int i = 0; i < kTm; ++i) ap[i] = t.as + (m0 + min(wm * (B / kWm) + 32 * i + r32, mrows - 1)) * nb;
-#pragma unroll
-  for (int i = 0; i < kTn; ++i) wp[i] = t.ws + (int64_t)(n0 + min(wn * (B / kWn) + 32 * i + r32, nrows - 1)) * nb;
-  uint32_t sa[kTm], sw[kTn];  // !kStaged: of the next step
-  auto load_scales = [&](int step) {
-#pragma unroll
-    for (int i = 0; i < kTm; ++i) sa[i] = load_u32(ap[i] + 4 * step);
-#pragma unroll
-    for (int i = 0; i < kTn; ++i) sw[i] = load_u32(wp[i] + 4 * step);
-  };
-  // kStaged: 16 bytes (four steps) of each of the tile's rows through LDS
+  // Scales.  kStaged: 16 bytes (four steps) of each of the tile's rows through LDS
   constexpr int kScaleLoads = 2 * B / 64;  // of 64 rows; one per wave (some twice where there are more waves)
   static_assert(kScaleLoads <= kWaves, "every wave does one load of scales");
-  __shared__ __attribute__((aligned(256))) uint32_t lsc[kStaged ? 2 * 2 * B * 4 : 1];
+  __shared__ __attribute__((aligned(256))) uint32_t lsc0[kStaged ? 2 * B * 4 : 1], lsc1[kStaged ? 2 * B * 4 : 1];  // (of even groups, of odd ones)
   const int sload = wave % kScaleLoads;
   const bool s_a = sload < kScaleLoads / 2;
   const int slrows = s_a ? mrows : nrows;
   const __amdgpu_buffer_rsrc_t rsc = __builtin_amdgcn_make_buffer_rsrc((void*)(s_a ? t.as + m0 * nb : t.ws + (int64_t)n0 * nb), 0, slrows * nb, 0x00020000);
   const int svoff = min(sload % (kScaleLoads / 2) * 64 + lane, slrows - 1) * nb;
-  auto issue_scales = [&](int group) {
-    uint32_t* dst = lsc + (group & 1) * 2 * B * 4 + sload * 256;
+  auto issue_scales = [&](int group, uint32_t* buf) {
+    uint32_t* dst = buf + sload * 256;
     const int so = 16 * min(group, (nb >> 4) - 1), vo = svoff;  // (past the last: that again, not used)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsc, dst, 16, vo, so, 0, 0);
   };
-  mx_u32x4 ga[kTm], gw[kTn];
-  uint32_t ca[kTm], cw[kTn];  // bytes 0 and 2: of this lane half's blocks of both instructions of the step
-  auto own_bytes = [&](uint32_t v) { return h ? v >> 8 : v; };
+  // !kStaged: from memory, those past K 127 (the value 1)
+  const uint8_t *ap[kTm], *wp[kTn];
+  if constexpr (!kStaged) {
+#pragma unroll
+    for (int i = 0; i < kTm; ++i) ap[i] = t.as + (m0 + min(wm * (B / kWm) + 32 * i + r32, mrows - 1)) * nb;
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) wp[i] = t.ws + (int64_t)(n0 + min(wn * (B / kWn) + 32 * i + r32, nrows - 1)) * nb;
+  }
+  auto scale4 = [&](const uint8_t* row, int step) -> uint32_t {
+    if (nb < 4) return load_tail(row, min(4 * step, nb), nb);
+    const int o = min(4 * step, nb - 4);
+    return load_u32(row + o);
+  };
+  // ... and what of the four bytes is past K
+  auto trim = [&](uint32_t v, int step) -> uint32_t {
+    const int k = nb < 4 ? 0 : min(max(4 * step - (nb - 4), 0), 4);
+    return (uint32_t)(((uint64_t)0x7F7F7F7Fu << 32 | v) >> (8 * k));
+  };
+  // The raw scales of this wave's step of a stage; bytes 0 and 2 of own_bytes() are
+  // those of this lane half's blocks of both instructions.
+  uint32_t na[kTm], nw[kTn];
+  auto read_scales = [&](int stage, const uint32_t* buf) {
+    const int step = stage * kSplit + ks;
+    if constexpr (kStaged) {
+      const uint32_t* const l = buf + (step & 3);
+#pragma unroll
+      for (int i = 0; i < kTm; ++i) na[i] = l[4 * (wm * (B / kWm) + 32 * i + r32)];
+#pragma unroll
+      for (int i = 0; i < kTn; ++i) nw[i] = l[4 * (B + wn * (B / kWn) + 32 * i + r32)];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTm; ++i) na[i] = scale4(ap[i], step);
+#pragma unroll
+      for (int i = 0; i < kTn; ++i) nw[i] = scale4(wp[i], step);
+    }
+  };
+  uint32_t ca[kTm], cw[kTn];
+  auto take_scales = [&](int stage) {
+    auto own_bytes = [&](uint32_t v) {
+      if constexpr (!kStaged) v = trim(v, stage * kSplit + ks);
+      return h ? v >> 8 : v;
+    };
+#pragma unroll
+    for (int i = 0; i < kTm; ++i) ca[i] = own_bytes(na[i]);
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) cw[i] = own_bytes(nw[i]);
+  };
 
   f32x16 acc[kTm][kTn];
 #pragma unroll
@@ -408,26 +451,45 @@ __global__ __launch_bounds__(kWm * kWn * 64) void mx8_tile_kernel(TileArgs t) {
 #pragma unroll
     for (int j = 0; j < kTn; ++j) acc[i][j] = f32x16{};
 
-  const uint32_t arow = (uint32_t)(wm * (B / kWm) + r32) * 128, wrow = (uint32_t)kADw * 4 + (uint32_t)(wn * (B / kWn) + r32) * 64;
-  // Instruction kk of a step held in `buf`; keep0, keep1: false zeroes its first
-  // or second block of A (blocks past K).
-  auto part = [&](const uint32_t* buf, auto kc, bool keep0, bool keep1) {
+  const uint32_t arow = (uint32_t)ks * kStepDw * 4 + (uint32_t)(wm * (B / kWm) + r32) * 128;
+  const uint32_t wrow = (uint32_t)(ks * kStepDw + kADw) * 4 + (uint32_t)(wn * (B / kWn) + r32) * 64;
+  // Operands of an instruction: as read, and split.
+  struct Raw {
+    mx_u32x4 a[kTm][2], w[kTn];
+  };
+  auto read = [&](const uint32_t* buf, auto kc, Raw& n) {
     constexpr int kk = decltype(kc)::value;
     const uint8_t* const l = reinterpret_cast<const uint8_t*>(buf);
-    mx_u32x4 fw[kTn];
-    Split fa[kTm];
     const uint32_t p0 = 16u * (uint32_t)place_a(4 * kk + h, r32), p1 = 16u * (uint32_t)place_a(4 * kk + 2 + h, r32);
     const uint32_t pw = 16u * (uint32_t)place_w(2 * kk + h, r32);
 #pragma unroll
-    for (int i = 0; i < kTn; ++i) fw[i] = *reinterpret_cast<const mx_u32x4*>(l + wrow + 32 * 64 * i + pw);
-#pragma unroll
     for (int i = 0; i < kTm; ++i) {
-      mx_u32x4 x0 = *reinterpret_cast<const mx_u32x4*>(l + arow + 32 * 128 * i + p0);
-      mx_u32x4 x1 = *reinterpret_cast<const mx_u32x4*>(l + arow + 32 * 128 * i + p1);
-      if (!keep0) x0 = mx_u32x4{0u, 0u, 0u, 0u};
-      if (!keep1) x1 = mx_u32x4{0u, 0u, 0u, 0u};
-      fa[i] = split8(x0, x1);
+      n.a[i][0] = *reinterpret_cast<const mx_u32x4*>(l + arow + 32 * 128 * i + p0);
+      n.a[i][1] = *reinterpret_cast<const mx_u32x4*>(l + arow + 32 * 128 * i + p1);
     }
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) n.w[i] = *reinterpret_cast<const mx_u32x4*>(l + wrow + 32 * 64 * i + pw);
+  };
+  Split fa[kTm];
+  mx_u32x4 fw[kTn];
+  // (blocks of A past K are zeroed: what lies there is another row's, or NaN codes)
+  auto split = [&](Raw& n, auto kc, int stage) {
+    constexpr int kk = decltype(kc)::value;
+    if constexpr (!kStaged) {
+      const int b0 = 4 * (stage * kSplit + ks) + 2 * kk;
+#pragma unroll
+      for (int i = 0; i < kTm; ++i) {
+        if (b0 >= nb) n.a[i][0] = mx_u32x4{0u, 0u, 0u, 0u};
+        if (b0 + 1 >= nb) n.a[i][1] = mx_u32x4{0u, 0u, 0u, 0u};
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kTm; ++i) fa[i] = split8(n.a[i][0], n.a[i][1]);
+#pragma unroll
+    for (int i = 0; i < kTn; ++i) fw[i] = n.w[i];
+  };
+  auto multiply = [&](auto kc) {
+    constexpr int kk = decltype(kc)::value;
 #pragma unroll
     for (int i = 0; i < kTm; ++i)
 #pragma unroll
@@ -441,92 +503,90 @@ __global__ __launch_bounds__(kWm * kWn * 64) void mx8_tile_kernel(TileArgs t) {
   };
   using C0 = std::integral_constant<int, 0>;
   using C1 = std::integral_constant<int, 1>;
-  using C2 = std::integral_constant<int, 2>;
-  using C3 = std::integral_constant<int, 3>;
 
-  // Whole groups of four steps.  Every step issues the loads of kRing - 1 steps
-  // on, the first of a group (kStaged; else every one) the scales of the next
-  // but those, without a branch, so the number of loads in flight is the same
-  // everywhere: when a step starts, the loads after its own are those of kRing -
-  // 2 steps and up to one set of scales.
-  const int full = nb >> 4;
-  auto stage = [&](auto uc, int q, uint32_t* cur, uint32_t* refill) {
-    constexpr int u = decltype(uc)::value;  // the step in its group
-    if constexpr (kStaged)
-      wait_vm<(kRing - 2) * kLoads + (kRing > 2 && (u == 1 || u == 2) ? 1 : 0)>();
-    else
-      wait_vm<kRing == 2 ? 0 : 2 * kLoads + kTm + kTn>();
+  // One stage, of which the first half step's operands are in registers: `cur` its
+  // buffer, `next` that of the next stage.  Between the halves the loads in flight
+  // are those of kRing - 1 stages (and up to two sets of scales); the oldest has to
+  // have landed, and with it, or before it, the scales that it needs.
+  auto stage = [&](auto uc, int q, uint32_t* cur, uint32_t* next) {
+    constexpr int u = decltype(uc)::value;  // q modulo 4 where groups have two stages, 8 where they have four
+    constexpr bool kLast = u % kGroup == kGroup - 1;  // of its group
+    uint32_t* const sn = (u + 1) / kGroup % 2 ? lsc1 : lsc0;  // the next stage's scales
+    Raw n;
+    read(cur, C1{}, n);
+    multiply(C0{});
+    split(n, C1{}, q);
+    wait_vm<(kRing - 2) * kLoads>();
     ring_barrier();
-    if constexpr (kStaged && u == 0) {
-      const uint32_t* const l = lsc + ((q >> 2) & 1) * 2 * B * 4;
-#pragma unroll
-      for (int i = 0; i < kTm; ++i) ga[i] = *reinterpret_cast<const mx_u32x4*>(l + 4 * (wm * (B / kWm) + 32 * i + r32));
-#pragma unroll
-      for (int i = 0; i < kTn; ++i) gw[i] = *reinterpret_cast<const mx_u32x4*>(l + 4 * (B + wn * (B / kWn) + 32 * i + r32));
-      asm volatile("" ::: "memory");
-      issue_scales((q >> 2) + 1);
-      asm volatile("" ::: "memory");
-    }
-    if constexpr (kStaged) {
-#pragma unroll
-      for (int i = 0; i < kTm; ++i) ca[i] = own_bytes(ga[i][u]);
-#pragma unroll
-      for (int i = 0; i < kTn; ++i) cw[i] = own_bytes(gw[i][u]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kTm; ++i) ca[i] = own_bytes(sa[i]);
-#pragma unroll
-      for (int i = 0; i < kTn; ++i) cw[i] = own_bytes(sw[i]);
-      load_scales(min(q + 1, 4 * full - 1));
-      asm volatile("" ::: "memory");
-    }
-    issue(q + kRing - 1, refill);
+    read_scales(q + 1, sn);
+    asm volatile("" ::: "memory");
+    if constexpr (kStaged && kLast) issue_scales((q + 1) / kGroup + 1, sn == lsc0 ? lsc1 : lsc0);
+    asm volatile("" ::: "memory");
+    issue(q + kRing, cur);
     asm volatile("" ::: "memory");  // the loads go out before the reads below
-    part(cur, C0{}, true, true);
-    part(cur, C1{}, true, true);
+    read(next, C0{}, n);
+    multiply(C1{});
+    split(n, C0{}, q + 1);
+    take_scales(q + 1);
   };
-  if constexpr (kStaged) issue_scales(0);
-  asm volatile("" ::: "memory");
-  if constexpr (kRing == 2) {
-    if (!kStaged && full > 0) load_scales(0);
+  {
+    Raw n;
+    if constexpr (kStaged) issue_scales(0, lsc0);
     asm volatile("" ::: "memory");
     issue(0, l0);
-    for (int q = 0; q < 4 * full; q += 4) {
-      stage(C0{}, q, l0, l1);
-      stage(C1{}, q + 1, l1, l0);
-      stage(C2{}, q + 2, l0, l1);
-      stage(C3{}, q + 3, l1, l0);
-    }
-  } else {
-    issue(0, l0);
+    if constexpr (kStaged) issue_scales(1, lsc1);
     issue(1, l1);
-    if (!kStaged && full > 0) load_scales(0);
-    asm volatile("" ::: "memory");
-    issue(2, l2);
-    for (int q = 0; q < 4 * full; q += 4) {
-      stage(C0{}, q, l0, l3);
-      stage(C1{}, q + 1, l1, l0);
-      stage(C2{}, q + 2, l2, l1);
-      stage(C3{}, q + 3, l3, l2);
-    }
-  }
-
-  // The rest of K, up to four steps.
-  const int rest = kStaged ? 0 : nsteps - 4 * full;
-  for (int u = 0; u < rest; ++u) {
-    const int q = 4 * full + u, b0 = 4 * q;
-    wait_vm<0>();
+    if constexpr (kRing > 2) issue(2, l2);
+    if constexpr (kRing > 3) issue(3, l3);
+    wait_vm<(kRing - 1) * kLoads>();
     ring_barrier();
-    auto pick = [&](int i) { return kRing == 2 ? (i & 1 ? l1 : l0) : (i & 3) == 0 ? l0 : (i & 3) == 1 ? l1 : (i & 3) == 2 ? l2 : l3; };
-    issue(q + kRing - 1, pick(u + kRing - 1));
-#pragma unroll
-    for (int i = 0; i < kTm; ++i) ca[i] = own_bytes(load_tail(ap[i], b0, nb));
-#pragma unroll
-    for (int i = 0; i < kTn; ++i) cw[i] = own_bytes(load_tail(wp[i], b0, nb));
-    part(pick(u), C0{}, true, b0 + 1 < nb);
-    part(pick(u), C1{}, b0 + 2 < nb, b0 + 3 < nb);
+    read_scales(0, lsc0);
+    take_scales(0);
+    read(l0, C0{}, n);
+    split(n, C0{}, 0);
+  }
+  // (kStaged: whole groups; no branch around a load, so that their number in flight is known everywhere)
+  auto four = [&](auto uc, int q) {  // stages q .. q + 3, false: that was all
+    constexpr int u = decltype(uc)::value;
+    stage(std::integral_constant<int, u>{}, q, l0, l1);
+    if (!kStaged && q + 1 == nstages) return false;
+    stage(std::integral_constant<int, u + 1>{}, q + 1, l1, kRing > 2 ? l2 : l0);
+    if ((!kStaged || kGroup == 2) && q + 2 == nstages) return false;
+    stage(std::integral_constant<int, u + 2>{}, q + 2, kRing > 2 ? l2 : l0, kRing > 2 ? l3 : l1);
+    if (!kStaged && q + 3 == nstages) return false;
+    stage(std::integral_constant<int, u + 3>{}, q + 3, kRing > 2 ? l3 : l1, l0);
+    return q + 4 < nstages;
+  };
+  if constexpr (kStaged && kGroup == 4) {
+    for (int q = 0;; q += 8)
+      if (!four(C0{}, q) || !four(std::integral_constant<int, 4>{}, q + 4)) break;
+  } else {
+    for (int q = 0; four(C0{}, q); q += 4) {}
   }
   wait_vm<0>();  // no load into LDS outlives the workgroup
+
+  if constexpr (kSplit > 1) {  // the other sets' sums through LDS, in order, an operand tile at a time
+    static_assert(kSplit == 2 && kSet * 1024 <= kStageDw, "a set's operand tiles fit a buffer");
+    float* const red = reinterpret_cast<float*>(l0);
+#pragma unroll
+    for (int i = 0; i < kTm; ++i)
+#pragma unroll
+      for (int j = 0; j < kTn; ++j) {
+        __syncthreads();
+        if (ks == 1)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) *reinterpret_cast<f32x4*>(red + (wave % kSet) * 1024 + 256 * v + 4 * lane) = f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+        __syncthreads();
+        if (ks == 0)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const f32x4 o = *reinterpret_cast<const f32x4*>(red + (wave % kSet) * 1024 + 256 * v + 4 * lane);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * v + e] += o[e];
+          }
+      }
+    if (ks != 0) return;
+  }
 
   // lane holds column n = lane % 32, rows 8 * (v / 4) + 4 * h + v % 4
 #pragma unroll
@@ -554,18 +614,20 @@ int few_rows(int nb, int lds) {
   return r < kFewRows ? r : kFewRows;
 }
 
-template <int B, int kWm, int kWn>
+template <int B, int kWm, int kWn, int kSplit, int kRing>
 hipError_t launch_square(const TileArgs& t, bool bf16, hipStream_t s) {
   const MxTileGrid g = mx_tile_grid(t.M, t.N, B);
-  const dim3 grid(g.x, g.y), block(kWm * kWn * 64);
+  const dim3 grid(g.x, g.y), block(kWm * kWn * kSplit * 64);
   auto go = [&](auto st, auto b) {
-    hipLaunchKernelGGL((mx8_tile_kernel<B, kWm, kWn, decltype(st)::value, decltype(b)::value>), grid, block, 0, s, t);
+    hipLaunchKernelGGL((mx8_tile_kernel<B, kWm, kWn, kSplit, kRing, decltype(st)::value, decltype(b)::value>), grid, block, 0, s, t);
   };
   const bool staged = t.nb % 16 == 0;
   if (staged && bf16) go(std::true_type{}, std::true_type{});
   else if (staged) go(std::true_type{}, std::false_type{});
-  else if (bf16) go(std::false_type{}, std::true_type{});
-  else go(std::false_type{}, std::false_type{});
+  else if constexpr (B < 256) {  // (the registers of the largest do not hold the scales of ragged rows, too)
+    if (bf16) go(std::false_type{}, std::true_type{});
+    else go(std::false_type{}, std::false_type{});
+  }
   return hipGetLastError();
 }
 
@@ -618,14 +680,24 @@ hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t
   // are resident at once.
   if (M <= kFewRows && fit >= M) return launch_few(f, kFewRows, true, out_bf16, s);
   if (M <= kFewRows && fit_all >= 1) return launch_few(f, fit_all, false, out_bf16, s);
-  if (K >= 4096 && fit >= 8 && (M + fit - 1) / fit * wgs <= 2 * cus) return launch_few(f, fit, true, out_bf16, s);
+  if (K >= 4096 && fit >= 4 && (M + fit - 1) / fit * wgs <= 2 * cus) return launch_few(f, fit, true, out_bf16, s);
   const TileArgs t{a, as, w, ws, (int)M, N, nb, out};
-  auto tiles = [&](int B) { return mx_tile_grid(t.M, N, B).total; };
-  // the largest tile that gives every CU one and that either side more than half fills
-  const int64_t side = M < N ? M : N;
-  if (side > 128 && tiles(256) >= cus) return launch_square<256, 4, 2>(t, out_bf16, s);
-  if (side > 64 && tiles(128) >= cus) return launch_square<128, 4, 2>(t, out_bf16, s);
-  return launch_square<64, 2, 2>(t, out_bf16, s);
+  // The tile side whose workgroups take the least time together.  A tile's time, in
+  // units of a 64 x 64 one that has a CU to itself (20 us at K = 7168: eight waves,
+  // each step of K another four's): 2.15 for 128 x 128 and 6.2 for 256 x 256.
+  // Several smaller ones share a CU, at 0.9 each (four waves then) and 2.1, two of
+  // them at no less than 1.6 and 3.6.  With `each` tiles per CU: 256 x 7168 x
+  // 7168, 448 tiles of 64, 33 us (128: 43); 512 x 7168 x 7168, 224 tiles of 128, 45
+  // us (64: 62); 2048 x 7168 x 7168, 224 tiles of 256, 129 us (128: 158).
+  auto each = [&](int B) { return (double)mx_tile_grid(t.M, N, B).total / (double)cus; };
+  const double e64 = each(64), e128 = each(128), e256 = each(256);
+  const double c64 = e64 <= 1.0 ? 1.0 : 0.9 * (e64 > 1.8 ? e64 : 1.8);
+  const double c128 = e128 <= 1.0 ? 2.15 : 2.1 * (e128 > 1.7 ? e128 : 1.7);
+  const double c256 = 6.2 * ceil(e256);
+  if (nb % 16 == 0 && c256 < c128 && c256 < c64) return launch_square<256, 4, 2, 1, 2>(t, out_bf16, s);
+  if (c128 < c64) return launch_square<128, 4, 2, 1, 2>(t, out_bf16, s);
+  if (e64 <= 1.0) return launch_square<64, 2, 2, 2, 4>(t, out_bf16, s);
+  return launch_square<64, 2, 2, 1, 4>(t, out_bf16, s);
 }
 
 }  // namespace k3moe
