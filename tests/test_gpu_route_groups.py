@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 
 # E, groups, keep, k
 SHAPES = [(8, 2, 1, 2), (1, 1, 1, 1), (64, 64, 5, 5), (60, 4, 4, 3), (96, 3, 2, 64), (256, 8, 4, 8), (896, 8, 4, 16), (896, 16, 5, 16), (1000, 125, 30, 24),
-          (1024, 32, 1, 32), (1100, 11, 3, 10), (1540, 20, 7, 24), (5000, 1, 1, 6), (4096, 4096, 40, 40), (130, 130, 64, 64), (62, 31, 30, 33), (8192, 8192, 3, 3)]
+          (1024, 32, 1, 32), (1100, 11, 3, 10), (1540, 20, 7, 24), (5000, 1, 1, 6), (4096, 4096, 40, 40), (130, 130, 64, 64), (62, 31, 30, 33), (8192, 8192, 3, 3), (130, 130, 100, 64), (900, 300, 70, 64)]
 
 
 def check(k3, z, bias, k, groups, keep, what=None, **kw):
@@ -64,6 +64,23 @@ def test_near_ties(k3, score):
         z[t, i] = np.nextafter(np.float32(0.75), np.float32(9 if t % 2 else -9))
     check(k3, z, None, 12, 16, 4, score=score)
     check(k3, z, (g.integers(-1, 2, 256) * 2.0**-30).astype(np.float32), 12, 16, 4, score=score)
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("E,groups,keep,k", [(64, 16, 5, 9), (256, 8, 4, 8), (896, 16, 5, 16), (1024, 64, 20, 64)])
+def test_groups_that_differ_in_fp64_only(k3, score, top, E, groups, keep, k):
+    """Every group has two clear best experts; their scores (and sums) differ by 1e-7 and less from group to group, some not at all."""
+    g = np.random.default_rng([E, top])
+    n = E // groups
+    for T, bias in ((40, False), (40, True)):
+        z = (-2.0 - g.random((T, groups, n))).astype(np.float32)
+        steps = g.integers(-2, 3, (T, groups, 2))
+        z[:, :, 0] = 1.0 + steps[..., 0] * np.float32(2.0**-23)
+        z[:, :, 1] = 0.5 - steps[..., 1] * np.float32(2.0**-24)
+        z = np.take_along_axis(z, np.argsort(g.random((T, groups, n)), -1), -1).reshape(T, E)
+        b = (g.integers(-1, 2, E) * 2.0**-28).astype(np.float32) if bias else None
+        check(k3, z, b, k, groups, keep, score=score, group_top=top)
 
 
 @pytest.mark.parametrize("score", ["sigmoid", "softmax"])

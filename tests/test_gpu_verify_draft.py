@@ -59,6 +59,28 @@ def test_full_vocabulary(k3, dtype):
     assert n.max() > 0
 
 
+@pytest.mark.parametrize("S,W,V", [(2, 3, 300001), (1, 2, 1200007), (40, 2, 50000)])
+@pytest.mark.parametrize("probs", [True, False])
+def test_many_chunks(k3, S, W, V, probs):
+    """More chunks than a wave has lanes, and enough of them for several to a workgroup."""
+    g = np.random.default_rng([S, V])
+    c = make(g, S, W, V, "bf16", probs=probs)
+    c["u_accept"][::2] = 0.999  # rejected, mostly
+    check(k3, c)
+    c["temperature"] = g.choice([0.0, 0.8], S).astype(np.float32)
+    check(k3, c)
+
+
+def test_draft_probabilities_of_zero(k3):
+    g = np.random.default_rng(21)
+    c = make(g, 12, 4, 3000)
+    i = np.arange(12)[:, None], np.arange(3)[None]
+    c["probs"][i[0], i[1], c["draft"]] = 0.0  # accepted wherever p is above 0
+    c["logits"][3, 1, c["draft"][3, 1]] = -np.inf
+    n, _ = check(k3, c)
+    assert n[3] == 1 and (np.delete(n, 3) == 3).all()
+
+
 def test_lengths_and_temperatures(k3):
     g = np.random.default_rng(12)
     S, W, V = 48, 6, 5003
