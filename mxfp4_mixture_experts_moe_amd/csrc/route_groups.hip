@@ -326,7 +326,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
     for (int j = 0; j < NPER; ++j) b[j] = 0.0f;
   }
 #pragma unroll
-  for (int j = 0; j < NPER; ++j) z[j] = lane + kWaveSize * j < a.E ? z[j] : -INFINITY;
+  for (int j = 0; j < NPER; ++j) z[j] = lane < a.E - kWaveSize * j ? z[j] : -INFINITY;
 
   // fp32 scores s, of experts past E -inf, and what groups add up (gs).  u = 2^-24:
   //   sigmoid: off by at most 2^-21 (1 + |s|) (route_device.h).
@@ -368,7 +368,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
   if (a.keep < a.groups) {
 #pragma unroll
     for (int j = 0; j < NPER; ++j)
-      if (lane + kWaveSize * j < a.E) score[lane + kWaveSize * j] = s[j];
+      if (lane < a.E - kWaveSize * j) score[lane + kWaveSize * j] = s[j];
     wave_fence();
     const int g = lane / lanes, sub = lane & (lanes - 1);
     float b1 = -INFINITY, b2 = -INFINITY;
@@ -450,10 +450,12 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
       if (__builtin_popcountll(kept) != a.keep) return false;
     }
   }
-  // An expert of a kept group, without a branch.
-  auto in_kept = [&](int e) -> bool {
-    const uint32_t g = __umul24((uint32_t)e, inv_size) >> 20;
-    return ((e < a.E) & (int)(kept >> ((g << shift) & 63u))) != 0;
+  // Bit g: group g is kept.  Whether expert lane + 64 j belongs to one, without a branch.
+  const uint64_t groups = a.keep < a.groups ? __builtin_amdgcn_ballot_w64(lane < a.groups && (kept >> ((lane << shift) & 63) & 1ull) != 0) : kept;
+  const uint32_t place = __umul24((uint32_t)lane, inv_size);
+  auto in_kept = [&](int j) -> bool {
+    const uint32_t g = (place + (uint32_t)(kWaveSize * j) * inv_size) >> 20;
+    return ((lane < a.E - kWaveSize * j) & (int)(groups >> (g & 63u))) != 0;
   };
 
   // Candidates: s[j] >= theta.
@@ -462,17 +464,13 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
   int total = 0;
   if (n_kept <= kWaveSize) {
 #pragma unroll
-    for (int j = 0; j < NPER; ++j) {
-      const int e = lane + kWaveSize * j;
-      s[j] = in_kept(e) ? 1.0f : -1.0f;
-    }
+    for (int j = 0; j < NPER; ++j) s[j] = in_kept(j) ? 1.0f : -1.0f;
   } else {
     float best = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NPER; ++j) {
-      const int e = lane + kWaveSize * j;
       const float v = by_logit ? fmaxf(z[j] - m, -700.0f) : s[j];
-      s[j] = in_kept(e) ? v : -INFINITY;
+      s[j] = in_kept(j) ? v : -INFINITY;
       best = fmaxf(best, s[j]);
     }
     const float thr = wave_kth_largest(best, a.k);
@@ -502,7 +500,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
   double sum = 1.0;
   if (a.softmax && (a.bias || !a.normalize)) {
     sum = 0.0;
-    constexpr int kBatch = NPER < 4 ? NPER : 4;
+    constexpr int kBatch = NPER % 4 == 0 ? 4 : NPER % 2 == 0 ? 2 : 1;
 #pragma unroll
     for (int j = 0; j < NPER; j += kBatch) {
       double d[kBatch], w[kBatch];
@@ -566,7 +564,7 @@ template <int NPER>
 __global__ __launch_bounds__(256) void route_groups_fast_kernel(GroupsArgs a, int shift, uint32_t inv_size, int lds_wave) {
   extern __shared__ double lds_scores[];
   const int lane = threadIdx.x & (kWaveSize - 1);
-  const int wave = threadIdx.x / kWaveSize;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
   double* const own = lds_scores + (size_t)wave * lds_wave;
   FastScratch& x = *reinterpret_cast<FastScratch*>(own);
   float* const score = reinterpret_cast<float*>(own + sizeof(FastScratch) / sizeof(double));
@@ -583,7 +581,7 @@ __global__ __launch_bounds__(256) void route_groups_fast_kernel(GroupsArgs a, in
 __global__ __launch_bounds__(256) void route_groups_kernel(GroupsArgs a) {
   extern __shared__ double lds_scores[];
   const int lane = threadIdx.x & (kWaveSize - 1);
-  const int wave = threadIdx.x / kWaveSize;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWaveSize);
   double* const own = lds_scores + (size_t)wave * (sizeof(Few) / sizeof(double) + a.E + a.groups);
   const int waves = blockDim.x / kWaveSize;
   // (a wave's tokens; the kernel has no block-level barrier)
@@ -605,11 +603,16 @@ hipError_t launch_route_groups(const RouteGroupsCall& c, hipStream_t s) {
     const int64_t wgs = (c.T + 3) / 4, wide = wgs < (1 << 20) ? wgs : 1 << 20;  // (a grid dimension has fewer than 2^32 threads)
     const dim3 grid((unsigned)wide, (unsigned)((wgs + wide - 1) / wide));
     auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(4 * kWaveSize), 4 * fast, s, a, shift, inv_size, (int)(fast / sizeof(double))); };
-    if (c.E <= kWaveSize) go(route_groups_fast_kernel<1>);
-    else if (c.E <= 2 * kWaveSize) go(route_groups_fast_kernel<2>);
-    else if (c.E <= 4 * kWaveSize) go(route_groups_fast_kernel<4>);
-    else if (c.E <= 8 * kWaveSize) go(route_groups_fast_kernel<8>);
-    else go(route_groups_fast_kernel<16>);
+    switch ((c.E + 2 * kWaveSize - 1) / (2 * kWaveSize)) {  // experts per lane, in twos
+      case 1: c.E <= kWaveSize ? go(route_groups_fast_kernel<1>) : go(route_groups_fast_kernel<2>); break;
+      case 2: go(route_groups_fast_kernel<4>); break;
+      case 3: go(route_groups_fast_kernel<6>); break;
+      case 4: go(route_groups_fast_kernel<8>); break;
+      case 5: go(route_groups_fast_kernel<10>); break;
+      case 6: go(route_groups_fast_kernel<12>); break;
+      case 7: go(route_groups_fast_kernel<14>); break;
+      default: go(route_groups_fast_kernel<16>); break;
+    }
     return hipGetLastError();
   }
   constexpr size_t kLdsBudget = 64 * 1024;

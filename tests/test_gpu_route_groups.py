@@ -10,7 +10,8 @@ pytestmark = pytest.mark.gpu
 
 # E, groups, keep, k
 SHAPES = [(8, 2, 1, 2), (1, 1, 1, 1), (64, 64, 5, 5), (60, 4, 4, 3), (96, 3, 2, 64), (256, 8, 4, 8), (896, 8, 4, 16), (896, 16, 5, 16), (1000, 125, 30, 24),
-          (1024, 32, 1, 32), (1100, 11, 3, 10), (1540, 20, 7, 24), (5000, 1, 1, 6), (4096, 4096, 40, 40), (130, 130, 64, 64), (62, 31, 30, 33), (8192, 8192, 3, 3), (130, 130, 100, 64), (900, 300, 70, 64)]
+          (1024, 32, 1, 32), (1100, 11, 3, 10), (1540, 20, 7, 24), (5000, 1, 1, 6), (4096, 4096, 40, 40), (130, 130, 64, 64), (62, 31, 30, 33), (8192, 8192, 3, 3), (130, 130, 100, 64), (900, 300, 70, 64),
+          (330, 10, 4, 12), (500, 4, 2, 9), (640, 5, 2, 7), (768, 24, 11, 40)]
 
 
 def check(k3, z, bias, k, groups, keep, what=None, **kw):
