@@ -89,6 +89,9 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float v) {
 // a group split K in pieces of 512, pieces asked for two turns ahead across
 // rounds, partial sums through LDS), with the rows of A, 8 bits an element, in
 // LDS.  Rows that do not fit together go in chunks, side by side in the grid.
+// Bound by the weight bytes: 8 x 33792 x 7168 takes 27 us, 4.8 TB/s of the 5.1 that
+// a copy reaches; of a small product (1 x 3584 x 7168: 7.1 us) by the chain of
+// launch, two turns of loads and the sum over the waves.
 constexpr int kFewWaves = 8;  // at most, per workgroup
 constexpr int kFewRows = 16;
 constexpr int kFewLds = 80 * 1024;     // two workgroups share a CU
@@ -284,6 +287,12 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
 // next are read and split; the barrier of a stage stands between its two halves,
 // when all of it has been read into registers: its buffer is free from there on,
 // and the next stage, whose loads the wave has waited for, is there.
+//
+// Bound, where tiles fill the CUs, by the matrix instructions and the register
+// work of the split beside them: 4096 x 7168 x 7168 260 us, 1.62 PFLOP/s (3.2 of
+// products of 8 bits, each going in twice).  Where they do not, by a stage's chain
+// of L2 latency, barrier, reads and split: 128 x 7168 x 7168 18.5 us, a quarter of
+// the CUs' matrix rate.
 //   kStaged (K a multiple of 512): scales, 16 bytes (four steps) of every row, go
 //     through LDS, too, one load per wave and four steps;
 //   else each lane loads the four scale bytes of its rows for every step, which
@@ -313,7 +322,7 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   constexpr int kStageDw = kSplit * kStepDw;
   constexpr int kLoadsA = kSplit * B / (8 * kWaves), kLoadsW = kSplit * B / (16 * kWaves), kLoads = kLoadsA + kLoadsW;  // 1 KB each, per wave and stage
   constexpr int kGroup = 4 / kSplit;  // stages that a load of scales lasts
-  static_assert((kRing == 2 || kRing == 4) && kGroup >= kRing - 2, "scales land with the stage that they are for");
+  static_assert((kRing == 2 || kRing == 4) && kSplit <= 2 && kGroup >= kRing - 2, "scales land with the stage that they are for");
   // one array per buffer, so that the compiler sees that a read of one buffer
   // does not depend on the loads in flight into the others
   __shared__ __attribute__((aligned(256))) uint32_t l0[kStageDw], l1[kStageDw], l2[kRing > 2 ? kStageDw : 1],
@@ -504,6 +513,29 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   using C0 = std::integral_constant<int, 0>;
   using C1 = std::integral_constant<int, 1>;
 
+  // Order of a half step: the reads, which the compiler would move to where their
+  // data are used, then the matrix instructions with the register work between
+  // them (two first, while the reads are on their way). 128 x 7168 x 7168 takes
+  // 18.5 us with it and 19.4 without, 2048 x 7168 x 7168 in tiles of 128 146 and
+  // 149; tiles of 256 have no registers for it (spills, 149 instead of 130).
+  auto ordered = [&](auto&& reads, auto&& work) {
+    reads();
+    if constexpr (B < 256) {
+      __builtin_amdgcn_sched_barrier(0);
+      work();
+      constexpr int kMfma = 2 * kTm * kTn, kGaps = kMfma > 2 ? kMfma - 2 : 1;
+      __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
+#pragma unroll
+      for (int i = 0; i < kGaps; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x2, (42 * kTm + kGaps - 1) / kGaps, 0);
+        __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    } else {
+      work();
+    }
+  };
+
   // One stage, of which the first half step's operands are in registers: `cur` its
   // buffer, `next` that of the next stage.  Between the halves the loads in flight
   // are those of kRing - 1 stages (and up to two sets of scales); the oldest has to
@@ -513,9 +545,7 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
     constexpr bool kLast = u % kGroup == kGroup - 1;  // of its group
     uint32_t* const sn = (u + 1) / kGroup % 2 ? lsc1 : lsc0;  // the next stage's scales
     Raw n;
-    read(cur, C1{}, n);
-    multiply(C0{});
-    split(n, C1{}, q);
+    ordered([&] { read(cur, C1{}, n); }, [&] { multiply(C0{}); split(n, C1{}, q); });
     wait_vm<(kRing - 2) * kLoads>();
     ring_barrier();
     read_scales(q + 1, sn);
@@ -524,9 +554,7 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
     asm volatile("" ::: "memory");
     issue(q + kRing, cur);
     asm volatile("" ::: "memory");  // the loads go out before the reads below
-    read(next, C0{}, n);
-    multiply(C1{});
-    split(n, C0{}, q + 1);
+    ordered([&] { read(next, C0{}, n); }, [&] { multiply(C1{}); split(n, C0{}, q + 1); });
     take_scales(q + 1);
   };
   {
@@ -565,9 +593,9 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   }
   wait_vm<0>();  // no load into LDS outlives the workgroup
 
-  if constexpr (kSplit > 1) {  // the other sets' sums through LDS, in order, an operand tile at a time
-    static_assert(kSplit == 2 && kSet * 1024 <= kStageDw, "a set's operand tiles fit a buffer");
-    float* const red = reinterpret_cast<float*>(l0);
+  if constexpr (kSplit == 2) {  // the second set's sums through LDS, an operand tile at a time
+    static_assert(kSet * 1024 <= kStageDw, "the set's operand tiles fit a buffer");
+    float* const red = reinterpret_cast<float*>(l0) + (wave % kSet) * 1024 + 4 * lane;
 #pragma unroll
     for (int i = 0; i < kTm; ++i)
 #pragma unroll
@@ -575,17 +603,18 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
         __syncthreads();
         if (ks == 1)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) *reinterpret_cast<f32x4*>(red + (wave % kSet) * 1024 + 256 * v + 4 * lane) = f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+          for (int v = 0; v < 4; ++v)
+            *reinterpret_cast<f32x4*>(red + 256 * v) = f32x4{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
         __syncthreads();
         if (ks == 0)
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            const f32x4 o = *reinterpret_cast<const f32x4*>(red + (wave % kSet) * 1024 + 256 * v + 4 * lane);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(red + 256 * v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][j][4 * v + e] += o[e];
+            for (int e = 0; e < 4; ++e) acc[i][j][4 * v + e] += x[e];
           }
       }
-    if (ks != 0) return;
+    if (ks == 1) return;
   }
 
   // lane holds column n = lane % 32, rows 8 * (v / 4) + 4 * h + v % 4
@@ -682,22 +711,21 @@ hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t
   if (M <= kFewRows && fit_all >= 1) return launch_few(f, fit_all, false, out_bf16, s);
   if (K >= 4096 && fit >= 4 && (M + fit - 1) / fit * wgs <= 2 * cus) return launch_few(f, fit, true, out_bf16, s);
   const TileArgs t{a, as, w, ws, (int)M, N, nb, out};
-  // The tile side whose workgroups take the least time together.  A tile's time, in
-  // units of a 64 x 64 one that has a CU to itself (20 us at K = 7168: eight waves,
-  // each step of K another four's): 2.15 for 128 x 128 and 6.2 for 256 x 256.
-  // Several smaller ones share a CU, at 0.9 each (four waves then) and 2.1, two of
-  // them at no less than 1.6 and 3.6.  With `each` tiles per CU: 256 x 7168 x
-  // 7168, 448 tiles of 64, 33 us (128: 43); 512 x 7168 x 7168, 224 tiles of 128, 45
-  // us (64: 62); 2048 x 7168 x 7168, 224 tiles of 256, 129 us (128: 158).
-  auto each = [&](int B) { return (double)mx_tile_grid(t.M, N, B).total / (double)cus; };
-  const double e64 = each(64), e128 = each(128), e256 = each(256);
-  const double c64 = e64 <= 1.0 ? 1.0 : 0.9 * (e64 > 1.8 ? e64 : 1.8);
-  const double c128 = e128 <= 1.0 ? 2.15 : 2.1 * (e128 > 1.7 ? e128 : 1.7);
-  const double c256 = 6.2 * ceil(e256);
+  // The tile side whose workgroups take the least time together, n of them on the
+  // CU with the most, in units of one 64 x 64 tile that has a CU to itself (18.6 us
+  // at K = 7168; with four buffers, which leave a CU no room for more than that
+  // one).  Where there are more of those, two buffers: 2 tiles of 64 take 28 us, 3
+  // 40, 4 51, 14 178, one of 128 43 (2 69 to 82, 4 147), one of 256 126 to 131.
+  // So 384 x 7168 x 7168 takes tiles of 64 (40 us, not 42), 512 x 7168 x 7168 of 128
+  // (43, not 51), 1536 x 7168 x 7168 of 128 (113, not 127), 2048 x 7168 x 7168 of
+  // 256 (131, not 147).
+  auto each = [&](int B) { return (double)((mx_tile_grid(t.M, N, B).total + cus - 1) / cus); };
+  const double n64 = each(64), n128 = each(128), n256 = each(256);
+  const double c64 = n64 <= 1 ? 1.0 : 0.2 + 0.65 * n64, c128 = n128 <= 1 ? 2.3 : 0.4 + 1.95 * n128, c256 = 7.0 * n256;
   if (nb % 16 == 0 && c256 < c128 && c256 < c64) return launch_square<256, 4, 2, 1, 2>(t, out_bf16, s);
-  if (c128 < c64) return launch_square<128, 4, 2, 1, 2>(t, out_bf16, s);
-  if (e64 <= 1.0) return launch_square<64, 2, 2, 2, 4>(t, out_bf16, s);
-  return launch_square<64, 2, 2, 1, 4>(t, out_bf16, s);
+  if (c128 < c64) return launch_square<128, 4, 1, 1, 2>(t, out_bf16, s);
+  if (n64 <= 1) return launch_square<64, 2, 1, 2, 4>(t, out_bf16, s);
+  return launch_square<64, 2, 1, 2, 2>(t, out_bf16, s);
 }
 
 }  // namespace k3moe
