@@ -291,7 +291,7 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
 // Bound, where tiles fill the CUs, by the matrix instructions and the register
 // work of the split beside them: 4096 x 7168 x 7168 260 us, 1.62 PFLOP/s (3.2 of
 // products of 8 bits, each going in twice).  Where they do not, by a stage's chain
-// of L2 latency, barrier, reads and split: 128 x 7168 x 7168 18.5 us, a quarter of
+// of L2 latency, barrier, reads and split: 128 x 7168 x 7168 17.7 us, a quarter of
 // the CUs' matrix rate.
 //   kStaged (K a multiple of 512): scales, 16 bytes (four steps) of every row, go
 //     through LDS, too, one load per wave and four steps;
@@ -516,8 +516,8 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   // Order of a half step: the reads, which the compiler would move to where their
   // data are used, then the matrix instructions with the register work between
   // them (two first, while the reads are on their way). 128 x 7168 x 7168 takes
-  // 18.5 us with it and 19.4 without, 2048 x 7168 x 7168 in tiles of 128 146 and
-  // 149; tiles of 256 have no registers for it (spills, 149 instead of 130).
+  // 0.9 us less with it than without, of 19.4, 2048 x 7168 x 7168 in tiles of 128 146
+  // us and not 149; tiles of 256 have no registers for it (spills, 149 instead of 130).
   auto ordered = [&](auto&& reads, auto&& work) {
     reads();
     if constexpr (B < 256) {
@@ -617,19 +617,23 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
     if (ks == 1) return;
   }
 
-  // lane holds column n = lane % 32, rows 8 * (v / 4) + 4 * h + v % 4
+  // lane holds column n = lane % 32, rows 8 * (v / 4) + 4 * h + v % 4; a whole tile's need no test each
+  const int64_t o0 = (m0 + wm * (B / kWm) + 4 * h) * (int64_t)t.N + n0 + wn * (B / kWn) + r32;
+  auto store = [&](auto whole) {
 #pragma unroll
-  for (int i = 0; i < kTm; ++i)
+    for (int i = 0; i < kTm; ++i)
 #pragma unroll
-    for (int j = 0; j < kTn; ++j) {
-      const int n = wn * (B / kWn) + 32 * j + r32;
-      if (n >= nrows) continue;
+      for (int j = 0; j < kTn; ++j) {
+        if (!decltype(whole)::value && wn * (B / kWn) + 32 * j + r32 >= nrows) continue;
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int m = wm * (B / kWm) + 32 * i + 8 * (v >> 2) + 4 * h + (v & 3);
-        if (m < mrows) store_out<kBf16>(t.out, (m0 + m) * (int64_t)t.N + n0 + n, acc[i][j][v]);
+        for (int v = 0; v < 16; ++v) {
+          const int m = 32 * i + 8 * (v >> 2) + (v & 3);
+          if (decltype(whole)::value || wm * (B / kWm) + 4 * h + m < mrows) store_out<kBf16>(t.out, o0 + (int64_t)m * t.N + 32 * j, acc[i][j][v]);
+        }
       }
-    }
+  };
+  if (mrows == B && nrows == B) store(std::true_type{});
+  else store(std::false_type{});
 }
 
 // LDS bytes of the few-row kernel: rows of codes (an odd number of 16-byte
@@ -712,16 +716,16 @@ hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t
   if (K >= 4096 && fit >= 4 && (M + fit - 1) / fit * wgs <= 2 * cus) return launch_few(f, fit, true, out_bf16, s);
   const TileArgs t{a, as, w, ws, (int)M, N, nb, out};
   // The tile side whose workgroups take the least time together, n of them on the
-  // CU with the most, in units of one 64 x 64 tile that has a CU to itself (18.6 us
+  // CU with the most, in units of one 64 x 64 tile that has a CU to itself (17.7 us
   // at K = 7168; with four buffers, which leave a CU no room for more than that
   // one).  Where there are more of those, two buffers: 2 tiles of 64 take 28 us, 3
-  // 40, 4 51, 14 178, one of 128 43 (2 69 to 82, 4 147), one of 256 126 to 131.
+  // 40, 4 51, 9 115, 14 178, one of 128 42 (2 69 to 82, 3 110, 4 147), one of 256 126 to 131.
   // So 384 x 7168 x 7168 takes tiles of 64 (40 us, not 42), 512 x 7168 x 7168 of 128
-  // (43, not 51), 1536 x 7168 x 7168 of 128 (113, not 127), 2048 x 7168 x 7168 of
-  // 256 (131, not 147).
+  // (42, not 51), 1280 x 7168 x 7168 of 128 (109, not 115), 1536 x 7168 x 7168 of 128
+  // (111, not 127), 2048 x 7168 x 7168 of 256 (131, not 147).
   auto each = [&](int B) { return (double)((mx_tile_grid(t.M, N, B).total + cus - 1) / cus); };
   const double n64 = each(64), n128 = each(128), n256 = each(256);
-  const double c64 = n64 <= 1 ? 1.0 : 0.2 + 0.65 * n64, c128 = n128 <= 1 ? 2.3 : 0.4 + 1.95 * n128, c256 = 7.0 * n256;
+  const double c64 = n64 <= 1 ? 1.0 : 0.15 + 0.7 * n64, c128 = n128 <= 1 ? 2.4 : 0.3 + 2.0 * n128, c256 = 7.0 * n256;
   if (nb % 16 == 0 && c256 < c128 && c256 < c64) return launch_square<256, 4, 2, 1, 2>(t, out_bf16, s);
   if (c128 < c64) return launch_square<128, 4, 1, 1, 2>(t, out_bf16, s);
   if (n64 <= 1) return launch_square<64, 2, 1, 2, 4>(t, out_bf16, s);
