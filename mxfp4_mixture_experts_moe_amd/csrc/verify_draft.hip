@@ -359,8 +359,10 @@ __global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
   __shared__ double part[kWaves], own_mass, sh_target, sh_before;
   __shared__ int sh_count, sh_last, sh_found, sh_residual, wat[kWaves], wlast[kWaves];
   const unsigned wgs = kProbs ? (unsigned)(a.chunks + kPer - 1) / (unsigned)(kProbs ? kPer : 1) : 1u;  // of a sequence
-  const int64_t s = blockIdx.x / wgs;
-  const int c = (int)(blockIdx.x - s * wgs);
+  const unsigned id = blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t s = id / wgs;
+  if (s >= a.S) return;
+  const int c = (int)(id - s * wgs);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int W = a.W, V = a.V, D = W - 1;
   const bool greedy = greedy_of(a, s);
@@ -590,7 +592,9 @@ hipError_t launch_verify_draft(const VerifyDraftCall& c, hipStream_t s) {
   // Chunks of a workgroup of the second launch: each takes the proposals' test
   // first, so four where that still leaves a workgroup for every CU.
   const int per = !c.q ? 0 : c.S * ((l.chunks + 3) / 4) >= device_cu_count() ? 4 : 1;
-  const dim3 g1((unsigned)(c.S * c.W * l.chunks)), g2((unsigned)(c.S * (per ? (l.chunks + per - 1) / per : 1)));
+  const unsigned wgs = (unsigned)(c.S * (per ? (l.chunks + per - 1) / per : 1));
+  const unsigned rows = 1 + (wgs >> 22);  // (a grid dimension has fewer than 2^32 threads)
+  const dim3 g1((unsigned)(c.S * c.W * l.chunks)), g2((wgs + rows - 1) / rows, rows);
   auto go = [&](auto type) -> hipError_t {
     constexpr int kType = decltype(type)::value;
     hipLaunchKernelGGL(stats_kernel<kType>, g1, dim3(kThreads), 0, s, a);

@@ -117,3 +117,17 @@ def test_long_verification_and_routing(k3):
     ids, w = k3.moe_route_groups(z, None, 16, 16, 5, score="softmax")
     li, lw = k3.moe_route_groups(z.repeat(5000, 1), None, 16, 16, 5, score="softmax")
     assert torch.equal(li, ids.repeat(5000, 1)) and torch.equal(lw, w.repeat(5000, 1))
+
+
+def test_most_sequences(k3):
+    """2^24 - 1 sequences of one row of two entries: the first where the uniform is below its probability (fp64, apart by more
+    than rounding: uniforms are multiples of 2^-24, p0 of 16-bit logits)."""
+    S = 2**24 - 1
+    l = torch.randn((S, 1, 2), device="cuda").half()
+    u = torch.rand((S,), device="cuda")
+    n, t, a = k3.moe_verify_draft(l, None, None, u)
+    p0 = torch.softmax(l.double(), -1)[:, 0, 0]
+    clear = (u.double() - p0).abs() > 1e-12
+    assert torch.equal(t[clear, 0], (u >= p0)[clear].int()) and int(n.abs().max()) == 0 and clear.float().mean() > 0.999
+    with pytest.raises(k3.K3MoeError):
+        k3.moe_verify_draft(torch.zeros((2**24, 1, 1), device="cuda"), None, None, torch.zeros(2**24, device="cuda"))
