@@ -208,14 +208,28 @@ __device__ __forceinline__ int wave_min(int v, int lane) {
   six_steps([&](auto k) { v = min(v, (int)partner<decltype(k)::value>((uint32_t)v, lane)); });
   return v;
 }
-// Sum over the lanes up to this one.
-__device__ __forceinline__ double wave_scan(double v, int lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double o = __shfl_up(v, d, 64);
-    if (lane >= d) v += o;
-  }
+// Value of another lane by DPP, 0 where there is none.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double moved(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, kCtrl, kRows, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), kCtrl, kRows, 0xF, false);
+  return __longlong_as_double((long long)((uint64_t)hi << 32 | lo));
+}
+// Sum over the lanes up to this one: inside rows of 16, then the rows before.
+__device__ __forceinline__ double wave_scan(double v) {
+  v += moved<0x111, 0xF>(v);  // lane - 1 of the row
+  v += moved<0x112, 0xF>(v);
+  v += moved<0x114, 0xF>(v);
+  v += moved<0x118, 0xF>(v);
+  v += moved<0x142, 0xA>(v);  // the last lane of the row before, in rows 1 and 3
+  v += moved<0x143, 0xC>(v);  // lane 31, in rows 2 and 3
   return v;
+}
+__device__ __forceinline__ double lane_before(double v) { return moved<0x138, 0xF>(v); }
+__device__ __forceinline__ double last_lane(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63)));
 }
 
 __device__ __forceinline__ bool greedy_of(const VerifyArgs& a, int64_t s) { return a.temperature && !(a.temperature[s] > 0.0f); }
@@ -474,31 +488,32 @@ __global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
       if (residual && i == own) return own_mass;
       return cs[i].z * weight(cs[i].m, d.sc) * d.inv_z;
     };
-    auto total_of = [&]() {
-      double v = 0.0;
-      for (int i = lane; i < a.chunks; i += 64) v += share(i);
-      return wave_sum(v, lane);
-    };
-    double total = total_of();
-    if (residual && !(total > 0.0)) {  // p nowhere above q: p itself
-      residual = false;
-      total = total_of();
+    double total, v, incl;  // (v, incl: the first 64 chunks', of which most rows have no more)
+    for (;;) {
+      v = share(lane);
+      incl = wave_scan(v);
+      total = last_lane(incl);
+      for (int i0 = 64; i0 < a.chunks; i0 += 64) total += last_lane(wave_scan(share(i0 + lane)));
+      if (!residual || total > 0.0) break;
+      residual = false;  // p nowhere above q: p itself
     }
     const double target = u * total;
     int found = -1;
     double base = 0.0, before = 0.0;
-    for (int i0 = 0; i0 < a.chunks; i0 += 64) {
-      const double v = share(i0 + lane);
-      const double incl = base + wave_scan(v, lane);
-      const double prev = __shfl_up(incl, 1, 64), excl = lane ? prev : base;
-      const uint64_t any = __builtin_amdgcn_ballot_w64(v > 0.0), over = __builtin_amdgcn_ballot_w64(v > 0.0 && incl > target);
+    for (int i0 = 0;;) {
+      const double prev = lane_before(incl), excl = base + prev;
+      const uint64_t any = __builtin_amdgcn_ballot_w64(v > 0.0), over = __builtin_amdgcn_ballot_w64(v > 0.0 && base + incl > target);
       if (any) {
         const int at = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(any);
         found = i0 + at;
         before = __shfl(excl, at, 64);
       }
       if (over) break;
-      base = __shfl(incl, 63, 64);
+      base += last_lane(incl);
+      i0 += 64;
+      if (i0 >= a.chunks) break;
+      v = share(i0 + lane);
+      incl = wave_scan(v);
     }
     if (lane == 0) {
       sh_found = found;
@@ -522,13 +537,12 @@ __global__ __launch_bounds__(kChooseThreads) void choose_kernel(VerifyArgs a) {
   for (int i = 0; i < kEach; i += kVec<kType>) entries16<kType>(d, row, b0 + i, V, (f + 1) * kVocabChunk <= V, e + i);
 #pragma unroll
   for (int i = 0; i < kEach; ++i) mine += e[i];
-  const double incl = wave_scan(mine, lane);
+  const double incl = wave_scan(mine);
   if (lane == 63) part[wave] = incl;
   __syncthreads();
   double sum = sh_before;
   for (int i = 0; i < wave; ++i) sum += part[i];
-  const double prev = __shfl_up(incl, 1, 64);
-  sum += lane ? prev : 0.0;
+  sum += lane_before(incl);
   int at = INT_MAX, last = -1;  // first entry over the target; last one that holds anything
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
