@@ -3,7 +3,8 @@
 //
 // Scale rule as in quant.hip (OCP Microscaling Formats specification 1.0,
 // section 6.3) with E4M3 elements.  A lane owns eight consecutive elements and
-// four neighbouring lanes hold one block, as there.
+// four neighbouring lanes hold one block, as there.  Bound by the bytes:
+// 16384 x 7168 bf16 are rounded in 64 us, 5.6 TB/s, and decoded in 50 to 57.
 #include "mx8_common.h"
 
 #include <type_traits>
@@ -109,6 +110,11 @@ unsigned copy_grid(int64_t units) {
 // shifted by one, and whether the lower word holds anything ("key").
 //
 // A row stays in the registers of its threads between the sum and the rounding.
+//
+// Bound by the bytes where rows are many: 16384 x 7168 bf16 with residual and sum,
+// 826 MB, 178 us, 4.6 TB/s (fp64 throughout and rows read twice: 368 us), with
+// y 218, f32 278 and 367 (5.5 TB/s); one row of 7168 takes 4.6 to 5 us, the chain
+// of loads, sum over the workgroup, root, division and rounding.
 
 constexpr int64_t kMaxGroups = 1 << 20;  // workgroups of a launch (a grid dimension has fewer than 2^32 threads)
 
@@ -448,7 +454,8 @@ void norm_launch(NormArgs a, hipStream_t s) {
     return;
   }
   // Few rows: as many threads as there are units.  Rows for every CU: more units
-  // a thread, so that several small workgroups, each at its own stage, share a CU.
+  // a thread, so that several small workgroups, each at its own stage, share a CU
+  // (16384 x 7168 bf16, one, two or four units a thread: 286, 205, 178 us).
   constexpr int kMost = kType == K3MOE_DTYPE_F32 ? 2 : 4;
   const int want = a.R <= device_cu_count() ? 1 : (a.units + 63) / 64;
   int per = 1;

@@ -90,7 +90,7 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float v) {
 // rounds, partial sums through LDS), with the rows of A, 8 bits an element, in
 // LDS.  Rows that do not fit together go in chunks, side by side in the grid.
 // Bound by the weight bytes: 8 x 33792 x 7168 takes 27 us, 4.8 TB/s of the 5.1 that
-// a copy reaches; of a small product (1 x 3584 x 7168: 7.1 us) by the chain of
+// a copy reaches; of a small product (1 x 3584 x 7168: 6.9 us) by the chain of
 // launch, two turns of loads and the sum over the waves.
 constexpr int kFewWaves = 8;  // at most, per workgroup
 constexpr int kFewRows = 16;
