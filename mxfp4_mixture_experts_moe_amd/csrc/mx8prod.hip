@@ -21,7 +21,7 @@
 // + 16 g of the G blocks.  The scale of a lane group is block g's for both.
 //
 // Two kernels, as for the 4-bit products (mxprod.hip): few rows, bound by the
-// weight bytes, and square tiles through a ring of LDS buffers.
+// weight bytes, and tiles through a ring of LDS buffers.
 #include "mx_common.h"
 #include "mx_shape.h"
 
@@ -275,7 +275,7 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
 }
 
 // ---------------------------------------------------------------------------
-// Tiles.  A workgroup owns a B x B tile of C; kWm x kWn waves share it, and kSplit
+// Tiles.  A workgroup owns a BM x BN tile of C; kWm x kWn waves share it, and kSplit
 // such sets of waves take the steps of K (128: four blocks, 128 bytes of a row of
 // A, 64 of W) in turn, each with sums of its own that are added at the end.  A
 // stage is kSplit steps; stages go through a ring of kRing LDS buffers filled by
@@ -290,9 +290,9 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
 //
 // Bound, where tiles fill the CUs, by the matrix instructions and the register
 // work of the split beside them: 4096 x 7168 x 7168 260 us, 1.62 PFLOP/s (3.2 of
-// products of 8 bits, each going in twice).  Where they do not, by a stage's chain
-// of L2 latency, barrier, reads and split: 128 x 7168 x 7168 17.7 us, a quarter of
-// the CUs' matrix rate.
+// products of 8 bits, each going in twice).  Where they do not, by what a CU gets
+// from its L2, 18 to 20 bytes a clock: 128 x 7168 x 7168 17.7 us, a quarter of the
+// matrix rate.
 //   kStaged (K a multiple of 512): scales, 16 bytes (four steps) of every row, go
 //     through LDS, too, one load per wave and four steps;
 //   else each lane loads the four scale bytes of its rows for every step, which
@@ -314,13 +314,13 @@ __device__ __forceinline__ void wait_vm() {
 // refilled after it) and its loads of the next stage's buffer have landed.
 __device__ __forceinline__ void ring_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <int B, int kWm, int kWn, int kSplit, int kRing, bool kStaged, bool kBf16>
+template <int BM, int BN, int kWm, int kWn, int kSplit, int kRing, bool kStaged, bool kBf16>
 __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileArgs t) {
   constexpr int kSet = kWm * kWn, kWaves = kSet * kSplit;
-  constexpr int kTm = B / (32 * kWm), kTn = B / (32 * kWn);  // 32-row operand tiles per wave
-  constexpr int kADw = B * 32, kStepDw = B * 48;  // dwords of a step's rows of A; and of W behind them
+  constexpr int kTm = BM / (32 * kWm), kTn = BN / (32 * kWn);  // 32-row operand tiles per wave
+  constexpr int kADw = BM * 32, kStepDw = kADw + BN * 16;  // dwords of a step's rows of A; and of W behind them
   constexpr int kStageDw = kSplit * kStepDw;
-  constexpr int kLoadsA = kSplit * B / (8 * kWaves), kLoadsW = kSplit * B / (16 * kWaves), kLoads = kLoadsA + kLoadsW;  // 1 KB each, per wave and stage
+  constexpr int kLoadsA = kSplit * BM / (8 * kWaves), kLoadsW = kSplit * BN / (16 * kWaves), kLoads = kLoadsA + kLoadsW;  // 1 KB each, per wave and stage
   constexpr int kGroup = 4 / kSplit;  // stages that a load of scales lasts
   static_assert((kRing == 2 || kRing == 4) && kSplit <= 2 && kGroup >= kRing - 2, "scales land with the stage that they are for");
   // one array per buffer, so that the compiler sees that a read of one buffer
@@ -334,7 +334,7 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
 
   // Tile order: the ids an XCD gets (id % 8) are a contiguous run of the
   // logical order, which walks groups of four tile rows column by column.
-  const int mt = mx_groups(t.M, B), nt = mx_groups(t.N, B);
+  const int mt = mx_groups(t.M, BM), nt = mx_groups(t.N, BN);
   const int64_t total = (int64_t)mt * nt;
   int64_t id = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
   if (id >= total) return;
@@ -345,30 +345,29 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   constexpr int kGm = 4;
   const int64_t grp = id / ((int64_t)kGm * nt), in = id - grp * kGm * nt;
   const int gm = mt - (int)grp * kGm < kGm ? mt - (int)grp * kGm : kGm;
-  const int64_t m0 = (grp * kGm + in % gm) * B;
-  const int n0 = (int)(in / gm) * B;
+  const int64_t m0 = (grp * kGm + in % gm) * BM;
+  const int n0 = (int)(in / gm) * BN;
 
   const int nb = t.nb;
   const uint32_t arowb = (uint32_t)nb * 32, wrowb = (uint32_t)nb * 16;
-  const int mrows = t.M - m0 < B ? (int)(t.M - m0) : B;
-  const int nrows = t.N - n0 < B ? t.N - n0 : B;
+  const int mrows = t.M - m0 < BM ? (int)(t.M - m0) : BM;
+  const int nrows = t.N - n0 < BN ? t.N - n0 : BN;
   const int nsteps = (nb + 3) >> 2, nstages = (nsteps + kSplit - 1) / kSplit;
 
   // position of 16-byte chunk c in LDS row r
   auto place_a = [](int c, int r) { return c ^ ((r >> 1) & 7); };
   auto place_w = [](int c, int r) { return c ^ ((r >> 2) & 3); };
-  // loads: wave w fills rows (w % kSet) * B / kSet .. of step w / kSet of a stage
-  constexpr int kRows = B / kSet;
-  const int lrow0 = wave % kSet * kRows;
+  // loads: wave w fills the (w % kSet)-th part of the rows of step w / kSet of a stage
+  const int arow0 = wave % kSet * (BM / kSet), wrow0 = wave % kSet * (BN / kSet);
   uint32_t aoff[kLoadsA], woff[kLoadsW];
 #pragma unroll
   for (int j = 0; j < kLoadsA; ++j) {
-    const int r = lrow0 + 8 * j + lane / 8;
+    const int r = arow0 + 8 * j + lane / 8;
     aoff[j] = (uint32_t)min(r, mrows - 1) * arowb + 16 * place_a(lane % 8, r);
   }
 #pragma unroll
   for (int j = 0; j < kLoadsW; ++j) {
-    const int r = lrow0 + 16 * j + lane / 4;
+    const int r = wrow0 + 16 * j + lane / 4;
     woff[j] = (uint32_t)min(r, nrows - 1) * wrowb + 16 * place_w(lane % 4, r);
   }
   // (steps past K are outside the buffers: zeros that cost no traffic)
@@ -377,8 +376,8 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(t.a + m0 * arowb), 0, step < nsteps ? (int)(mrows * arowb) : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rw =
         __builtin_amdgcn_make_buffer_rsrc((void*)(t.w + (int64_t)n0 * wrowb), 0, step < nsteps ? (int)(nrows * wrowb) : 0, 0x00020000);
-    uint32_t* const da = buf + ks * kStepDw + lrow0 * 32;
-    uint32_t* const dw = buf + ks * kStepDw + kADw + lrow0 * 16;
+    uint32_t* const da = buf + ks * kStepDw + arow0 * 32;
+    uint32_t* const dw = buf + ks * kStepDw + kADw + wrow0 * 16;
     const int sa = __builtin_amdgcn_readfirstlane(128 * step), sw = __builtin_amdgcn_readfirstlane(64 * step);
 #pragma unroll
     for (int j = 0; j < kLoadsA; ++j) {
@@ -393,14 +392,14 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   };
 
   // Scales.  kStaged: 16 bytes (four steps) of each of the tile's rows through LDS
-  constexpr int kScaleLoads = 2 * B / 64;  // of 64 rows; one per wave (some twice where there are more waves)
+  constexpr int kScaleA = (BM + 63) / 64, kScaleLoads = kScaleA + BN / 64;  // of 64 rows; one per wave (some twice where there are more waves)
   static_assert(kScaleLoads <= kWaves, "every wave does one load of scales");
-  __shared__ __attribute__((aligned(256))) uint32_t lsc0[kStaged ? 2 * B * 4 : 1], lsc1[kStaged ? 2 * B * 4 : 1];  // (of even groups, of odd ones)
+  __shared__ __attribute__((aligned(256))) uint32_t lsc0[kStaged ? kScaleLoads * 256 : 1], lsc1[kStaged ? kScaleLoads * 256 : 1];  // (of even groups, of odd ones)
   const int sload = wave % kScaleLoads;
-  const bool s_a = sload < kScaleLoads / 2;
+  const bool s_a = sload < kScaleA;
   const int slrows = s_a ? mrows : nrows;
   const __amdgpu_buffer_rsrc_t rsc = __builtin_amdgcn_make_buffer_rsrc((void*)(s_a ? t.as + m0 * nb : t.ws + (int64_t)n0 * nb), 0, slrows * nb, 0x00020000);
-  const int svoff = min(sload % (kScaleLoads / 2) * 64 + lane, slrows - 1) * nb;
+  const int svoff = min((s_a ? sload : sload - kScaleA) * 64 + lane, slrows - 1) * nb;
   auto issue_scales = [&](int group, uint32_t* buf) {
     uint32_t* dst = buf + sload * 256;
     const int so = 16 * min(group, (nb >> 4) - 1), vo = svoff;  // (past the last: that again, not used)
@@ -410,9 +409,9 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   const uint8_t *ap[kTm], *wp[kTn];
   if constexpr (!kStaged) {
 #pragma unroll
-    for (int i = 0; i < kTm; ++i) ap[i] = t.as + (m0 + min(wm * (B / kWm) + 32 * i + r32, mrows - 1)) * nb;
+    for (int i = 0; i < kTm; ++i) ap[i] = t.as + (m0 + min(wm * (BM / kWm) + 32 * i + r32, mrows - 1)) * nb;
 #pragma unroll
-    for (int i = 0; i < kTn; ++i) wp[i] = t.ws + (int64_t)(n0 + min(wn * (B / kWn) + 32 * i + r32, nrows - 1)) * nb;
+    for (int i = 0; i < kTn; ++i) wp[i] = t.ws + (int64_t)(n0 + min(wn * (BN / kWn) + 32 * i + r32, nrows - 1)) * nb;
   }
   auto scale4 = [&](const uint8_t* row, int step) -> uint32_t {
     if (nb < 4) return load_tail(row, min(4 * step, nb), nb);
@@ -432,9 +431,9 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
     if constexpr (kStaged) {
       const uint32_t* const l = buf + (step & 3);
 #pragma unroll
-      for (int i = 0; i < kTm; ++i) na[i] = l[4 * (wm * (B / kWm) + 32 * i + r32)];
+      for (int i = 0; i < kTm; ++i) na[i] = l[4 * (wm * (BM / kWm) + 32 * i + r32)];
 #pragma unroll
-      for (int i = 0; i < kTn; ++i) nw[i] = l[4 * (B + wn * (B / kWn) + 32 * i + r32)];
+      for (int i = 0; i < kTn; ++i) nw[i] = l[4 * (kScaleA * 64 + wn * (BN / kWn) + 32 * i + r32)];
     } else {
 #pragma unroll
       for (int i = 0; i < kTm; ++i) na[i] = scale4(ap[i], step);
@@ -460,8 +459,8 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
 #pragma unroll
     for (int j = 0; j < kTn; ++j) acc[i][j] = f32x16{};
 
-  const uint32_t arow = (uint32_t)ks * kStepDw * 4 + (uint32_t)(wm * (B / kWm) + r32) * 128;
-  const uint32_t wrow = (uint32_t)(ks * kStepDw + kADw) * 4 + (uint32_t)(wn * (B / kWn) + r32) * 64;
+  const uint32_t arow = (uint32_t)ks * kStepDw * 4 + (uint32_t)(wm * (BM / kWm) + r32) * 128;
+  const uint32_t wrow = (uint32_t)(ks * kStepDw + kADw) * 4 + (uint32_t)(wn * (BN / kWn) + r32) * 64;
   // Operands of an instruction: as read, and split.
   struct Raw {
     mx_u32x4 a[kTm][2], w[kTn];
@@ -520,7 +519,7 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   // us and not 149; tiles of 256 have no registers for it (spills, 149 instead of 130).
   auto ordered = [&](auto&& reads, auto&& work) {
     reads();
-    if constexpr (B < 256) {
+    if constexpr (BM < 256) {
       __builtin_amdgcn_sched_barrier(0);
       work();
       constexpr int kMfma = 2 * kTm * kTn, kGaps = kMfma > 2 ? kMfma - 2 : 1;
@@ -618,21 +617,21 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   }
 
   // lane holds column n = lane % 32, rows 8 * (v / 4) + 4 * h + v % 4; a whole tile's need no test each
-  const int64_t o0 = (m0 + wm * (B / kWm) + 4 * h) * (int64_t)t.N + n0 + wn * (B / kWn) + r32;
+  const int64_t o0 = (m0 + wm * (BM / kWm) + 4 * h) * (int64_t)t.N + n0 + wn * (BN / kWn) + r32;
   auto store = [&](auto whole) {
 #pragma unroll
     for (int i = 0; i < kTm; ++i)
 #pragma unroll
       for (int j = 0; j < kTn; ++j) {
-        if (!decltype(whole)::value && wn * (B / kWn) + 32 * j + r32 >= nrows) continue;
+        if (!decltype(whole)::value && wn * (BN / kWn) + 32 * j + r32 >= nrows) continue;
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
           const int m = 32 * i + 8 * (v >> 2) + (v & 3);
-          if (decltype(whole)::value || wm * (B / kWm) + 4 * h + m < mrows) store_out<kBf16>(t.out, o0 + (int64_t)m * t.N + 32 * j, acc[i][j][v]);
+          if (decltype(whole)::value || wm * (BM / kWm) + 4 * h + m < mrows) store_out<kBf16>(t.out, o0 + (int64_t)m * t.N + 32 * j, acc[i][j][v]);
         }
       }
   };
-  if (mrows == B && nrows == B) store(std::true_type{});
+  if (mrows == BM && nrows == BN) store(std::true_type{});
   else store(std::false_type{});
 }
 
@@ -647,17 +646,17 @@ int few_rows(int nb, int lds) {
   return r < kFewRows ? r : kFewRows;
 }
 
-template <int B, int kWm, int kWn, int kSplit, int kRing>
-hipError_t launch_square(const TileArgs& t, bool bf16, hipStream_t s) {
-  const MxTileGrid g = mx_tile_grid(t.M, t.N, B);
+template <int BM, int BN, int kWm, int kWn, int kSplit, int kRing>
+hipError_t launch_tiles(const TileArgs& t, bool bf16, hipStream_t s) {
+  const MxTileGrid g = mx_tile_grid(t.M, t.N, BM, BN);
   const dim3 grid(g.x, g.y), block(kWm * kWn * kSplit * 64);
   auto go = [&](auto st, auto b) {
-    hipLaunchKernelGGL((mx8_tile_kernel<B, kWm, kWn, kSplit, kRing, decltype(st)::value, decltype(b)::value>), grid, block, 0, s, t);
+    hipLaunchKernelGGL((mx8_tile_kernel<BM, BN, kWm, kWn, kSplit, kRing, decltype(st)::value, decltype(b)::value>), grid, block, 0, s, t);
   };
   const bool staged = t.nb % 16 == 0;
   if (staged && bf16) go(std::true_type{}, std::true_type{});
   else if (staged) go(std::true_type{}, std::false_type{});
-  else if constexpr (B < 256) {  // (the registers of the largest do not hold the scales of ragged rows, too)
+  else if constexpr (BM < 256) {  // (the registers of the largest do not hold the scales of ragged rows, too)
     if (bf16) go(std::false_type{}, std::true_type{});
     else go(std::false_type{}, std::false_type{});
   }
@@ -717,21 +716,29 @@ hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t
   if (M <= kFewRows && fit_all >= 1) return launch_few(f, fit_all, false, out_bf16, s);
   if (K > 512 && fit >= 4 && (M + fit - 1) / fit * wgs <= 2 * cus) return launch_few(f, fit, true, out_bf16, s);
   const TileArgs t{a, as, w, ws, (int)M, N, nb, out};
-  // The tile side whose workgroups take the least time together, n of them on the
-  // CU with the most, in units of one 64 x 64 tile that has a CU to itself (17.7 us
-  // at K = 7168; with four buffers, which leave a CU no room for more than that
+  // Tiles of 32 x 64 where there are no more of them than CUs (what a CU gets from
+  // the L2 bounds such a product: 16 KB a stage, not the 24 of 64 x 64; 32 x 7168 x
+  // 3584 8.7 us, not 11.1, 64 x 7168 x 3584 8.8, not 10.7), and for up to 32 rows
+  // (with two buffers, as there are several on a CU: 32 x 33792 x 7168 32 us, 39 in
+  // tiles of 64).
+  const int64_t narrow = mx_tile_grid(t.M, N, 32, 64).total;
+  if (narrow <= cus) return launch_tiles<32, 64, 1, 2, 2, 4>(t, out_bf16, s);
+  if (M <= 32) return launch_tiles<32, 64, 1, 2, 2, 2>(t, out_bf16, s);
+  // Else the tile side whose workgroups take the least time together, n of them on
+  // the CU with the most, in units of one 64 x 64 tile that has a CU to itself (17.7
+  // us at K = 7168; with four buffers, which leave a CU no room for more than that
   // one).  Where there are more of those, two buffers: 2 tiles of 64 take 28 us, 3
-  // 40, 4 51, 9 115, 14 178, one of 128 42 (2 69 to 82, 3 110, 4 147), one of 256 126 to 131.
-  // So 384 x 7168 x 7168 takes tiles of 64 (40 us, not 42), 512 x 7168 x 7168 of 128
-  // (42, not 51), 1280 x 7168 x 7168 of 128 (109, not 115), 1536 x 7168 x 7168 of 128
-  // (111, not 127), 2048 x 7168 x 7168 of 256 (131, not 147).
-  auto each = [&](int B) { return (double)((mx_tile_grid(t.M, N, B).total + cus - 1) / cus); };
+  // 40, 4 51, 9 115, 14 178, one of 128 42 (2 69 to 82, 3 110, 4 147), one of 256
+  // 126 to 131.  So 384 x 7168 x 7168 takes tiles of 64 (40 us, not 42), 512 x 7168 x
+  // 7168 of 128 (42, not 51), 1280 x 7168 x 7168 of 128 (109, not 115), 1536 x 7168 x
+  // 7168 of 128 (111, not 127), 2048 x 7168 x 7168 of 256 (131, not 147).
+  auto each = [&](int side) { return (double)((mx_tile_grid(t.M, N, side).total + cus - 1) / cus); };
   const double n64 = each(64), n128 = each(128), n256 = each(256);
   const double c64 = n64 <= 1 ? 1.0 : 0.15 + 0.7 * n64, c128 = n128 <= 1 ? 2.4 : 0.3 + 2.0 * n128, c256 = 7.0 * n256;
-  if (nb % 16 == 0 && c256 < c128 && c256 < c64) return launch_square<256, 4, 2, 1, 2>(t, out_bf16, s);
-  if (c128 < c64) return launch_square<128, 4, 1, 1, 2>(t, out_bf16, s);
-  if (n64 <= 1) return launch_square<64, 2, 1, 2, 4>(t, out_bf16, s);
-  return launch_square<64, 2, 1, 2, 2>(t, out_bf16, s);
+  if (nb % 16 == 0 && c256 < c128 && c256 < c64) return launch_tiles<256, 256, 4, 2, 1, 2>(t, out_bf16, s);
+  if (c128 < c64) return launch_tiles<128, 128, 4, 1, 1, 2>(t, out_bf16, s);
+  if (n64 <= 1) return launch_tiles<64, 64, 2, 1, 2, 4>(t, out_bf16, s);
+  return launch_tiles<64, 64, 2, 1, 2, 2>(t, out_bf16, s);
 }
 
 }  // namespace k3moe

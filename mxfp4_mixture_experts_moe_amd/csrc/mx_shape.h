@@ -36,10 +36,11 @@ struct MxTileGrid {
   int64_t total;
   unsigned x, y;
 };
-constexpr MxTileGrid mx_tile_grid(int m, int n, int side) {
-  const int64_t total = (int64_t)mx_groups(m, side) * mx_groups(n, side);
+constexpr MxTileGrid mx_tile_grid(int m, int n, int rows, int columns) {
+  const int64_t total = (int64_t)mx_groups(m, rows) * mx_groups(n, columns);
   const int64_t x = total < (1 << 20) ? total : 1 << 20;
   return {total, (unsigned)x, (unsigned)((total + x - 1) / x)};
 }
+constexpr MxTileGrid mx_tile_grid(int m, int n, int side) { return mx_tile_grid(m, n, side, side); }
 
 }  // namespace k3moe

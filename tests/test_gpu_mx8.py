@@ -231,10 +231,12 @@ def test_matmul_large_tiles_exact(k3, M, N, K):
     assert torch.equal(k3.mxfp8_matmul(ac, as_, wp, ws).double(), ref)
 
 
-@pytest.mark.parametrize("M,N,K", [(150, 3000, 2080), (130, 3500, 2048), (1000, 2000, 544), (1000, 2000, 512), (640, 1600, 2560), (1900, 2040, 1536), (1920, 2048, 1056),
-                                   (1920, 2048, 3584), (1037, 7000, 1024), (2048, 7168, 512), (2047, 7100, 1536), (500, 800, 32)])
+@pytest.mark.parametrize("M,N,K", [(64, 7200, 2048), (31, 9000, 1504), (97, 3000, 2560), (17, 20001, 1056), (32, 16448, 3584),
+                                   (150, 4200, 2080), (130, 3500, 2048), (150, 7000, 2080), (160, 6400, 2048), (1000, 2000, 544),
+                                   (1000, 2000, 512), (640, 1600, 2560), (1900, 2040, 1536), (1920, 2048, 1056), (1920, 2048, 3584),
+                                   (1037, 7000, 1024), (2048, 7168, 512), (2047, 7100, 1536), (500, 800, 32)])
 def test_matmul_tile_sides_exact(k3, M, N, K):
-    """One and several tiles of 64 and of 128 a CU and one of 256, whole and ragged, of whole and ragged groups of scales."""
+    """One and several tiles of 32 x 64, of 64 and of 128 a CU and one of 256, whole and ragged, of whole and ragged groups of scales."""
     g = np.random.default_rng([3, M, N, K])
     ac, as_, wp, ws = [to_dev_u8(t) for p in (rows8(g, M, K, 6, 8, 126, 127), weights4(g, N, K, 126, 127)) for t in p]
     ref = k3.mxfp8_unpack(ac, as_).double() @ k3.mxfp4_unpack(wp, ws).double().t()
