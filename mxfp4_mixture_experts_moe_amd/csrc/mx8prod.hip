@@ -290,9 +290,9 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
 //
 // Bound, where tiles fill the CUs, by the matrix instructions and the register
 // work of the split beside them: 4096 x 7168 x 7168 260 us, 1.62 PFLOP/s (3.2 of
-// products of 8 bits, each going in twice).  Where they do not, by what a CU gets
-// from its L2, 18 to 20 bytes a clock: 128 x 7168 x 7168 17.7 us, a quarter of the
-// matrix rate.
+// products of 8 bits, each going in twice).  Where they do not, half of a stage is
+// matrix instructions and the rest the way of its 16 or 24 KB into LDS, the barrier
+// and the reads behind it: 128 x 7168 x 7168 16.0 us.
 //   kStaged (K a multiple of 512): scales, 16 bytes (four steps) of every row, go
 //     through LDS, too, one load per wave and four steps;
 //   else each lane loads the four scale bytes of its rows for every step, which
@@ -371,7 +371,8 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
     woff[j] = (uint32_t)min(r, nrows - 1) * wrowb + 16 * place_w(lane % 4, r);
   }
   // (steps past K are outside the buffers: zeros that cost no traffic)
-  auto issue = [&](int stage, uint32_t* buf) {
+  auto issue = [&](int stage, uint32_t* buf, auto fromc, auto toc) {  // the loads from .. to - 1 of a wave's
+    constexpr int from = decltype(fromc)::value, to = decltype(toc)::value;
     const int step = stage * kSplit + ks;
     const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc((void*)(t.a + m0 * arowb), 0, step < nsteps ? (int)(mrows * arowb) : 0, 0x00020000);
     const __amdgpu_buffer_rsrc_t rw =
@@ -381,11 +382,13 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
     const int sa = __builtin_amdgcn_readfirstlane(128 * step), sw = __builtin_amdgcn_readfirstlane(64 * step);
 #pragma unroll
     for (int j = 0; j < kLoadsA; ++j) {
+      if (j < from || j >= to) continue;
       const uint32_t vo = aoff[j];  // (an array element passed straight makes the host pass drop the kernel's launch stub)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, da + 256 * j, 16, vo, sa, 0, 0);
     }
 #pragma unroll
     for (int j = 0; j < kLoadsW; ++j) {
+      if (kLoadsA + j < from || kLoadsA + j >= to) continue;
       const uint32_t vo = woff[j];
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, dw + 256 * j, 16, vo, sw, 0, 0);
     }
@@ -513,11 +516,12 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   using C1 = std::integral_constant<int, 1>;
 
   // Order of a half step: the reads, which the compiler would move to where their
-  // data are used, then the matrix instructions with the register work between
-  // them (two first, while the reads are on their way). 128 x 7168 x 7168 takes
-  // 0.9 us less with it than without, of 19.4, 2048 x 7168 x 7168 in tiles of 128 146
-  // us and not 149; tiles of 256 have no registers for it (spills, 149 instead of 130).
-  auto ordered = [&](auto&& reads, auto&& work) {
+  // data are used, then the matrix instructions with the register work, and the
+  // loads of a later stage, between them (two first, while the reads are on their
+  // way). 128 x 7168 x 7168 took 19.4 us without any order, 18.5 with it; 2048 x 7168
+  // x 7168 in tiles of 128 149 and 146; tiles of 256 have no registers for it (spills,
+  // 149 instead of 130).
+  auto ordered = [&](auto loads, auto&& reads, auto&& work) {
     reads();
     if constexpr (BM < 256) {
       __builtin_amdgcn_sched_barrier(0);
@@ -526,8 +530,14 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
       __builtin_amdgcn_sched_group_barrier(0x8, 2, 0);
 #pragma unroll
       for (int i = 0; i < kGaps; ++i) {
+        if (decltype(loads)::value) __builtin_amdgcn_sched_group_barrier(0x10, (decltype(loads)::value + kGaps - 1) / kGaps, 0);
         __builtin_amdgcn_sched_group_barrier(0x2, (42 * kTm + kGaps - 1) / kGaps, 0);
         __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+      }
+      // (split before the branch that may follow, not behind it)
+      if constexpr (kStaged) {
+#pragma unroll
+        for (int i = 0; i < kTm; ++i) asm volatile("" : "+v"(fa[i].hi), "+v"(fa[i].lo));
       }
       __builtin_amdgcn_sched_barrier(0);
     } else {
@@ -535,37 +545,55 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
     }
   };
 
-  // One stage, of which the first half step's operands are in registers: `cur` its
-  // buffer, `next` that of the next stage.  Between the halves the loads in flight
-  // are those of kRing - 1 stages (and up to two sets of scales); the oldest has to
-  // have landed, and with it, or before it, the scales that it needs.
-  auto stage = [&](auto uc, int q, uint32_t* cur, uint32_t* next) {
+  // One stage, of which the first half step's operands are in registers: `prev`,
+  // `cur`, `next` the buffers of the stage before, its own and the next stage's.
+  // Between the halves the loads in flight are those of kRing - 1 stages (and up to
+  // two sets of scales); the oldest has to have landed, and with it, or before it,
+  // the scales that it needs.
+  // Into a buffer that is free goes the stage kRing further.  With four buffers its
+  // loads are spread over this half step and the first of the next stage: the waves
+  // would wait for each other's, all at once behind the barrier (128 x 7168 x 7168
+  // 17.7 us, spread 16.0).  With two, they have to go out at once, and other
+  // workgroups fill the CU meanwhile (1003 x 4000 x 4128 40 us, spread 48).
+  using L0 = std::integral_constant<int, 0>;
+  using LA = std::integral_constant<int, kLoads>;
+  constexpr bool kSpread = kRing > 2;
+  using LH = std::integral_constant<int, (kSpread ? kLoads / 2 : kLoads)>;  // those of a stage's second half
+  using LR = std::integral_constant<int, kLoads - LH::value>;               // and of the first half of the next
+  auto stage = [&](auto uc, int q, uint32_t* prev, uint32_t* cur, uint32_t* next) {
     constexpr int u = decltype(uc)::value;  // q modulo 4 where groups have two stages, 8 where they have four
     constexpr bool kLast = u % kGroup == kGroup - 1;  // of its group
     uint32_t* const sn = (u + 1) / kGroup % 2 ? lsc1 : lsc0;  // the next stage's scales
     Raw n;
-    ordered([&] { read(cur, C1{}, n); }, [&] { multiply(C0{}); split(n, C1{}, q); });
+    ordered(LR{}, [&] { read(cur, C1{}, n); }, [&] { multiply(C0{}); split(n, C1{}, q); issue(q - 1 + kRing, prev, LH{}, LA{}); });
     wait_vm<(kRing - 2) * kLoads>();
     ring_barrier();
     read_scales(q + 1, sn);
     asm volatile("" ::: "memory");
     if constexpr (kStaged && kLast) issue_scales((q + 1) / kGroup + 1, sn == lsc0 ? lsc1 : lsc0);
     asm volatile("" ::: "memory");
-    issue(q + kRing, cur);
-    asm volatile("" ::: "memory");  // the loads go out before the reads below
-    ordered([&] { read(next, C0{}, n); }, [&] { multiply(C1{}); split(n, C0{}, q + 1); });
+    if constexpr (kSpread) {
+      ordered(LH{}, [&] { read(next, C0{}, n); }, [&] { multiply(C1{}); split(n, C0{}, q + 1); issue(q + kRing, cur, L0{}, LH{}); });
+    } else {
+      issue(q + kRing, cur, L0{}, LA{});
+      asm volatile("" ::: "memory");  // the loads go out before the reads below
+      ordered(L0{}, [&] { read(next, C0{}, n); }, [&] { multiply(C1{}); split(n, C0{}, q + 1); });
+    }
     take_scales(q + 1);
   };
   {
     Raw n;
     if constexpr (kStaged) issue_scales(0, lsc0);
     asm volatile("" ::: "memory");
-    issue(0, l0);
+    issue(0, l0, L0{}, LA{});
     if constexpr (kStaged) issue_scales(1, lsc1);
-    issue(1, l1);
-    if constexpr (kRing > 2) issue(2, l2);
-    if constexpr (kRing > 3) issue(3, l3);
-    wait_vm<(kRing - 1) * kLoads>();
+    if constexpr (kRing == 2) issue(1, l1, L0{}, LH{});
+    if constexpr (kRing > 2) {
+      issue(1, l1, L0{}, LA{});
+      issue(2, l2, L0{}, LA{});
+      issue(3, l3, L0{}, LH{});
+    }
+    wait_vm<(kRing - 2) * kLoads + LH::value>();
     ring_barrier();
     read_scales(0, lsc0);
     take_scales(0);
@@ -575,13 +603,13 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   // (kStaged: whole groups; no branch around a load, so that their number in flight is known everywhere)
   auto four = [&](auto uc, int q) {  // stages q .. q + 3, false: that was all
     constexpr int u = decltype(uc)::value;
-    stage(std::integral_constant<int, u>{}, q, l0, l1);
+    stage(std::integral_constant<int, u>{}, q, kRing > 2 ? l3 : l1, l0, l1);
     if (!kStaged && q + 1 == nstages) return false;
-    stage(std::integral_constant<int, u + 1>{}, q + 1, l1, kRing > 2 ? l2 : l0);
+    stage(std::integral_constant<int, u + 1>{}, q + 1, l0, l1, kRing > 2 ? l2 : l0);
     if ((!kStaged || kGroup == 2) && q + 2 == nstages) return false;
-    stage(std::integral_constant<int, u + 2>{}, q + 2, kRing > 2 ? l2 : l0, kRing > 2 ? l3 : l1);
+    stage(std::integral_constant<int, u + 2>{}, q + 2, l1, kRing > 2 ? l2 : l0, kRing > 2 ? l3 : l1);
     if (!kStaged && q + 3 == nstages) return false;
-    stage(std::integral_constant<int, u + 3>{}, q + 3, kRing > 2 ? l3 : l1, l0);
+    stage(std::integral_constant<int, u + 3>{}, q + 3, kRing > 2 ? l2 : l0, kRing > 2 ? l3 : l1, l0);
     return q + 4 < nstages;
   };
   if constexpr (kStaged && kGroup == 4) {
@@ -716,25 +744,24 @@ hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t
   if (M <= kFewRows && fit_all >= 1) return launch_few(f, fit_all, false, out_bf16, s);
   if (K > 512 && fit >= 4 && (M + fit - 1) / fit * wgs <= 2 * cus) return launch_few(f, fit, true, out_bf16, s);
   const TileArgs t{a, as, w, ws, (int)M, N, nb, out};
-  // Tiles of 32 x 64 where there are no more of them than CUs (what a CU gets from
-  // the L2 bounds such a product: 16 KB a stage, not the 24 of 64 x 64; 32 x 7168 x
-  // 3584 8.7 us, not 11.1, 64 x 7168 x 3584 8.8, not 10.7), and for up to 32 rows
-  // (with two buffers, as there are several on a CU: 32 x 33792 x 7168 32 us, 39 in
-  // tiles of 64).
+  // Tiles of 32 x 64 where there are no more of them than CUs (a stage brings a CU 16
+  // KB, not the 24 of 64 x 64; 32 x 7168 x 3584 8.0 us, not 10.5, 64 x 7168 x 3584
+  // 8.1, not 9.4), and for up to 32 rows (with two buffers, as there are several on
+  // a CU: 32 x 33792 x 7168 30 to 34 us, 39 in tiles of 64).
   const int64_t narrow = mx_tile_grid(t.M, N, 32, 64).total;
   if (narrow <= cus) return launch_tiles<32, 64, 1, 2, 2, 4>(t, out_bf16, s);
   if (M <= 32) return launch_tiles<32, 64, 1, 2, 2, 2>(t, out_bf16, s);
   // Else the tile side whose workgroups take the least time together, n of them on
-  // the CU with the most, in units of one 64 x 64 tile that has a CU to itself (17.7
-  // us at K = 7168; with four buffers, which leave a CU no room for more than that
-  // one).  Where there are more of those, two buffers: 2 tiles of 64 take 28 us, 3
-  // 40, 4 51, 9 115, 14 178, one of 128 42 (2 69 to 82, 3 110, 4 147), one of 256
-  // 126 to 131.  So 384 x 7168 x 7168 takes tiles of 64 (40 us, not 42), 512 x 7168 x
-  // 7168 of 128 (42, not 51), 1280 x 7168 x 7168 of 128 (109, not 115), 1536 x 7168 x
-  // 7168 of 128 (111, not 127), 2048 x 7168 x 7168 of 256 (131, not 147).
+  // the CU with the most, in units of 17.7 us at K = 7168.  One tile of 64 with a CU
+  // to itself takes 16 us (with four buffers, which leave no room for another);
+  // where there are more of those, two buffers: 2 take 27 us, 3 39, 4 50, 9 115, 14
+  // 178; one of 128 41 (2 69 to 82, 3 109, 4 147), one of 256 126 to 131.  So 384 x
+  // 7168 x 7168 takes tiles of 64 (39 us, not 42), 512 x 7168 x 7168 of 128 (41, not
+  // 51), 1280 x 7168 x 7168 of 128 (107, not 115), 1536 x 7168 x 7168 of 128 (109, not
+  // 127), 2048 x 7168 x 7168 of 256 (130, not 147).
   auto each = [&](int side) { return (double)((mx_tile_grid(t.M, N, side).total + cus - 1) / cus); };
   const double n64 = each(64), n128 = each(128), n256 = each(256);
-  const double c64 = n64 <= 1 ? 1.0 : 0.15 + 0.7 * n64, c128 = n128 <= 1 ? 2.4 : 0.3 + 2.0 * n128, c256 = 7.0 * n256;
+  const double c64 = n64 <= 1 ? 0.9 : 0.15 + 0.7 * n64, c128 = n128 <= 1 ? 2.4 : 0.3 + 2.0 * n128, c256 = 7.0 * n256;
   if (nb % 16 == 0 && c256 < c128 && c256 < c64) return launch_tiles<256, 256, 4, 2, 1, 2>(t, out_bf16, s);
   if (c128 < c64) return launch_tiles<128, 128, 4, 1, 1, 2>(t, out_bf16, s);
   if (n64 <= 1) return launch_tiles<64, 64, 2, 1, 2, 4>(t, out_bf16, s);
