@@ -301,6 +301,7 @@ def mxfp4_dequant(blocks: torch.Tensor, out_dtype: torch.dtype = torch.float32,
 
 
 _FLOAT_CODES = {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}
+_FLOATS = tuple(_FLOAT_CODES)
 
 
 def _out_code(out_dtype: torch.dtype) -> int:
@@ -338,7 +339,7 @@ def mxfp4_quantize(x: torch.Tensor, saturate: bool = True, packed: torch.Tensor 
     layout mxfp4_repack, mxfp4_matmul and mxfp4_linear read. saturate=False
     takes the next larger scale where a block's largest element would be
     clamped."""
-    _dev(x, "x", tuple(_FLOAT_CODES))
+    _dev(x, "x", _FLOATS)
     if x.dim() < 1:
         raise ValueError("x must be [..., K]")
     K = x.shape[-1]
@@ -409,7 +410,7 @@ def mxfp4_linear(x: torch.Tensor, w_packed: torch.Tensor, w_scale: torch.Tensor,
     """Rows x [M, K] (f32, bf16 or f16), quantised as mxfp4_quantize does, times
     a microscaled weight matrix W [N, K]: out [M, N] f32 or bf16. The same bits
     as mxfp4_quantize and mxfp4_matmul in turn."""
-    _dev(x, "x", tuple(_FLOAT_CODES))
+    _dev(x, "x", _FLOATS)
     K = _mx_pair(w_packed, w_scale, "W", 2)
     if x.dim() != 2 or x.shape[1] != K:
         raise ValueError("x must be [M, K]")
@@ -453,7 +454,7 @@ def mxfp8_quantize(x: torch.Tensor, saturate: bool = True, codes: torch.Tensor |
     microscaled 8 bits: (codes u8 [..., R, K] of E4M3, scale u8 [..., R, K/32]),
     what mxfp8_matmul reads. saturate=False takes the next larger scale where a
     block's largest element would be clamped."""
-    _dev(x, "x", tuple(_FLOAT_CODES))
+    _dev(x, "x", _FLOATS)
     if x.dim() < 1:
         raise ValueError("x must be [..., K]")
     K = x.shape[-1]
@@ -461,7 +462,7 @@ def mxfp8_quantize(x: torch.Tensor, saturate: bool = True, codes: torch.Tensor |
         raise ValueError("K must be a multiple of 32")
     given = codes is not None or scale is not None
     if codes is None:
-        codes = x.new_empty(x.shape, dtype=torch.uint8)
+        codes = torch.empty_like(x, dtype=torch.uint8)
     if scale is None:
         scale = x.new_empty((*x.shape[:-1], K // 32), dtype=torch.uint8)
     if given:
@@ -505,35 +506,38 @@ def mxfp8_rms_norm(x: torch.Tensor, gamma: torch.Tensor | None = None, residual:
     without a residual, unless a buffer for it is given; it may be `residual` or
     `x` itself, which is then updated), y the normed rows in x's type (None unless
     `normed` or a buffer is given)."""
-    _dev(x, "x", tuple(_FLOAT_CODES))
+    _dev(x, "x", _FLOATS)
     if x.dim() < 1:
         raise ValueError("x must be [..., K]")
     K = x.shape[-1]
     if K % 32:
         raise ValueError("K must be a multiple of 32")
+    shape, dtype = x.shape, x.dtype
     for name, t in (("residual", residual), ("total", total), ("y", y)):
         if t is not None:
-            _dev(t, name, x.dtype)
-            if t.shape != x.shape:
+            _dev(t, name, dtype)
+            if t.shape != shape:
                 raise ValueError(f"{name} must have x's shape")
     if gamma is not None:
-        _dev(gamma, "gamma", tuple(_FLOAT_CODES))
+        _dev(gamma, "gamma", _FLOATS)
         if gamma.shape != (K,):
             raise ValueError("gamma must be [K]")
+    _same_device(x, residual=residual, gamma=gamma, total=total, y=y)
     if total is None and residual is not None:
         total = torch.empty_like(x)
     if y is None and normed:
         y = torch.empty_like(x)
     given = codes is not None or scale is not None
     if codes is None:
-        codes = x.new_empty(x.shape, dtype=torch.uint8)
+        codes = torch.empty_like(x, dtype=torch.uint8)
     if scale is None:
-        scale = x.new_empty((*x.shape[:-1], K // 32), dtype=torch.uint8)
-    if given and (_mx8_pair(codes, scale, "output") != K or codes.shape != x.shape):
-        raise ValueError("codes must have x's shape")
-    _same_device(x, residual=residual, gamma=gamma, total=total, y=y, codes=codes)
+        scale = x.new_empty((*shape[:-1], K // 32), dtype=torch.uint8)
+    if given:
+        if _mx8_pair(codes, scale, "output") != K or codes.shape != shape:
+            raise ValueError("codes must have x's shape")
+        _same_device(x, codes=codes)
     R = x.numel() // K if K else 0
-    _launch("mxfp8_rms_norm", x.device, x.data_ptr(), _ptr(residual), _ptr(gamma), _FLOAT_CODES[x.dtype],
+    _launch("mxfp8_rms_norm", x.device, x.data_ptr(), _ptr(residual), _ptr(gamma), _FLOAT_CODES[dtype],
             DTYPE_F32 if gamma is None else _FLOAT_CODES[gamma.dtype], R, K, float(eps), int(bool(saturate)), _ptr(total),
             _ptr(y), codes.data_ptr(), scale.data_ptr())
     return codes, scale, total, y
@@ -611,7 +615,7 @@ def moe_verify_draft(logits: torch.Tensor, draft_ids: torch.Tensor | None, u_acc
     Returns (n_accepted i32 [S], tokens i32 [S, W]: the accepted proposals, the
     next token, then -1, accept_prob f32 [S, W-1]: each proposal's probability of
     being accepted)."""
-    _dev(logits, "logits", tuple(_FLOAT_CODES))
+    _dev(logits, "logits", _FLOATS)
     if logits.dim() != 3:
         raise ValueError("logits must be [S, W, V]")
     S, W, V = logits.shape
