@@ -317,6 +317,8 @@ struct FastScratch {
 template <int NPER>
 __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t, int lane, int shift, uint32_t inv_size, FastScratch& x, float* score) {
   const int lanes = 1 << shift;
+  // whether expert lane + 64 j exists (NPER, in twos, is no larger than it has to be)
+  auto real = [&](int j) -> bool { return j < NPER - 2 || lane < a.E - kWaveSize * j; };
   // (a buffer ends with the token's row: what lies past it costs no address arithmetic and reads as zeros)
   const uint32_t at = 4u * (uint32_t)lane, bytes = 4u * (uint32_t)a.E;
   const __amdgpu_buffer_rsrc_t zr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.z + t * (int64_t)a.E), 0, (int)bytes, 0x00020000);
@@ -332,7 +334,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
     for (int j = 0; j < NPER; ++j) b[j] = 0.0f;
   }
 #pragma unroll
-  for (int j = 0; j < NPER; ++j) z[j] = lane < a.E - kWaveSize * j ? z[j] : -INFINITY;
+  for (int j = 0; j < NPER; ++j) z[j] = real(j) ? z[j] : -INFINITY;
 
   // fp32 scores s, of experts past E -inf, and what groups add up (gs).  u = 2^-24:
   //   sigmoid: off by at most 2^-21 (1 + |s|) (route_device.h).
@@ -374,7 +376,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
   if (a.keep < a.groups) {
 #pragma unroll
     for (int j = 0; j < NPER; ++j)
-      if (lane < a.E - kWaveSize * j) score[lane + kWaveSize * j] = s[j];
+      if (real(j)) score[lane + kWaveSize * j] = s[j];
     wave_fence();
     const int g = lane / lanes, sub = lane & (lanes - 1);
     float b1 = -INFINITY, b2 = -INFINITY;
@@ -461,7 +463,7 @@ __device__ __forceinline__ bool route_token_fast(const GroupsArgs& a, int64_t t,
   const uint32_t place = __umul24((uint32_t)lane, inv_size);
   auto in_kept = [&](int j) -> bool {
     const uint32_t g = (place + (uint32_t)(kWaveSize * j) * inv_size) >> 20;
-    return ((lane < a.E - kWaveSize * j) & (int)(groups >> (g & 63u))) != 0;
+    return ((int)real(j) & (int)(groups >> (g & 63u))) != 0;
   };
 
   // Candidates: s[j] >= theta.
