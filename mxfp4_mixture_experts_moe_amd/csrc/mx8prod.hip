@@ -289,7 +289,7 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
 // and the next stage, whose loads the wave has waited for, is there.
 //
 // Bound, where tiles fill the CUs, by the matrix instructions and the register
-// work of the split beside them: 4096 x 7168 x 7168 260 us, 1.62 PFLOP/s (3.2 of
+// work of the split beside them: 4096 x 7168 x 7168 239 us, 1.76 PFLOP/s (3.5 of
 // products of 8 bits, each going in twice).  Where they do not, half of a stage is
 // matrix instructions and the rest the way of its 16 or 24 KB into LDS, the barrier
 // and the reads behind it: 128 x 7168 x 7168 16.0 us.
@@ -318,9 +318,10 @@ template <int BM, int BN, int kWm, int kWn, int kSplit, int kRing, bool kStaged,
 __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileArgs t) {
   constexpr int kSet = kWm * kWn, kWaves = kSet * kSplit;
   constexpr int kTm = BM / (32 * kWm), kTn = BN / (32 * kWn);  // 32-row operand tiles per wave
-  constexpr int kADw = BM * 32, kStepDw = kADw + BN * 16;  // dwords of a step's rows of A; and of W behind them
+  constexpr int kBN = (BN + 16 * kSet - 1) / (16 * kSet) * (16 * kSet);  // rows of W in LDS: as many for every wave
+  constexpr int kADw = BM * 32, kStepDw = kADw + kBN * 16;  // dwords of a step's rows of A; and of W behind them
   constexpr int kStageDw = kSplit * kStepDw;
-  constexpr int kLoadsA = kSplit * BM / (8 * kWaves), kLoadsW = kSplit * BN / (16 * kWaves), kLoads = kLoadsA + kLoadsW;  // 1 KB each, per wave and stage
+  constexpr int kLoadsA = kSplit * BM / (8 * kWaves), kLoadsW = kSplit * kBN / (16 * kWaves), kLoads = kLoadsA + kLoadsW;  // 1 KB each, per wave and stage
   constexpr int kGroup = 4 / kSplit;  // stages that a load of scales lasts
   static_assert((kRing == 2 || kRing == 4) && kSplit <= 2 && kGroup >= kRing - 2, "scales land with the stage that they are for");
   // one array per buffer, so that the compiler sees that a read of one buffer
@@ -358,7 +359,7 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   auto place_a = [](int c, int r) { return c ^ ((r >> 1) & 7); };
   auto place_w = [](int c, int r) { return c ^ ((r >> 2) & 3); };
   // loads: wave w fills the (w % kSet)-th part of the rows of step w / kSet of a stage
-  const int arow0 = wave % kSet * (BM / kSet), wrow0 = wave % kSet * (BN / kSet);
+  const int arow0 = wave % kSet * (BM / kSet), wrow0 = wave % kSet * (kBN / kSet);
   uint32_t aoff[kLoadsA], woff[kLoadsW];
 #pragma unroll
   for (int j = 0; j < kLoadsA; ++j) {
@@ -368,7 +369,7 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
 #pragma unroll
   for (int j = 0; j < kLoadsW; ++j) {
     const int r = wrow0 + 16 * j + lane / 4;
-    woff[j] = (uint32_t)min(r, nrows - 1) * wrowb + 16 * place_w(lane % 4, r);
+    woff[j] = r < BN ? (uint32_t)min(r, nrows - 1) * wrowb + 16 * place_w(lane % 4, r) : 0x80000000u;  // (outside)
   }
   // (steps past K are outside the buffers: zeros that cost no traffic)
   auto issue = [&](int stage, uint32_t* buf, auto fromc, auto toc) {  // the loads from .. to - 1 of a wave's
@@ -395,7 +396,7 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   };
 
   // Scales.  kStaged: 16 bytes (four steps) of each of the tile's rows through LDS
-  constexpr int kScaleA = (BM + 63) / 64, kScaleLoads = kScaleA + BN / 64;  // of 64 rows; one per wave (some twice where there are more waves)
+  constexpr int kScaleA = (BM + 63) / 64, kScaleLoads = kScaleA + (BN + 63) / 64;  // of 64 rows; one per wave (some twice where there are more waves)
   static_assert(kScaleLoads <= kWaves, "every wave does one load of scales");
   __shared__ __attribute__((aligned(256))) uint32_t lsc0[kStaged ? kScaleLoads * 256 : 1], lsc1[kStaged ? kScaleLoads * 256 : 1];  // (of even groups, of odd ones)
   const int sload = wave % kScaleLoads;
@@ -519,11 +520,11 @@ __global__ __launch_bounds__(kWm * kWn * kSplit * 64) void mx8_tile_kernel(TileA
   // data are used, then the matrix instructions with the register work, and the
   // loads of a later stage, between them (two first, while the reads are on their
   // way). 128 x 7168 x 7168 took 19.4 us without any order, 18.5 with it; 2048 x 7168
-  // x 7168 in tiles of 128 149 and 146; tiles of 256 have no registers for it (spills,
-  // 149 instead of 130).
+  // x 7168 in tiles of 128 149 and 146; waves of more than 192 columns have no
+  // registers for it (spills).
   auto ordered = [&](auto loads, auto&& reads, auto&& work) {
     reads();
-    if constexpr (BM < 256) {
+    if constexpr (kTm == 1 && kTn < 7) {
       __builtin_amdgcn_sched_barrier(0);
       work();
       constexpr int kMfma = 2 * kTm * kTn, kGaps = kMfma > 2 ? kMfma - 2 : 1;
@@ -684,7 +685,7 @@ hipError_t launch_tiles(const TileArgs& t, bool bf16, hipStream_t s) {
   const bool staged = t.nb % 16 == 0;
   if (staged && bf16) go(std::true_type{}, std::true_type{});
   else if (staged) go(std::true_type{}, std::false_type{});
-  else if constexpr (BM < 256) {  // (the registers of the largest do not hold the scales of ragged rows, too)
+  else if constexpr (BN <= 192) {  // (the registers of the largest do not hold the scales of ragged rows, too)
     if (bf16) go(std::false_type{}, std::true_type{});
     else go(std::false_type{}, std::false_type{});
   }
@@ -751,18 +752,25 @@ hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t
   const int64_t narrow = mx_tile_grid(t.M, N, 32, 64).total;
   if (narrow <= cus) return launch_tiles<32, 64, 1, 2, 2, 4>(t, out_bf16, s);
   if (M <= 32) return launch_tiles<32, 64, 1, 2, 2, 2>(t, out_bf16, s);
-  // Else the tile side whose workgroups take the least time together, n of them on
-  // the CU with the most, in units of 17.7 us at K = 7168.  One tile of 64 with a CU
-  // to itself takes 16 us (with four buffers, which leave no room for another);
-  // where there are more of those, two buffers: 2 take 27 us, 3 39, 4 50, 9 115, 14
-  // 178; one of 128 41 (2 69 to 82, 3 109, 4 147), one of 256 126 to 131.  So 384 x
-  // 7168 x 7168 takes tiles of 64 (39 us, not 42), 512 x 7168 x 7168 of 128 (41, not
-  // 51), 1280 x 7168 x 7168 of 128 (107, not 115), 1536 x 7168 x 7168 of 128 (109, not
-  // 127), 2048 x 7168 x 7168 of 256 (130, not 147).
-  auto each = [&](int side) { return (double)((mx_tile_grid(t.M, N, side).total + cus - 1) / cus); };
-  const double n64 = each(64), n128 = each(128), n256 = each(256);
-  const double c64 = n64 <= 1 ? 0.9 : 0.15 + 0.7 * n64, c128 = n128 <= 1 ? 2.4 : 0.3 + 2.0 * n128, c256 = 7.0 * n256;
-  if (nb % 16 == 0 && c256 < c128 && c256 < c64) return launch_tiles<256, 256, 4, 2, 1, 2>(t, out_bf16, s);
+  // Else the tile whose workgroups take the least time together, n of them on the CU
+  // with the most, in units of 17.7 us at K = 7168.  One tile of 64 with a CU to
+  // itself takes 16 us (with four buffers, which leave no room for another); where
+  // there are more of those, two buffers: 2 take 27 us, 3 39, 4 50, 9 115, 14 178;
+  // one of 128 41 (2 69 to 82, 3 108, 4 141, 7 264).  One of 256 rows, one to a CU:
+  // 97 to 101 us with 192 columns, 107 to 120 with 224, 120 to 134 with 256 (more
+  // where all CUs have one), so that 7168 columns are 28, 32 or 38 tiles and the
+  // last round is full or not: 1536 x 7168 x 7168 101 us by 192 (128: 108, 224: 109),
+  // 4096 x 7168 x 7168 239 by 224 (256: 251, 128: 264), 4096 x 4096 x 7168 134 by 256
+  // (128: 152, 192: 194).  384 x 7168 x 7168 takes tiles of 64 (39 us, not 42), 512 x
+  // 7168 x 7168 of 128 (41, not 51).
+  auto each = [&](int rows, int columns) { return (double)((mx_tile_grid(t.M, N, rows, columns).total + cus - 1) / cus); };
+  const double n64 = each(64, 64), n128 = each(128, 128);
+  const double c64 = n64 <= 1 ? 0.9 : 0.15 + 0.7 * n64, c128 = n128 <= 1 ? 2.3 : 0.2 + 2.05 * n128;
+  const double c192 = 5.65 * each(256, 192), c224 = 6.7 * each(256, 224), c256 = 7.2 * each(256, 256);
+  const double small = c64 < c128 ? c64 : c128;
+  if (nb % 16 == 0 && c224 < small && c224 <= c192 && c224 <= c256) return launch_tiles<256, 224, 8, 1, 1, 2>(t, out_bf16, s);
+  if (nb % 16 == 0 && c256 < small && c256 <= c192) return launch_tiles<256, 256, 8, 1, 1, 2>(t, out_bf16, s);
+  if (c192 < small) return launch_tiles<256, 192, 8, 1, 1, 2>(t, out_bf16, s);
   if (c128 < c64) return launch_tiles<128, 128, 4, 1, 1, 2>(t, out_bf16, s);
   if (n64 <= 1) return launch_tiles<64, 64, 2, 1, 2, 4>(t, out_bf16, s);
   return launch_tiles<64, 64, 2, 1, 2, 2>(t, out_bf16, s);

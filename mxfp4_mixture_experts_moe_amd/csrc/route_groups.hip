@@ -20,8 +20,8 @@
 // scores themselves have become -inf by then), and top_of() takes the best, of
 // groups as of experts.
 //
-// 16384 tokens of 896 take 39 us, bound by the vector instructions (the logits
-// are 59 MB, 12 us at 5.1 TB/s); 8 tokens 7.2 us, one wave's way through them.  A
+// 16384 tokens of 896 take 38 us, bound by the vector instructions (the logits
+// are 59 MB, 12 us at 5.1 TB/s); 8 tokens 6.8 us, one wave's way through them.  A
 // wave a token without a loop, 120 -> 78 us (the loop's spilled scalars); groups
 // too near for fp32 settled by two experts' fp64 scores instead of the plain way,
 // 78 -> 45; as many logits a lane as there are instead of 4, 8 or 16, 45 -> 39.

@@ -234,7 +234,9 @@ def test_matmul_large_tiles_exact(k3, M, N, K):
 @pytest.mark.parametrize("M,N,K", [(64, 7200, 2048), (31, 9000, 1504), (97, 3000, 2560), (17, 20001, 1056), (32, 16448, 3584),
                                    (150, 4200, 2080), (130, 3500, 2048), (150, 7000, 2080), (160, 6400, 2048), (1000, 2000, 544),
                                    (1000, 2000, 512), (640, 1600, 2560), (1900, 2040, 1536), (1920, 2048, 1056), (1920, 2048, 3584),
-                                   (1037, 7000, 1024), (2048, 7168, 512), (2047, 7100, 1536), (500, 800, 32)])
+                                   (1037, 7000, 1024), (2048, 7168, 512), (2047, 7100, 1536), (500, 800, 32),
+                                   (1530, 7160, 1024), (1900, 6100, 1056), (2300, 4800, 2080), (3900, 4090, 1024), (4096, 3584, 512),
+                                   (1000, 10000, 1536)])
 def test_matmul_tile_sides_exact(k3, M, N, K):
     """One and several tiles of 32 x 64, of 64 and of 128 a CU and one of 256, whole and ragged, of whole and ragged groups of scales."""
     g = np.random.default_rng([3, M, N, K])
