@@ -609,8 +609,11 @@ hipError_t launch_verify_draft(const VerifyDraftCall& c, hipStream_t s) {
   a.tokens = c.tokens;
   a.accept_prob = c.accept_prob;
   // Chunks of a workgroup of the second launch: each takes the proposals' test
-  // first, so four where that still leaves a workgroup for every CU.
-  const int per = !c.q ? 0 : c.S * ((l.chunks + 3) / 4) >= device_cu_count() ? 4 : 1;
+  // first, so two where that leaves more workgroups than CUs, four where it leaves
+  // four for each (by one, two, four, us: 13 x 5 x 32003 16, 17, 20; 32 x 8 x 163840
+  // 63, 58, 58; 128 x 4 x 163840 140, 127, 119).
+  const int64_t cus = device_cu_count();
+  const int per = !c.q ? 0 : c.S * ((l.chunks + 3) / 4) >= 4 * cus ? 4 : c.S * ((l.chunks + 1) / 2) > cus ? 2 : 1;
   const unsigned wgs = (unsigned)(c.S * (per ? (l.chunks + per - 1) / per : 1));
   const unsigned rows = 1 + (wgs >> 22);  // (a grid dimension has fewer than 2^32 threads)
   const dim3 g1((unsigned)(c.S * c.W * l.chunks)), g2((wgs + rows - 1) / rows, rows);
@@ -621,6 +624,7 @@ hipError_t launch_verify_draft(const VerifyDraftCall& c, hipStream_t s) {
     if (e != hipSuccess) return e;
     if (per == 0) hipLaunchKernelGGL((choose_kernel<kType, 0>), g2, dim3(kChooseThreads), 0, s, a);
     else if (per == 1) hipLaunchKernelGGL((choose_kernel<kType, 1>), g2, dim3(kChooseThreads), 0, s, a);
+    else if (per == 2) hipLaunchKernelGGL((choose_kernel<kType, 2>), g2, dim3(kChooseThreads), 0, s, a);
     else hipLaunchKernelGGL((choose_kernel<kType, 4>), g2, dim3(kChooseThreads), 0, s, a);
     return hipGetLastError();
   };

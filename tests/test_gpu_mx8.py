@@ -286,6 +286,18 @@ def test_matmul_nan_stays_in_its_row_and_column(k3, M):
     assert torch.equal(torch.isnan(out), nan)
 
 
+@pytest.mark.parametrize("M,N,K", [(9, 300, 4096), (40, 300, 1024), (60, 7000, 1024), (150, 4200, 2048), (1000, 2000, 512),
+                                   (1900, 2040, 1536), (1530, 7160, 1024), (2048, 7168, 512), (3900, 4090, 1024)])
+def test_matmul_nan_beside_whole_groups_of_scales(k3, M, N, K):
+    """A NaN code, a NaN scale of A and one of W: their rows and column, and nothing else."""
+    g = np.random.default_rng([5, M, N, K])
+    ac, as_, wp, ws = [to_dev_u8(t) for p in (rows8(g, M, K, 6, 8, 126, 127), weights4(g, N, K, 126, 127)) for t in p]
+    ref = k3.mxfp8_matmul(ac, as_, wp, ws)
+    ac[M // 2, K - 1], as_[M - 1, 0], ws[N - 2, K // 32 - 1] = 127, 255, 255
+    ref[M // 2], ref[M - 1], ref[:, N - 2] = (float("nan"),) * 3
+    assert torch.equal(torch.nan_to_num(k3.mxfp8_matmul(ac, as_, wp, ws), nan=1e30), torch.nan_to_num(ref, nan=1e30))
+
+
 def test_matmul_matches_linear_by_four_bits(k3):
     """Rows that hold E2M1 values: the 8-bit product gives what the 4-bit one gives."""
     g = np.random.default_rng(3)

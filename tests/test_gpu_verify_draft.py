@@ -59,7 +59,7 @@ def test_full_vocabulary(k3, dtype):
     assert n.max() > 0
 
 
-@pytest.mark.parametrize("S,W,V", [(2, 3, 300001), (1, 2, 1200007), (40, 2, 50000)])
+@pytest.mark.parametrize("S,W,V", [(2, 3, 300001), (1, 2, 1200007), (40, 2, 50000), (520, 2, 20500)])
 @pytest.mark.parametrize("probs", [True, False])
 def test_many_chunks(k3, S, W, V, probs):
     """More chunks than a wave has lanes, and enough of them for several to a workgroup."""
