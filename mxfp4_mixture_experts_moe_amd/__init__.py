@@ -638,11 +638,11 @@ def moe_verify_draft(logits: torch.Tensor, draft_ids: torch.Tensor | None, u_acc
         if t.get_device() != index:
             raise ValueError(f"{name}: must be on {logits.device}")
     if n_accepted is None:
-        n_accepted = logits.new_empty((S,), dtype=torch.int32)
+        n_accepted = torch.empty_like(u_sample, dtype=torch.int32)
     if tokens is None:
         tokens = logits.new_empty((S, W), dtype=torch.int32)
     if accept_prob is None:
-        accept_prob = logits.new_empty((S, W - 1), dtype=torch.float32)
+        accept_prob = logits.new_empty((S, W - 1), dtype=torch.float32) if u_accept is None else torch.empty_like(u_accept)
     if workspace is None:
         workspace = logits.new_empty(moe_verify_draft_workspace_size(S, W, V), dtype=torch.uint8)
     else:
