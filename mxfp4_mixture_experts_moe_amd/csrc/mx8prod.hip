@@ -163,6 +163,9 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
   mx_u32x4 raw[kBatch];
   uint32_t rsc[kBatch];
   int at0 = 0;  // first unit of the batch
+  // row and unit of the row to place next, and what `threads` units further adds
+  const int dm = __builtin_amdgcn_readfirstlane(threads / (2 * nb)), dr = threads - dm * 2 * nb;
+  int pm = tid / (2 * nb), pr = tid - pm * 2 * nb;
   auto fetch = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
@@ -174,12 +177,13 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
   auto stage = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int u = at0 + b * threads + tid;
-      const int m = u / (2 * nb), r = u - m * 2 * nb;
-      if (u < units) {
-        *reinterpret_cast<mx_u32x4*>(codes + m * a.arow + 16 * r) = raw[b];
-        if ((r & 1) == 0) scales[m * a.srow + (r >> 1)] = (uint8_t)rsc[b];
+      if (pm < M) {
+        *reinterpret_cast<mx_u32x4*>(codes + pm * a.arow + 16 * pr) = raw[b];
+        if ((pr & 1) == 0) scales[pm * a.srow + (pr >> 1)] = (uint8_t)rsc[b];
       }
+      pm += dm;
+      pr += dr;
+      if (pr >= 2 * nb) pr -= 2 * nb, ++pm;
     }
     at0 += kBatch * threads;
   };
