@@ -157,17 +157,22 @@ __device__ __forceinline__ float scaled_odd(double y, uint32_t e) {
 }
 
 // fp64 rounded once to a 16-bit type: by way of an fp32 number rounded to odd
-// inside fp32's normal range, and directly outside.
+// inside fp32's normal range, and directly outside.  bf16 has numbers below that
+// range, n steps of 2^-133 whose bits are n: the sum with 1.5 * 2^-81, where fp64 has
+// these steps, ends in n.  (fp32's own steps there, 2^-149, would round a first time,
+// and that onto ties.)
 template <int kType>
 __device__ __forceinline__ uint16_t round16(double d) {
   const uint32_t k = key_of(d), hi = k >> 1;
   const float plain = (float)d;
-  const bool normal = hi - 0x38100000u < 0x47F00000u - 0x38100000u;
-  const float f = normal ? __uint_as_float((hi - 0x38000000u) << 3 | (k & 1u) | sign_of(d)) : plain;
-  if constexpr (kType == K3MOE_DTYPE_BF16)
-    return __builtin_bit_cast(uint16_t, (__bf16)f);
-  else
+  const bool inside = (kType == K3MOE_DTYPE_BF16 || hi >= 0x38100000u) && hi < 0x47F00000u;
+  const float f = inside ? __uint_as_float((hi - 0x38000000u) << 3 | (k & 1u) | sign_of(d)) : plain;
+  if constexpr (kType == K3MOE_DTYPE_BF16) {
+    const uint32_t n = (uint32_t)(uint64_t)__double_as_longlong(fabs(d) + 0x1.8p-81) | sign_of(d) >> 16;
+    return hi < 0x38100000u ? (uint16_t)n : __builtin_bit_cast(uint16_t, (__bf16)f);
+  } else {
     return __builtin_bit_cast(uint16_t, (_Float16)f);
+  }
 }
 template <int kType>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
@@ -272,8 +277,11 @@ __device__ __forceinline__ void exact_unit(const NormArgs& a, const Unit<kType>&
     for (int i = 0; i < 8; ++i) {
       if constexpr (kType == K3MOE_DTYPE_F32)
         yr.q[i >> 2][i & 3] = __float_as_uint((float)y[i]);
-      else if (i % 2 == 0)
-        yr.q[0][i / 2] = (uint32_t)round16<kType>(y[i]) | (uint32_t)round16<kType>(y[i + 1]) << 16;
+      else if (i % 2 == 0) {
+        uint32_t p = (uint32_t)round16<kType>(y[i]) | (uint32_t)round16<kType>(y[i + 1]) << 16;
+        if constexpr (kType == K3MOE_DTYPE_BF16) asm volatile("" : "+v"(p));  // (a pair at a time: all eight at once spill)
+        yr.q[0][i / 2] = p;
+      }
     }
   }
   uint32_t top = 0u;
