@@ -336,9 +336,10 @@ __device__ __forceinline__ bool quick_unit(const NormArgs& a, const Unit<kType>&
       const float p = y[2 * i], q = y[2 * i + 1];
       yr.q[0][i] = pack16<kType>(p * (1.0f - kOff), q * (1.0f - kOff));
       sure &= yr.q[0][i] == pack16<kType>(p * (1.0f + kOff), q * (1.0f + kOff));
-      // a result below fp32's normal range, or lost below it
-      sure &= (__float_as_uint(p) & 0x7FFFFFFFu) >= 0x01000000u || v[2 * i] == 0.0f;
-      sure &= (__float_as_uint(q) & 0x7FFFFFFFu) >= 0x01000000u || v[2 * i + 1] == 0.0f;
+      // below 2^-106 the result, or v * rstd under a gamma of up to 2^19, may lie below fp32's
+      // normal range, where roundings are not relative any more
+      sure &= (__float_as_uint(p) & 0x7FFFFFFFu) >= (127u - 106u) << 23 || v[2 * i] == 0.0f;
+      sure &= (__float_as_uint(q) & 0x7FFFFFFFu) >= (127u - 106u) << 23 || v[2 * i + 1] == 0.0f;
     }
   }
   return sure;

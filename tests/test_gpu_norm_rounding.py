@@ -1,5 +1,5 @@
-"""The norm's y and sum are rounded once, bit for bit, also below the normal range, where fp32 on the way would round before
-the type does."""
+"""The norm's y and sum are rounded once, bit for bit, also where fp32 on the way would round before the type does: y below
+the normal range, and elements whose v / sqrt(..) is below it while gamma takes y back above."""
 
 import numpy as np
 import pytest
@@ -73,3 +73,17 @@ def test_random_below_the_normal_range(k3, dtype, K):
     gamma = torch.exp2(torch.randint(-bits - 6, 6, (K,), generator=g).float()) * n(K) * 2.0 ** (least + 4 if dtype == torch.float16 else -20)
     x = n(3, K) * (1.0 if dtype == torch.float16 else 2.0 ** (least + 20))
     check(k3, x.to(dtype), gamma, None, 1.0)
+
+
+@pytest.mark.parametrize("K", [64, 1024, 9216, 40960])
+@pytest.mark.parametrize("eps", [3.0, 3.0 * 2.0**16, 5.0 * 2.0**20])
+def test_bf16_that_gamma_takes_back_above(k3, K, eps):
+    """A 1 in every block, which keeps its scale ordinary, beside elements whose v / sqrt(..) holds only a few of fp32's bits
+    below 2^-126, times a gamma of 2^17 to 2^19."""
+    g = torch.Generator().manual_seed(K)
+    k = torch.randint(1, 128, (4, K), generator=g).float() * torch.exp2(torch.randint(0, 8, (4, K), generator=g).float())
+    x = (k * 2.0**-133).bfloat16()
+    x[:, ::32] = 1.0
+    gamma = torch.exp2(17 + 2 * torch.rand((K,), generator=g)).clamp(max=2.0**19 - 1)
+    check(k3, x, gamma, None, eps)
+    check(k3, x / 2, -gamma, x / 2, eps, saturate=False)
