@@ -745,12 +745,13 @@ hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t
   const int fit = few_rows(nb, kFewLds), fit_all = few_rows(nb, kFewLdsAll);
   const int64_t cus = device_cu_count(), wgs = (mx_groups(N, 16) + f.rw - 1) / f.rw;
   // Few rows: two workgroups a CU where all rows fit half of its LDS, else one, in
-  // chunks of what fits.  More, of K beyond a tile's first few stages: where the
+  // chunks of what fits, of a long K as mx8_few_in_chunks says.  More, of K beyond a tile's first few stages: where the
   // workgroups of every chunk are resident at once (32 x 3584 x 3584 7.9 us, in
   // tiles 11; 64 x 2048 x 2048 5.3, not 7.6; 77 x 1003 x 4128 11, not 17; 256 x 2048 x
   // 512 5.1 by either; beyond, 64 x 3584 x 3584 12.7 instead of 10.3 in tiles).
   if (M <= kFewRows && fit >= M) return launch_few(f, kFewRows, true, out_bf16, s);
-  if (M <= kFewRows && fit_all >= 1) return launch_few(f, fit_all, false, out_bf16, s);
+  if (M <= kFewRows && fit_all >= 1 && mx8_few_in_chunks(N, (M + fit_all - 1) / fit_all, nb % 16 == 0, (int)cus))
+    return launch_few(f, fit_all, false, out_bf16, s);
   if (K > 512 && fit >= 4 && (M + fit - 1) / fit * wgs <= 2 * cus) return launch_few(f, fit, true, out_bf16, s);
   const TileArgs t{a, as, w, ws, (int)M, N, nb, out};
   // Tiles of 32 x 64 where there are no more of them than CUs (a stage brings a CU 16

@@ -30,6 +30,19 @@ constexpr int mx_few_rounds(int n, int side, int wgs) {
   return (mx_groups(n, 16) + step - 1) / step;
 }
 
+// Whether the few-row kernel takes up to 16 rows of 8 bits in `chunks`, each of
+// which reads all weights, and has a CU to itself for 16 of their rows; else tiles of
+// 32 x 64 take them, in one pass.  A tile takes as long as three rounds of such
+// workgroups (four of them hold a tile's weight rows), as six where K is no multiple
+// of 512 (not `whole`).  us in chunks and in tiles: 16 x 4096 x 12288 (two chunks, 64
+// tiles) 18 and 19, 16 x 7168 x 9216 (two, 112) 23 and 15, 12 x 4096 x 33792
+// (three, 64) 51 and 56, 16 x 7168 x 33792 (four, 112) 103 and 58, 16 x 16384 x 65536
+// (eight, 256) 947 and 132; 16 x 9000 x 16416 (two, 141) 50 and 52, 16 x 7168 x 33760
+// (four, 112) 120 and 99.
+constexpr bool mx8_few_in_chunks(int n, int64_t chunks, bool whole, int cus) {
+  return chunks == 1 || chunks * mx_groups(n, 64) <= (whole ? cus - cus / 4 : cus + cus / 2);
+}
+
 // Grid of the tile kernel: `total` tiles, x * y workgroups (a grid dimension has
 // fewer than 2^32 threads).
 struct MxTileGrid {
