@@ -68,12 +68,13 @@ int mxfp8_unpack(const uint8_t* codes, const uint8_t* scale, int64_t R, int64_t 
  *   codes, scale the pair of mxfp8_quantize(y) with `saturate`: out, or both
  *                NULL where y is not
  *
- * v, the mean, y and its rounding to 8 bits are computed in fp64, so y's codes
- * are those of the exact y unless it lies within about 1e-15 of a border between
- * two codes, and neither sum's nor y's own rounding enters them. A row with a
- * non-finite v, or (eps == 0) of zeros, gives what that arithmetic gives: NaN,
- * or zeros beside an infinity, and scale bytes as mxfp8_quantize; so does a
- * block with elements beyond 2^136.
+ * v, the mean, y and its rounding to 8 bits are computed in fp64, so y's
+ * codes are those of the exact y unless it lies within about 1e-15 of a
+ * border between two codes, and neither sum's nor y's own rounding enters
+ * them. y is rounded once from that fp64 value, subnormal results of its
+ * type included. A row with a non-finite v, or (eps == 0) of zeros, gives
+ * what that arithmetic gives: NaN, or zeros beside an infinity, and scale
+ * bytes as mxfp8_quantize; so does a block with elements beyond 2^136.
  * sum may be x or residual itself (updated in place); else no output overlaps
  * an input or another output. Deterministic.
  * Sizes: as mxfp4_quantize, eps >= 0 (K3MOE_ERR_SHAPE). Unknown types:
@@ -114,17 +115,19 @@ int mxfp8_matmul(const uint8_t* a_codes, const uint8_t* a_scale, const uint8_t* 
  *   logits  f32 [T, E], bias f32 [E] or NULL for zero
  *   topk_ids i32 [T, k], topk_w f32 [T, k]: out, best first
  *
- * Gate g[t,e] = 1/(1+exp(-z)) (K3MOE_SCORE_SIGMOID) or exp(z) / sum_e' exp(z)
- * (K3MOE_SCORE_SOFTMAX), score s = g + b, evaluated in fp64. A group's score is
- * the sum of its group_top (1 or 2) best scores (of all, where it has fewer).
- * The topk_groups best groups are kept, and of their experts the k with the
- * highest scores are selected; the lower index goes first among equal scores,
- * of groups as of experts. A NaN score ranks below every number, as -inf. The
- * weight of a selected expert is its gate (the bias only steers selection),
- * divided by the sum over the k selected when `normalize` != 0 (0 where that
- * sum is 0), times `route_scale`, rounded once to f32. NaN logits leave the
- * softmax of the others as it is without them; where logits are +inf, they share it
- * equally; where all are -inf, every gate is 0.
+ * Gate g[t,e] = 1/(1+exp(-z)) (K3MOE_SCORE_SIGMOID) or exp(z) / sum_e'
+ * exp(z) (K3MOE_SCORE_SOFTMAX), score s = g + b, evaluated in fp64 (a
+ * softmax to about 2e-14 of itself: scores nearer than that, but of other
+ * logits and biases, may rank either way). A group's score is the sum of its
+ * group_top (1 or 2) best scores (of all, where it has fewer). The
+ * topk_groups best groups are kept, and of their experts the k with the
+ * highest scores are selected; the lower index goes first among equal
+ * scores, of groups as of experts. A NaN score ranks below every number, as
+ * -inf. The weight of a selected expert is its gate (the bias only steers
+ * selection), divided by the sum over the k selected when `normalize` != 0
+ * (0 where that sum is 0), times `route_scale`, rounded once to f32. NaN
+ * logits leave the softmax of the others as it is without them; where logits
+ * are +inf, they share it equally; where all are -inf, every gate is 0.
  * Sizes: 0 <= T <= 2^36 (T == 0 is a no-op), 1 <= E <= K3MOE_MAX_EXPERTS_FFN, groups
  * >= 1 divides E, 1 <= topk_groups <= groups, 1 <= k <= min(K3MOE_MAX_TOPK,
  * topk_groups * E / groups); K3MOE_ERR_SHAPE otherwise. Unknown score, or a
@@ -169,10 +172,11 @@ int moe_route_groups(const float* logits, const float* bias, int64_t T, int32_t 
  * is not accepted (of p, should that be 0 everywhere), or of p in row draft_len
  * where all are. Greedy: a proposal is accepted where it is the row's largest
  * logit's lowest index, which is also the next token; draft_probs do not enter.
- * Everything is computed in fp64 from the logits as given. NaN and -inf logits
- * have probability 0; where logits are +inf, they share the row equally; a row
- * with neither these nor a finite logit accepts nothing and gives the token -1.
- * A proposal outside [0, V) is not accepted. Deterministic.
+ * Everything is computed in fp64 from the logits as given (exponentials to
+ * 1.5e-14 of themselves). NaN and -inf logits have probability 0; where
+ * logits are +inf, they share the row equally; a row with neither these nor
+ * a finite logit accepts nothing and gives the token -1. A proposal outside
+ * [0, V) is not accepted. Deterministic.
  *   workspace  moe_verify_draft_workspace_size() bytes; contents on entry do
  *              not matter and are clobbered
  * Two launches. Sizes: S >= 0 (S == 0 is a no-op), 1 <= W <=

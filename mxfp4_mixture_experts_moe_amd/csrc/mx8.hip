@@ -112,9 +112,11 @@ unsigned copy_grid(int64_t units) {
 // A row stays in the registers of its threads between the sum and the rounding.
 //
 // Bound by the bytes where rows are many: 16384 x 7168 bf16 with residual and sum,
-// 826 MB, 178 us, 4.6 TB/s (fp64 throughout and rows read twice: 368 us), with
-// y 218, f32 278 and 367 (5.5 TB/s); one row of 7168 takes 4.6 to 5 us, the chain
-// of loads, sum over the workgroup, root, division and rounding.
+// 826 MB, 177 to 182 us, 4.5 to 4.7 TB/s (fp64 throughout and rows read twice: 368
+// us), with y, 1.06 GB, 217; f16 177 and, y in fp64, 240; f32 282 and 369 (5.4
+// TB/s).  (On a card that has been idle the first 25 ms are slower, 202 instead of
+// 177.)  One row of 7168 takes 4.4 to 5 us, the chain of loads, sum over the
+// workgroup, root, division and rounding.
 
 constexpr int64_t kMaxGroups = 1 << 20;  // workgroups of a launch (a grid dimension has fewer than 2^32 threads)
 

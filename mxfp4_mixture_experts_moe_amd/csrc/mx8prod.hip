@@ -89,9 +89,12 @@ __device__ __forceinline__ void store_out(void* out, int64_t i, float v) {
 // a group split K in pieces of 512, pieces asked for two turns ahead across
 // rounds, partial sums through LDS), with the rows of A, 8 bits an element, in
 // LDS.  Rows that do not fit together go in chunks, side by side in the grid.
-// Bound by the weight bytes: 8 x 33792 x 7168 takes 27 us, 4.8 TB/s of the 5.1 that
-// a copy reaches; of a small product (1 x 3584 x 7168: 6.4 us) by the chain of
-// launch, two turns of loads and the sum over the waves.
+// Bound by the weight bytes: 8 x 33792 x 7168 takes 31 us, 4.2 TB/s of the 5.1 that
+// a copy reaches (27 us where the caches still hold part of the weights from the call
+// before); of a small product (1 x 3584 x 7168: 6.2 to 7.3 us) by the chain of
+// launch, two turns of loads and the sum over the waves; of one with many rows of A
+// by their way into LDS, which every workgroup goes before its first product (16 x
+// 7168 x 7168 11 to 13 us, of which the weights' bytes are 5.4).
 constexpr int kFewWaves = 8;  // at most, per workgroup
 constexpr int kFewRows = 16;
 constexpr int kFewLds = 80 * 1024;     // two workgroups share a CU
@@ -297,8 +300,10 @@ __global__ __launch_bounds__(kFewWaves * 64, kLds > kFewLds ? 2 : 4) void mx8_fe
 // and the next stage, whose loads the wave has waited for, is there.
 //
 // Bound, where tiles fill the CUs, by the matrix instructions and the register
-// work of the split beside them: 4096 x 7168 x 7168 239 us, 1.76 PFLOP/s (3.5 of
-// products of 8 bits, each going in twice).  Where they do not, half of a stage is
+// work of the split beside them: 4096 x 7168 x 7168 239 to 266 us by session and data,
+// 1.6 to 1.76 PFLOP/s (twice that of products of 8 bits, each going in twice).  That
+// is a card at work: after idling its first 20 calls take 313, where a library
+// product of 8192^3 in bf16 takes 900 us and then 775.  Where they do not, half of a stage is
 // matrix instructions and the rest the way of its 16 or 24 KB into LDS, the barrier
 // and the reads behind it: 128 x 7168 x 7168 16.0 us.
 //   kStaged (K a multiple of 512): scales, 16 bytes (four steps) of every row, go
@@ -762,7 +767,9 @@ hipError_t launch_mx8_product(const uint8_t* a, const uint8_t* as, const uint8_t
   if (narrow <= cus) return launch_tiles<32, 64, 1, 2, 2, 4>(t, out_bf16, s);
   if (M <= 32) return launch_tiles<32, 64, 1, 2, 2, 2>(t, out_bf16, s);
   // Else the tile whose workgroups take the least time together, n of them on the CU
-  // with the most, in units of 17.7 us at K = 7168.  One tile of 64 with a CU to
+  // with the most, in units of 17.7 us at K = 7168 (of a short K more is a tile's fixed
+  // part, which the costs do not hold: 1536 x 7168 x 512 with f32 output takes 17.3 us in
+  // tiles of 256 x 192, in those of 128 15.8).  One tile of 64 with a CU to
   // itself takes 16 us (with four buffers, which leave no room for another); where
   // there are more of those, two buffers: 2 take 27 us, 3 39, 4 50, 9 115, 14 178;
   // one of 128 41 (2 69 to 82, 3 108, 4 141, 7 264).  One of 256 rows, one to a CU:

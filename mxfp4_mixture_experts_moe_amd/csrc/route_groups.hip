@@ -13,12 +13,17 @@
 // groups that come within the error of the k-th best lane's best, at most 64,
 // are scored in fp64 and ranked by counting.  Without a bias a softmax's experts
 // are compared by their logits, which fp32 holds exactly.
-// What fp32 is not sure of (heavy ties, values that are no numbers, masked rows:
-// about 30 us for such a token of 896) and larger sizes go the plain way: the
-// fp64 scores of a token lie in LDS ([E]) beside those of its groups
-// ([groups]); experts of the groups that are not kept are marked with NaN (NaN
-// scores themselves have become -inf by then), and top_of() takes the best, of
-// groups as of experts.
+// What fp32 is not sure of goes the plain way: heavy ties, values that are no
+// numbers, masked rows, and every token where the bias masks a group, whose score
+// then sets the error that is allowed for (896 experts, one of 16 groups masked: 8
+// tokens 30 us, 16384 158, with a softmax 185).  So do larger sizes (8 and 3584
+// tokens of 2048 experts 31 and 76 us, of 4096 48 and 225, with a softmax 65 and 313;
+// of 1024 by registers 6.6 and 12 to 16).  There the fp64 scores of a token lie in
+// LDS ([E]) beside those of its groups ([groups]); experts of the groups that are not
+// kept are marked with NaN (NaN scores themselves have become -inf by then), and
+// top_of() takes the best, of groups as of experts.
+// A softmax's sum is taken with the library's exponential there and for groups that
+// are near each other, and with the fitted one for experts: to 2e-14 the same.
 //
 // 16384 tokens of 896 take 38 us, bound by the vector instructions (the logits
 // are 59 MB, 12 us at 5.1 TB/s); 8 tokens 6.8 us, one wave's way through them.  A

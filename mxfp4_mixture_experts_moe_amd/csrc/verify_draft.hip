@@ -22,7 +22,7 @@
 //           sequence that the first launch clears; nothing waits.
 //
 // The first launch is bound by the logits' bytes beside the fp64 polynomials: 256
-// rows of 163840 f32 39 to 42 us, 4.3 TB/s (about 24 us of it are the polynomials alone);
+// rows of 163840 f32 38 to 42 us, 4.0 to 4.4 TB/s (about 24 us of it are the polynomials alone);
 // the second by a chain of loads, sums and barriers: 32 sequences 15 to 19 us, of
 // which 8 are the bytes of a row and its q; one sequence without q 7.
 #include "k3moe_internal.h"
